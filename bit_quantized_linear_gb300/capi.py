@@ -20,9 +20,12 @@ QLIN_OK, QLIN_ERR_INVALID_ARG, QLIN_ERR_UNSUPPORTED, QLIN_ERR_WORKSPACE, QLIN_ER
 QLIN_INT8, QLIN_E4M3 = 0, 1
 (QLIN_OP_QUANTIZE_WEIGHT, QLIN_OP_ACT_SCALE, QLIN_OP_QUANTIZE_ACT, QLIN_OP_W8A16_LINEAR,
  QLIN_OP_W8A8_LINEAR, QLIN_OP_I8_GEMM_S32, QLIN_OP_W8A8_DYNAMIC_LINEAR, QLIN_OP_KV_STORE_MIXED,
- QLIN_OP_KV_LOAD_MIXED, QLIN_OP_W8A16_GATE_UP_SILU, QLIN_OP_W8A8_GATE_UP_SILU) = range(11)
+ QLIN_OP_KV_LOAD_MIXED, QLIN_OP_W8A16_GATE_UP_SILU, QLIN_OP_W8A8_GATE_UP_SILU, QLIN_OP_RMSNORM,
+ QLIN_OP_RMSNORM_QUANT, QLIN_OP_W8A8_LINEAR_CODES, QLIN_OP_ROPE, QLIN_OP_ROPE_KV_STORE_MIXED) = range(16)
 
 QTYPES = {"int8": QLIN_INT8, "e4m3": QLIN_E4M3}
+ROPE_LAYOUTS = {"half": 0, "pairs": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 # Every symbol the header declares (checked by the not-gpu ABI test).
 EXPORTS = ["qlin_quantize_weight", "qlin_act_scale_from_calib", "qlin_quantize_act_static",
@@ -30,7 +33,10 @@ EXPORTS = ["qlin_quantize_weight", "qlin_act_scale_from_calib", "qlin_quantize_a
            "qlin_get_device_status", "qlin_status_string", "qlin_version", "qlin_debug_wait_flag",
            "qlin_kernel_name", "qlin_launch_count", "qlin_w8a8_linear_noalloc",
            "qlin_quantize_act_dynamic", "qlin_w8a8_dynamic_linear", "qlin_kv_store_mixed",
-           "qlin_kv_load_mixed", "qlin_w8a16_gate_up_silu", "qlin_w8a8_gate_up_silu"]
+           "qlin_kv_load_mixed", "qlin_w8a16_gate_up_silu", "qlin_w8a8_gate_up_silu",
+           "qlin_rmsnorm", "qlin_rmsnorm_quant", "qlin_w8a8_linear_codes", "qlin_rope_table", "qlin_rope",
+           "qlin_rope_kv_store_mixed", "qlin_attn_mixed", "qlin_attn_mixed_workspace_bytes",
+           "qlin_attn_mixed_kernel_name"]
 
 # Size of the library-owned scratch of qlin_w8a8_linear_noalloc (QLIN_W8A8_NOALLOC_SCRATCH_BYTES).
 W8A8_NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -47,6 +53,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"libqlin.so is not built ({LIB_PATH}); run __graft_entry__.build()")
     L = ctypes.CDLL(LIB_PATH)
     P, I64, I, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+    F, F64 = ctypes.c_float, ctypes.c_double
     sig = {
         "qlin_quantize_weight": [I, I64, I64, P, P, P, P],
         "qlin_act_scale_from_calib": [I, I64, I64, P, P, P, SZ, P],
@@ -68,6 +75,17 @@ def _load() -> ctypes.CDLL:
         "qlin_kv_load_mixed": [I64, I64, I64, P, I64, P, P, P, P, P, P, P],
         "qlin_w8a16_gate_up_silu": [I, I64, I64, I64, P, P, P, P, P, P, SZ, P],
         "qlin_w8a8_gate_up_silu": [I, I64, I64, I64, P, P, P, P, P, P, P, SZ, P],
+        "qlin_rmsnorm": [I64, I64, P, I64, P, I64, P, F, P, P, P],
+        "qlin_rmsnorm_quant": [I, I64, I64, P, I64, P, I64, P, F, P, P, P, P, P],
+        "qlin_w8a8_linear_codes": [I, I64, I64, I64, P, P, I, P, P, P, P, P, SZ, P],
+        "qlin_rope_table": [I64, I64, F64, I, F64, F64, F64, F64, F64, P, P],
+        "qlin_rope": [I, I64, I64, I64, I64, I64, P, I64, P, P, I64, P, I64, P, I64, P, I64, P],
+        "qlin_rope_kv_store_mixed": [I, I64, I64, I64, I64, I64, P, I64, P, P, I64, P, I64, P, I64, P, I64, P, I64,
+                                     P, P, P, P, P],
+        "qlin_attn_mixed": [I64, I64, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, I64, I64, P, P, P, P, F, I, I64,
+                            P, I64, P, SZ, P],
+        "qlin_attn_mixed_workspace_bytes": [I64] * 7,
+        "qlin_attn_mixed_kernel_name": [I64] * 7,
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -77,6 +95,8 @@ def _load() -> ctypes.CDLL:
     L.qlin_status_string.restype = ctypes.c_char_p
     L.qlin_kernel_name.restype = ctypes.c_char_p
     L.qlin_launch_count.restype = ctypes.c_uint64
+    L.qlin_attn_mixed_workspace_bytes.restype = SZ
+    L.qlin_attn_mixed_kernel_name.restype = ctypes.c_char_p
     return L
 
 
@@ -220,6 +240,97 @@ def qlin_kv_load_mixed(slots, k_cache, k_scale, v_cache, v_scale, k_out, v_out, 
                                    _p(k_out), _p(v_out), _stream(stream)), "qlin_kv_load_mixed")
 
 
+def _row_stride(t, least: int) -> int:
+    """Row stride (elements) of a 2-D tensor whose rows are contiguous."""
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError("rows must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), least)
+
+
+def qlin_rmsnorm(x, residual, weight, eps: float, h_out, y_out, stream=None):
+    """x, residual (or None) BF16 [M, K] rows; h_out (with a residual) and y_out BF16 [M, K]."""
+    M, K = x.shape
+    _check(_lib.qlin_rmsnorm(M, K, _p(x), _row_stride(x, K), _p(residual),
+                             0 if residual is None else _row_stride(residual, K), _p(weight), eps, _p(h_out),
+                             _p(y_out), _stream(stream)), "qlin_rmsnorm")
+
+
+def qlin_rmsnorm_quant(qtype, x, residual, weight, eps: float, input_scale, h_out, qx, x_scale, stream=None):
+    """As qlin_rmsnorm with 1-byte codes qx [M, K]: under input_scale [1] (x_scale None), or per-token
+    scales written to x_scale [M] (input_scale None)."""
+    M, K = x.shape
+    _check(_lib.qlin_rmsnorm_quant(_qt(qtype), M, K, _p(x), _row_stride(x, K), _p(residual),
+                                   0 if residual is None else _row_stride(residual, K), _p(weight), eps,
+                                   _p(input_scale), _p(h_out), _p(qx), _p(x_scale), _stream(stream)),
+           "qlin_rmsnorm_quant")
+
+
+def qlin_w8a8_linear_codes(qtype, qx, x_scale, qw, w_scale, bias, y, ws=None, stream=None):
+    """qx [M, K] codes; x_scale one value (per tensor) or [M] (per token, told apart by its size: a single
+    row's one scale is both)."""
+    M, K = qx.shape
+    N = qw.shape[0]
+    wp, wb = _ws(ws)
+    _check(_lib.qlin_w8a8_linear_codes(_qt(qtype), M, K, N, _p(qx), _p(x_scale), int(x_scale.numel() > 1), _p(qw),
+                                       _p(w_scale), _p(bias), _p(y), wp, wb, _stream(stream)),
+           "qlin_w8a8_linear_codes")
+
+
+def qlin_rope_table(table, theta: float, scaling="plain", factor: float = 1.0, original_context: float = 0.0,
+                    beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float = 1.0, stream=None):
+    """Fills table, fp32 [max_pos, rot]."""
+    max_pos, rot = table.shape
+    _check(_lib.qlin_rope_table(max_pos, rot, theta, ROPE_SCALINGS[scaling], factor, original_context, beta_fast,
+                                beta_slow, amplitude, _p(table), _stream(stream)), "qlin_rope_table")
+
+
+def qlin_rope(layout, Hq: int, Hk: int, D: int, rot: int, table, positions, q, k, q_out, k_out, stream=None):
+    """q [T, >= Hq*D] and k [T, >= Hk*D] BF16 rows (k and k_out None when Hk is 0); table of qlin_rope_table."""
+    if table.shape[1] != rot:
+        raise ValueError(f"the table turns {table.shape[1]} dimensions, not {rot}")
+    T = positions.shape[0]
+    n, m = Hq * D, Hk * D
+    _check(_lib.qlin_rope(ROPE_LAYOUTS[layout], T, Hq, Hk, D, rot, _p(table), table.shape[0], _p(positions), _p(q),
+                          _row_stride(q, n), _p(k), 0 if k is None else _row_stride(k, m), _p(q_out),
+                          _row_stride(q_out, n), _p(k_out), 0 if k_out is None else _row_stride(k_out, m),
+                          _stream(stream)), "qlin_rope")
+
+
+def qlin_rope_kv_store_mixed(layout, Hq: int, rot: int, table, positions, q, k, v, q_out, slots, k_cache, k_scale,
+                             v_cache, v_scale, stream=None):
+    """q turned into q_out; k (turned) and v quantized into their slots of the caches of kv_cache_alloc()."""
+    if table.shape[1] != rot:
+        raise ValueError(f"the table turns {table.shape[1]} dimensions, not {rot}")
+    S, H, D = k_cache.shape
+    n, m = Hq * D, H * D
+    _check(_lib.qlin_rope_kv_store_mixed(ROPE_LAYOUTS[layout], positions.shape[0], Hq, H, D, rot, _p(table),
+                                         table.shape[0], _p(positions), _p(q), _row_stride(q, n), _p(k),
+                                         _row_stride(k, m), _p(v), _row_stride(v, m), _p(q_out),
+                                         _row_stride(q_out, n), _p(slots), S, _p(k_cache), _p(k_scale), _p(v_cache),
+                                         _p(v_scale), _stream(stream)), "qlin_rope_kv_store_mixed")
+
+
+def qlin_attn_mixed(q, q_start, kv_len, block_table, block_size: int, k_cache, k_scale, v_cache, v_scale, max_q: int,
+                    max_kv: int, scale: float, causal: bool, window: int, out, ws=None, stream=None):
+    """q, out BF16 [T, Hq*D] rows; q_start int32 [B+1]; kv_len int32 [B]; block_table int32 [B, max_blocks]."""
+    S, H, D = k_cache.shape
+    T, B = q.shape[0], kv_len.shape[0]
+    n = q.shape[1]
+    wp, wb = _ws(ws)
+    _check(_lib.qlin_attn_mixed(B, T, n // D, H, D, _p(q), _row_stride(q, n), _p(q_start), max_q, _p(kv_len), max_kv,
+                                _p(block_table), block_table.shape[1], block_size, S, _p(k_cache), _p(k_scale),
+                                _p(v_cache), _p(v_scale), scale, int(causal), window, _p(out), _row_stride(out, n),
+                                wp, wb, _stream(stream)), "qlin_attn_mixed")
+
+
+def qlin_attn_mixed_workspace_bytes(B: int, Hq: int, H: int, D: int, max_q: int, max_kv: int, window: int = 0) -> int:
+    return int(_lib.qlin_attn_mixed_workspace_bytes(B, Hq, H, D, max_q, max_kv, window))
+
+
+def qlin_attn_mixed_kernel_name(B: int, Hq: int, H: int, D: int, max_q: int, max_kv: int, window: int = 0) -> str:
+    return _lib.qlin_attn_mixed_kernel_name(B, Hq, H, D, max_q, max_kv, window).decode()
+
+
 def qlin_kernel_name(op: int, qtype, M: int, K: int, N: int) -> str:
     return _lib.qlin_kernel_name(op, _qt(qtype), M, K, N).decode()
 
@@ -347,3 +458,52 @@ def w8a8_gate_up_silu(qtype, x, input_scale, qw, w_scale, bias=None):
     ws = workspace(QLIN_OP_W8A8_GATE_UP_SILU, qtype, M, K, I, device=x.device)
     qlin_w8a8_gate_up_silu(qtype, x, input_scale, qw, w_scale, bias, y, ws)
     return y
+
+
+def rmsnorm(x, weight, eps: float, residual=None):
+    """BF16 norm; returns (h, y) with h = x when there is no residual."""
+    h = None if residual is None else torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    qlin_rmsnorm(x, residual, weight, eps, h, y)
+    return (x if h is None else h), y
+
+
+def rmsnorm_quant(qtype, x, weight, eps: float, residual=None, input_scale=None):
+    """8-bit norm; returns (h, codes, scale): scale is input_scale, or the per-token scales made here."""
+    h = None if residual is None else torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    qx = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    s = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device) if input_scale is None else None
+    qlin_rmsnorm_quant(qtype, x, residual, weight, eps, input_scale, h, qx, s)
+    return (x if h is None else h), qx, (s if input_scale is None else input_scale)
+
+
+def w8a8_linear_codes(qtype, qx, x_scale, qw, w_scale, bias=None):
+    M, K = qx.shape
+    N = qw.shape[0]
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=qx.device)
+    ws = workspace(QLIN_OP_W8A8_LINEAR_CODES, qtype, M, K, N, device=qx.device)
+    qlin_w8a8_linear_codes(qtype, qx, x_scale, qw, w_scale, bias, y, ws)
+    return y
+
+
+def rope_table(max_pos: int, rot: int, theta: float = 10000.0, device=None, **scaling):
+    """The table qlin_rope reads, fp32 [max_pos, rot]; scaling as the arguments of qlin_rope_table."""
+    table = torch.empty((max_pos, rot), dtype=torch.float32, device=device or "cuda")
+    qlin_rope_table(table, theta, **scaling)
+    return table
+
+
+def attn_mixed(q, q_start, kv_len, block_table, block_size: int, cache, max_q: int, max_kv: int, scale=None,
+               causal: bool = True, window: int = 0, out=None, ws=None):
+    """Attention of q over a mixed cache (the four arrays of kv_cache_alloc()); scale defaults to D^-1/2."""
+    D = cache[0].shape[2]
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if ws is None:
+        n = qlin_attn_mixed_workspace_bytes(kv_len.shape[0], q.shape[1] // D, cache[0].shape[1], D, max_q, max_kv,
+                                            window)
+        if 0 < n < 2 ** 63:  # invalid sizes are the call's to report
+            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    qlin_attn_mixed(q, q_start, kv_len, block_table, block_size, *cache, max_q, max_kv,
+                    D ** -0.5 if scale is None else scale, causal, window, out, ws)
+    return out

@@ -1,0 +1,693 @@
+// Attention over the mixed 8-bit KV cache for few rows: decode, and short runs
+// of new tokens.  Bound by HBM: a (token, kv head) is 2D codes, D/16 bytes of key
+// scales and 2 of value scale, read once for all of the head's rows.
+//
+// Rows and positions.  The rows of a sequence that read one kv head (its new
+// tokens times the Hq/H query heads of the group) are tiled by 8*NT.  Each CTA
+// takes one row tile and one part of the positions; its four warps take 16
+// positions at a time, each with a ring of its own in shared memory that it
+// fills with 16-byte cp.async, so nothing but the end of the part makes warps
+// wait for one another.
+//
+// Arithmetic.  Scores and outputs are transposed, S^T = K q^T and O^T = V^T P^T,
+// so that positions (then head dimensions) fill the 16 rows of
+// mma.m16n8k16 and the 8 query heads its columns: with the usual orientation
+// the heads of one group would leave half of the 16 rows empty.  tcgen05 would
+// want 128 rows of one operand staged in shared memory as 16-bit values; here
+// codes go from the ring to registers once and the tensor pipe is far from its
+// limit.  Codes become float16 exactly (INT8 by a byte permute and a
+// subtraction, E4M3 by conversion); q is scaled by a power of two per row to
+// use float16's whole range; the products of one 32-dimension key group are
+// summed in fp32 and then scaled by the group's scale in fp32.  P is multiplied
+// by the value scales (and a power of two that keeps the product below 2^15)
+// in fp32 and rounded once to float16.  P^T as the second operand needs P's
+// fragments transposed: two movmatrix per 16 positions.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv_quant.cuh"
+#include "tc_ptx.cuh"
+
+namespace qlin {
+
+namespace {
+
+constexpr int kAttnWarps = 4;
+constexpr int kTile = 16;    // positions a warp handles at once
+constexpr float kLog2e = 1.44269504088896341f;
+
+struct SplitParams {
+  const uint16_t *q;
+  const int32_t *q_start, *kv_len, *block_table;
+  const uint8_t *kc, *vc;
+  const uint16_t *ks, *vs;
+  uint16_t *out;
+  float *part_o, *part_lse;
+  int64_t ldq, ldo, max_blocks, chunk;
+  int T, H, G, max_q, max_kv, block_size, block_shift, num_blocks, row_tiles, splits, causal, window;
+  float scale_log2;
+  unsigned *status;
+};
+
+// What a CTA (or a row of the join) knows of its sequence.  Counts that break
+// the contract are cut to what is in bounds; `broken` says so.
+struct Sequence {
+  int first, n, kept, kv;  // first row, new tokens, those within max_q, positions
+  bool broken;
+};
+__device__ __forceinline__ Sequence sequence(const SplitParams &p, int b) {
+  Sequence s;
+  const int end = p.q_start[b + 1];
+  s.first = p.q_start[b];
+  s.n = end - s.first;
+  s.kv = p.kv_len[b];
+  const int64_t room = p.max_blocks * p.block_size;
+  const bool rows_ok = s.first >= 0 && end >= s.first && end <= p.T;
+  s.broken = !rows_ok || s.n > p.max_q || s.kv < 0 || s.kv > p.max_kv || s.kv > room;
+  if (!rows_ok) s.n = 0;
+  s.kept = min(s.n, p.max_q);
+  s.kv = max(0, min(s.kv, p.max_kv));
+  if (s.kv > room) s.kv = (int)room;
+  return s;
+}
+// Positions [lo, hi) that the new token `tok` of a sequence sees.
+__device__ __forceinline__ void sees(const SplitParams &p, const Sequence &s, int tok, int &lo, int &hi) {
+  const int pos = s.kv - s.n + tok;
+  lo = 0;
+  hi = s.kv;
+  if (p.causal) hi = min(hi, pos + 1);
+  if (p.window > 0) {
+    lo = max(lo, pos - p.window + 1);
+    if (!p.causal) hi = (int)min((int64_t)hi, (int64_t)pos + p.window);
+  }
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 0 : 16) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^e as fp32, e in [-126, 127].
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Four INT8 codes -> two words of float16: with the sign bit flipped a code is
+// u = c + 128, and the bytes (u, 0x64) are the float16 1024 + u; minus 1152.
+__device__ __forceinline__ void int8x4_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t *>(&x);
+  hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+// Two E4M3 codes -> float16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_half(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+
+template <int D, int NT>
+struct Geometry {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kGroups = D / 32;
+  static constexpr int kChunks = D / 16;  // 16-byte pieces of a row of codes
+  static constexpr int kCodes = kTile * D;
+  static constexpr int kStages = D >= 256 ? 3 : 4;  // tiles in a warp's ring
+  // one stage: key codes, value codes, key scales, value scales, {valid, largest value scale}
+  static constexpr int kScaleAt = 2 * kCodes;
+  static constexpr int kVScaleAt = kScaleAt + kTile * kGroups * 4;
+  static constexpr int kInfoAt = kVScaleAt + kTile * 4;
+  static constexpr int kStageBytes = kInfoAt + 16;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kJoinFloats = kRows * D + 2 * kRows + 4;  // a warp's result: O, m, l, exponent
+  static constexpr int kWarpBytes = kRingBytes > kJoinFloats * 4 ? kRingBytes : kJoinFloats * 4;
+  static constexpr int kSmem = kAttnWarps * kWarpBytes;
+  static constexpr int kCtas = D >= 256 || NT > 1 ? 2 : 3;  // resident CTAs the registers are budgeted for
+};
+
+// Key rows are read 32 bytes (a group) at a time by four lanes, four rows of a
+// half-warp at once: groups are rotated by the row so that those four rows sit in
+// different banks.  Value rows are read D/8 bytes a lane, rows 2t by the lanes t:
+// their 16-byte pieces are exchanged by bits of the row.
+template <int D>
+__device__ __forceinline__ int key_chunk(int row, int c) {
+  if constexpr (D == 32) return c;
+  const int r = D == 64 ? row >> 1 : row;
+  return ((((c >> 1) + r) & (D / 32 - 1)) << 1) | (c & 1);
+}
+template <int D>
+__device__ __forceinline__ int value_chunk(int row, int c) {
+  if constexpr (D == 32) return c;
+  return D == 64 ? c ^ (row & 2) : c ^ (row & 6);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_attn_split(const SplitParams p) {
+  using Geo = Geometry<D, NT>;
+  constexpr int kGroups = Geo::kGroups, kRows = Geo::kRows, kStages = Geo::kStages;
+  constexpr int kDims = D / 8;  // dimensions of a value row a lane holds
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t *ring = smem + warp * Geo::kWarpBytes;
+  const uint32_t ring_at = tc::smem_u32(ring);
+
+  const int64_t cta = blockIdx.x;
+  const int split = (int)(cta % p.splits);
+  const int64_t unit = cta / p.splits;
+  const int tile = (int)(unit % p.row_tiles);
+  const int h = (int)(unit / p.row_tiles % p.H), b = (int)(unit / p.row_tiles / p.H);
+  pdl_wait();
+  pdl_trigger();
+  const Sequence sq = sequence(p, b);
+  if (sq.broken && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
+  const int R = sq.kept * p.G, r0 = tile * kRows;
+  if (r0 >= R) return;
+
+  // positions of this CTA: what any of its rows sees, cut into parts
+  const int last = min(r0 + kRows, R) - 1;
+  int lo, hi, beg, end;
+  {
+    int unused;
+    sees(p, sq, r0 / p.G, lo, unused);
+    sees(p, sq, last / p.G, unused, hi);
+    const int64_t from = (int64_t)(lo & ~(kTile - 1)) + (int64_t)split * p.chunk;
+    beg = (int)min(from, (int64_t)max(hi, 0));
+    end = split == p.splits - 1 ? max(hi, beg) : (int)min(from + p.chunk, (int64_t)max(hi, beg));
+  }
+
+  // q: row 8*nt + g, as the second operand; its largest magnitude becomes 2^14..2^15
+  uint32_t qf[NT][kGroups][4];
+  float cf[NT][2];               // score factors of columns 2t and 2t + 1
+  int vlo[NT][2], vhi[NT][2];    // positions those columns see
+  int all_lo = lo, all_hi = hi;  // positions every row sees
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = r0 + nt * 8 + g;
+    uint4 w[kGroups];
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      w[k] = make_uint4(0, 0, 0, 0);
+      if (r < R) {
+        const uint16_t *row =
+            p.q + (int64_t)(sq.first + r / p.G) * p.ldq + (int64_t)(h * p.G + r % p.G) * D + k * 32 + t * 8;
+        w[k] = *reinterpret_cast<const uint4 *>(row);
+      }
+      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+    }
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+    int e = (int)(__float_as_uint(top) >> 23) - 127;
+    e = top > 0.0f && e < 128 ? max(e, -100) : 14;
+    const float up = pow2i(14 - e), factor = p.scale_log2 * pow2i(max(e - 14, -126));
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        qf[nt][k][j] = half2_bits(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      cf[nt][c] = __shfl_sync(~0u, factor, (2 * t + c) * 4);
+      const int rc = r0 + nt * 8 + 2 * t + c;
+      vlo[nt][c] = lo, vhi[nt][c] = hi;  // columns without a row see everything (their q is 0)
+      if (rc < R) sees(p, sq, rc / p.G, vlo[nt][c], vhi[nt][c]);
+      all_lo = max(all_lo, vlo[nt][c]);
+      all_hi = min(all_hi, vhi[nt][c]);
+    }
+  }
+  all_lo = __reduce_max_sync(~0u, all_lo);
+  all_hi = __reduce_min_sync(~0u, all_hi);
+
+  float m[NT][2], l[NT][2], O[NT][kDims / 2][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kDims / 2; ++i) O[nt][i][0] = O[nt][i][1] = O[nt][i][2] = O[nt][i][3] = 0.0f;
+  }
+  int vexp = -1000;  // O is sum p v 2^-vexp
+
+  // ---- the ring: tile n covers positions beg + (n * warps + warp) * 16 ...
+  const int tiles = (end - beg + kTile - 1) / kTile;
+  const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
+  const int row16 = lane & 15;
+  const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
+  const auto position = [&](int n) { return beg + (n * kAttnWarps + warp) * kTile + row16; };
+  const auto block_of = [&](int j) { return p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size; };
+  const auto page = [&](int n) {  // page of the lane's position of tile n (-1: none)
+    const int j = position(n);
+    return n < mine && j >= lo && j < end ? __ldg(table + block_of(j)) : -1;
+  };
+  uint32_t sc[(kGroups + 1) / 2];  // the lane's scales of the tile issued last
+  uint32_t sv = 0;
+  bool sok = false;
+  int next_page = page(0);
+  const auto issue = [&](int n) {
+    const int j = position(n), blk = next_page;
+    const bool wanted = n < mine && j >= lo && j < end;
+    sok = wanted && blk >= 0 && blk < p.num_blocks;
+    if (wanted && !sok && lane < 16) set_status(p.status, QLIN_ERR_INVALID_ARG);
+    const int64_t slot = sok ? (int64_t)blk * p.block_size + (j - block_of(j) * p.block_size) : 0;
+    const int64_t base = slot * p.H + h;
+    next_page = page(n + 1);
+    if (n < mine) {
+      const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
+      const unsigned ok = __ballot_sync(~0u, sok);
+#pragma unroll
+      for (int i = 0; i < Geo::kChunks / 2; ++i) {
+        const int piece = i * 32 + lane, r = piece / Geo::kChunks, c = piece % Geo::kChunks;
+        const int64_t off = __shfl_sync(~0u, base, r) * D + c * 16;
+        const bool fill = !((ok >> r) & 1);
+        cp_async16(at + r * D + key_chunk<D>(r, c) * 16, p.kc + off, fill);
+        cp_async16(at + Geo::kCodes + r * D + value_chunk<D>(r, c) * 16, p.vc + off, fill);
+      }
+      sv = 0;
+#pragma unroll
+      for (int k = 0; k < (kGroups + 1) / 2; ++k) sc[k] = 0;
+      if (sok && lane < 16) {
+        sv = __ldg(p.vs + base);
+        if constexpr (kGroups == 1) {
+          sc[0] = __ldg(p.ks + base);
+        } else {
+          load_words<kGroups / 2>(p.ks + base * kGroups, sc);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  // the scales of the tile issued last, as fp32, into its stage
+  const auto put_scales = [&](int n) {
+    if (n >= mine) return;
+    uint8_t *at = ring + (n % kStages) * Geo::kStageBytes;
+    const float v = half_bits_to_f32((uint16_t)sv);
+    const unsigned ok = __ballot_sync(~0u, sok);
+    const unsigned top = __reduce_max_sync(~0u, min(__float_as_uint(fabsf(v)), 0x7F7FFFFFu));
+    if (lane < 16) {
+      float *k = reinterpret_cast<float *>(at + Geo::kScaleAt) + lane * kGroups;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) k[i] = half_bits_to_f32((uint16_t)(sc[i / 2] >> (16 * (i & 1))));
+      reinterpret_cast<float *>(at + Geo::kVScaleAt)[lane] = v;
+    }
+    if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(ok & 0xFFFFu, top);
+  };
+
+  for (int n = 0; n < kStages - 1; ++n) {
+    issue(n);
+    if (n < kStages - 2) put_scales(n);
+  }
+  for (int n = 0; n < mine; ++n) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    put_scales(n + kStages - 2);
+    issue(n + kStages - 1);
+    const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
+    uint8_t *stage = ring + (n % kStages) * Geo::kStageBytes;
+    const uint2 info = *reinterpret_cast<const uint2 *>(stage + Geo::kInfoAt);
+    const int j0 = beg + (n * kAttnWarps + warp) * kTile;
+    const bool full = info.x == 0xFFFFu && j0 >= all_lo && j0 + kTile <= all_hi;
+    float vs0 = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[g];
+    float vs1 = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[g + 8];
+
+    // scores of positions g, g + 8 and columns 2t, 2t + 1
+    float S[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      uint32_t w0[2], w1[2];
+      const uint32_t a0 = at + g * D + key_chunk<D>(g, 2 * k) * 16 + t * 8;
+      const uint32_t a1 = at + (g + 8) * D + key_chunk<D>(g + 8, 2 * k) * 16 + t * 8;
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(a0));
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(a1));
+      float acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t a[4];
+        int8x4_to_half(w0[j], a[0], a[2]);
+        int8x4_to_half(w1[j], a[1], a[3]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a, qf[nt][k][2 * j], qf[nt][k][2 * j + 1]);
+      }
+      const float k0 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[g * kGroups + k];
+      const float k1 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[(g + 8) * kGroups + k];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        S[nt][0] = fmaf(acc[nt][0], k0, S[nt][0]);
+        S[nt][1] = fmaf(acc[nt][1], k0, S[nt][1]);
+        S[nt][2] = fmaf(acc[nt][2], k1, S[nt][2]);
+        S[nt][3] = fmaf(acc[nt][3], k1, S[nt][3]);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      S[nt][0] *= cf[nt][0], S[nt][2] *= cf[nt][0];
+      S[nt][1] *= cf[nt][1], S[nt][3] *= cf[nt][1];
+    }
+    if (!full) {
+      const bool ok0 = (info.x >> g) & 1, ok1 = (info.x >> (g + 8)) & 1;
+      const int p0 = j0 + g, p1 = p0 + 8;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (!ok0 || p0 < vlo[nt][c] || p0 >= vhi[nt][c]) S[nt][c] = -INFINITY;
+          if (!ok1 || p1 < vlo[nt][c] || p1 >= vhi[nt][c]) S[nt][2 + c] = -INFINITY;
+        }
+      // A NaN value code times P = 0 would reach rows that do not see it: such
+      // codes become 0 and their position's scale NaN.  (Two lanes to a row.)
+      unsigned bad = 0;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(stage + Geo::kCodes + (lane >> 1) * D + (lane & 1) * (D / 2)) + i;
+        const uint32_t nan = __vcmpeq4(*w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (nan) *w &= ~nan;
+        bad |= nan;
+      }
+      const unsigned rows = __ballot_sync(~0u, bad != 0);
+      if ((rows >> (2 * g)) & 3) vs0 = NAN;
+      if ((rows >> (2 * g + 16)) & 3) vs1 = NAN;
+      __syncwarp();
+    }
+
+    // value scales relative to 2^vexp; the exponent grows when P would pass 2^15
+    int e = (int)(info.y >> 23) - 127;
+    e = min(max(e, -24), 16);
+    if (e - vexp > 13) {
+      const float down = exp2_approx((float)(vexp - (e - 7)));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < kDims / 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) O[nt][i][c] *= down;
+      vexp = e - 7;
+    }
+    vs0 *= pow2i(-vexp);
+    vs1 *= pow2i(-vexp);
+
+    // online softmax per column
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mx[2] = {fmaxf(S[nt][0], S[nt][2]), fmaxf(S[nt][1], S[nt][3])};
+#pragma unroll
+      for (int o = 4; o < 32; o *= 2) {
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(~0u, mx[0], o));
+        mx[1] = fmaxf(mx[1], __shfl_xor_sync(~0u, mx[1], o));
+      }
+      const bool grew = mx[0] > m[nt][0] || mx[1] > m[nt][1];
+      if (__any_sync(~0u, grew)) {
+        float a[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float now = fmaxf(m[nt][c], mx[c]);
+          a[c] = exp2_approx(m[nt][c] - (now == -INFINITY ? 0.0f : now));
+          m[nt][c] = now;
+          l[nt][c] *= a[c];
+        }
+#pragma unroll
+        for (int i = 0; i < kDims / 2; ++i) {
+          O[nt][i][0] *= a[0], O[nt][i][2] *= a[0];
+          O[nt][i][1] *= a[1], O[nt][i][3] *= a[1];
+        }
+      }
+      const float z0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], z1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+      const float p00 = exp2_approx(S[nt][0] - z0), p01 = exp2_approx(S[nt][1] - z1);
+      const float p10 = exp2_approx(S[nt][2] - z0), p11 = exp2_approx(S[nt][3] - z1);
+      l[nt][0] += p00 + p10;
+      l[nt][1] += p01 + p11;
+      float w00 = p00 * vs0, w01 = p01 * vs0, w10 = p10 * vs1, w11 = p11 * vs1;
+      if (!full) {  // an unseen position adds nothing, whatever its scale
+        if (S[nt][0] == -INFINITY) w00 = 0.0f;
+        if (S[nt][1] == -INFINITY) w01 = 0.0f;
+        if (S[nt][2] == -INFINITY) w10 = 0.0f;
+        if (S[nt][3] == -INFINITY) w11 = 0.0f;
+      }
+      pf[nt][0] = transpose8x8(half2_bits(w00, w01));
+      pf[nt][1] = transpose8x8(half2_bits(w10, w11));
+    }
+
+    // O^T += V^T P^T: positions 2t, 2t+1 (and +8), dimensions g*D/8 ...
+    constexpr int kW = kDims / 4;  // words of a lane's piece of a value row
+    uint32_t v[4][kW];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+      const uint8_t *row = stage + Geo::kCodes + r * D;
+      if constexpr (kDims >= 16) {
+#pragma unroll
+        for (int c = 0; c < kDims / 16; ++c) {
+          const uint4 x =
+              *reinterpret_cast<const uint4 *>(row + value_chunk<D>(r, g * (kDims / 16) + c) * 16);
+          v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
+        }
+      } else if constexpr (kDims == 8) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(row + value_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
+        v[i][0] = x.x, v[i][1] = x.y;
+      } else {
+        v[i][0] = *reinterpret_cast<const uint32_t *>(row + g * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      // (position 2t, 2t+1) byte pairs of dimensions 4i, 4i+1 | 4i+2, 4i+3
+      const uint32_t x0 = __byte_perm(v[0][i], v[1][i], 0x5140), x1 = __byte_perm(v[0][i], v[1][i], 0x7362);
+      const uint32_t y0 = __byte_perm(v[2][i], v[3][i], 0x5140), y1 = __byte_perm(v[2][i], v[3][i], 0x7362);
+      const uint32_t a0[4] = {e4m3x2_to_half((uint16_t)x0), e4m3x2_to_half((uint16_t)(x0 >> 16)),
+                              e4m3x2_to_half((uint16_t)y0), e4m3x2_to_half((uint16_t)(y0 >> 16))};
+      const uint32_t a1[4] = {e4m3x2_to_half((uint16_t)x1), e4m3x2_to_half((uint16_t)(x1 >> 16)),
+                              e4m3x2_to_half((uint16_t)y1), e4m3x2_to_half((uint16_t)(y1 >> 16))};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16(O[nt][2 * i], a0, pf[nt][0], pf[nt][1]);
+        mma_f16(O[nt][2 * i + 1], a1, pf[nt][0], pf[nt][1]);
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // ---- join the warps
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int o = 4; o < 32; o *= 2) {
+      l[nt][0] += __shfl_xor_sync(~0u, l[nt][0], o);
+      l[nt][1] += __shfl_xor_sync(~0u, l[nt][1], o);
+    }
+  __syncwarp();
+  float *res = reinterpret_cast<float *>(ring);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int r = nt * 8 + 2 * t + c;
+#pragma unroll
+      for (int i = 0; i < kDims / 2; ++i)
+        *reinterpret_cast<float2 *>(res + r * D + g * kDims + 2 * i) = make_float2(O[nt][i][c], O[nt][i][2 + c]);
+      if (g == 0) {
+        res[kRows * D + r] = m[nt][c];
+        res[kRows * D + kRows + r] = l[nt][c];
+      }
+    }
+  if (lane == 0) res[kRows * D + 2 * kRows] = mine ? pow2i(vexp) : 0.0f;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * D / 4; i += 32 * kAttnWarps) {
+    const int r = i / (D / 4), d = i % (D / 4) * 4;
+    if (r0 + r >= R) break;
+    const float *w = reinterpret_cast<const float *>(smem);
+    constexpr int kStep = Geo::kWarpBytes / 4;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kAttnWarps; ++k) top = fmaxf(top, w[k * kStep + kRows * D + r]);
+    const float z = top == -INFINITY ? 0.0f : top;
+    float L = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kAttnWarps; ++k) {
+      const float *x = w + k * kStep;
+      const float f = exp2_approx(x[kRows * D + r] - z);
+      L = fmaf(f, x[kRows * D + kRows + r], L);
+      const float fo = f * x[kRows * D + 2 * kRows];
+      const float4 y = *reinterpret_cast<const float4 *>(x + r * D + d);
+      o.x = fmaf(fo, y.x, o.x), o.y = fmaf(fo, y.y, o.y), o.z = fmaf(fo, y.z, o.z), o.w = fmaf(fo, y.w, o.w);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    if (p.splits == 1) {
+      const int rr = r0 + r;
+      uint16_t *dst = p.out + (int64_t)(sq.first + rr / p.G) * p.ldo + (int64_t)(h * p.G + rr % p.G) * D + d;
+      *reinterpret_cast<uint2 *>(dst) =
+          make_uint2((uint32_t)f32_to_bf16_bits(o.x) | ((uint32_t)f32_to_bf16_bits(o.y) << 16),
+                     (uint32_t)f32_to_bf16_bits(o.z) | ((uint32_t)f32_to_bf16_bits(o.w) << 16));
+    } else {
+      const int64_t at = cta * kRows + r;
+      *reinterpret_cast<float4 *>(p.part_o + at * D + d) = o;
+      if (d == 0) p.part_lse[at] = L == 0.0f ? -INFINITY : top + log2f(L);
+    }
+  }
+}
+
+// Joins the parts of one row: out = sum_s w_s o_s / sum_s w_s with
+// w_s = 2^(lse_s - max lse).  A CTA per row, its warps over the parts.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams p, int rows) {
+  constexpr int V = D / 32;  // floats of a lane
+  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float s_w[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t unit = blockIdx.x / rows;
+  const int r = blockIdx.x % rows;
+  const int tile = (int)(unit % p.row_tiles);
+  const int h = (int)(unit / p.row_tiles % p.H), b = (int)(unit / p.row_tiles / p.H);
+  pdl_wait();
+  pdl_trigger();
+  const Sequence sq = sequence(p, b);
+  const int rr = tile * rows + r;
+  if (rr >= sq.kept * p.G) return;
+  const float *lse = p.part_lse + unit * p.splits * rows + r;
+  float top = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, lse[(int64_t)s * rows]);
+  top = warp_max(top);
+  const float z = top == -INFINITY ? 0.0f : top;
+  float o[V], W = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.0f;
+#pragma unroll 4
+  for (int s = warp; s < p.splits; s += kJoinWarps) {
+    const float w = exp2_approx(lse[(int64_t)s * rows] - z);
+    const float *src = p.part_o + ((unit * p.splits + s) * rows + r) * D + lane * V;
+    W += w;
+    uint32_t x[V];
+    load_words<V>(src, x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = fmaf(w, __uint_as_float(x[i]), o[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
+  if (lane == 0) s_w[warp] = W;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    const int d = 2 * threadIdx.x;
+    float a = 0.0f, c = 0.0f, w = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) {
+      a += s_o[k][d];
+      c += s_o[k][d + 1];
+      w += s_w[k];
+    }
+    const float inv = w == 0.0f ? 0.0f : 1.0f / w;
+    uint16_t *dst = p.out + (int64_t)(sq.first + rr / p.G) * p.ldo + (int64_t)(h * p.G + rr % p.G) * D + d;
+    *reinterpret_cast<uint32_t *>(dst) =
+        (uint32_t)f32_to_bf16_bits(a * inv) | ((uint32_t)f32_to_bf16_bits(c * inv) << 16);
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_nt(const SplitParams &p, int64_t units, cudaStream_t st) {
+  using Geo = Geometry<D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(k_attn_split<D, NT>, dim3((unsigned)(units * p.splits)), dim3(32 * kAttnWarps), Geo::kSmem, st, 1,
+                    p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  return launch_kernel(k_attn_join<D>, dim3((unsigned)(units * Geo::kRows)), dim3(32 * kJoinWarps), 0, st, 1, p,
+                       (int)Geo::kRows);
+}
+template <int D>
+cudaError_t launch_d(const SplitParams &p, int rows, int64_t units, cudaStream_t st) {
+  return rows == 8 ? launch_nt<D, 1>(p, units, st) : launch_nt<D, 2>(p, units, st);
+}
+
+}  // namespace
+
+// Rows are tiled by 8 where one tile holds them, else by 16 (each code is then
+// converted for twice the rows).  Positions are split until one wave of CTAs
+// fills the GPU, but not below 128 positions a part; where there are more units
+// than that, into parts of at least 1024 so that ragged sequences even out.
+AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
+                              int64_t window, int sms) {
+  AttnSplitPlan plan{};
+  const int64_t G = Hq / H, R = max_q * G;
+  plan.rows = R <= 8 ? 8 : 16;
+  plan.row_tiles = (int)((R + plan.rows - 1) / plan.rows);
+  int64_t range = max_kv;
+  if (window > 0 && window < max_kv) range = std::min(range, window + plan.rows / G + 1);
+  range += kTile - 1;  // the first part begins at a multiple of 16; the last one takes what is left
+  const int64_t units = B * H * plan.row_tiles, slots = (int64_t)sms * (plan.rows == 8 ? 3 : 2);
+  const int64_t fill = std::min((slots + units - 1) / units, (range + 127) / 128);
+  const int64_t even = std::min((4 * slots + units - 1) / units, range / 1024);
+  const int64_t want = std::max<int64_t>(1, std::max(fill, even));
+  constexpr int64_t step = kTile * kAttnWarps;
+  plan.chunk = std::max(step, (range + want * step - 1) / (want * step) * step);
+  plan.splits = (int)std::max<int64_t>(1, (range + plan.chunk - 1) / plan.chunk);
+  plan.ws_bytes = plan.splits > 1 ? (size_t)(units * plan.splits * plan.rows * (D + 1) * 4) : 0;
+  plan.ws_bytes = round_up(plan.ws_bytes, 256);
+  return plan;
+}
+
+cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, void *ws, unsigned *status,
+                              cudaStream_t st) {
+  SplitParams p{};
+  p.q = (const uint16_t *)a.q, p.q_start = a.q_start, p.kv_len = a.kv_len, p.block_table = a.block_table;
+  p.kc = (const uint8_t *)a.k_cache, p.vc = (const uint8_t *)a.v_cache;
+  p.ks = (const uint16_t *)a.k_scale, p.vs = (const uint16_t *)a.v_scale;
+  p.out = (uint16_t *)a.out, p.ldq = a.ldq, p.ldo = a.ldo, p.max_blocks = a.max_blocks;
+  p.T = (int)a.T, p.H = (int)a.H, p.G = (int)(a.Hq / a.H), p.max_q = (int)a.max_q, p.max_kv = (int)a.max_kv;
+  p.block_size = (int)a.block_size;
+  p.block_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (a.block_size == (int64_t)1 << s) p.block_shift = s;
+  p.num_blocks = (int)(a.num_slots / a.block_size);
+  p.row_tiles = plan.row_tiles, p.splits = plan.splits, p.chunk = plan.chunk;
+  p.causal = a.causal != 0, p.window = (int)std::min<int64_t>(a.window, 1 << 30);
+  p.scale_log2 = a.scale * kLog2e;
+  p.status = status;
+  const int64_t units = a.B * a.H * plan.row_tiles;
+  p.part_o = (float *)ws;
+  p.part_lse = p.part_o ? p.part_o + units * plan.splits * plan.rows * a.D : nullptr;
+  switch (a.D) {
+    case 32: return launch_d<32>(p, plan.rows, units, st);
+    case 64: return launch_d<64>(p, plan.rows, units, st);
+    case 128: return launch_d<128>(p, plan.rows, units, st);
+    case 256: return launch_d<256>(p, plan.rows, units, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace qlin

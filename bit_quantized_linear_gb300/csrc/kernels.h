@@ -26,6 +26,20 @@ qlin_status w8a8_check_args(int qtype, int64_t M, int64_t K, int64_t N, const vo
                             const void *qw, const float *w_scale, const void *bias, const void *y);
 qlin_status device_ready();
 
+// The current device's cached facts; QLIN_OK or the status to return.
+qlin_status current_device(DeviceInfo **out);
+// Its SM count for choices made without a launch (152, a GB300's, before the first call).
+int sm_count();
+
+// Small checks shared by the entry points.
+inline bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+inline bool valid_qtype(int t) { return t == QLIN_INT8 || t == QLIN_E4M3; }
+inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+inline qlin_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLIN_OK : QLIN_ERR_CUDA; }
+qlin_status check_linear_shape(int64_t M, int64_t K, int64_t N);
+qlin_status check_kv(int64_t T, int64_t H, int64_t D, const int64_t *slots, int64_t num_slots, const void *k_cache,
+                     const void *k_scale, const void *v_cache, const void *v_scale);
+
 // Launches `kernel` on `st` with programmatic stream serialization (the kernel
 // calls pdl_wait() before reading global inputs) and an optional cluster
 // shape along z.
@@ -200,6 +214,74 @@ struct KvArgs {
 };
 cudaError_t launch_kv_store(const KvArgs &a, unsigned *status, int sms, cudaStream_t st);
 cudaError_t launch_kv_load(const KvArgs &a, unsigned *status, cudaStream_t st);
+
+// RMSNorm with the residual's addition (norm_kernels.cu).  Strides in elements;
+// residual and h_out may be null, x_scale is null for a static scale.
+constexpr int64_t kNormMaxK = 32768;  // a row stays in the registers of at most 16 warps
+enum NormOut { kNormBf16 = 0, kNormInt8 = 1, kNormE4m3 = 2 };
+struct NormArgs {
+  int64_t M, K;
+  int out;                   // NormOut
+  const void *x, *residual;  // BF16 [M, K]
+  int64_t ldx, ldr;
+  const void *weight;        // BF16 [K]
+  float eps;
+  const float *input_scale;  // static scale (device scalar) or null: per-token scales
+  void *h_out;               // BF16 [M, K], the sum
+  void *y;                   // BF16 [M, K] or codes
+  float *x_scale;            // [M]
+};
+cudaError_t launch_rmsnorm(const NormArgs &a, int sms, cudaStream_t st);
+
+// Rotary positions (rope_kernels.cu), alone or with the store into the mixed
+// KV cache (kv.k, kv.v, kv.slots and the caches; kv.T and kv.D as here).
+struct RopeArgs {
+  int layout;  // qlin_rope_layout
+  int64_t T, Hq, Hk, D, rot;
+  const float *table;  // [max_pos, rot]: rot/2 cosines, then rot/2 sines
+  int64_t max_pos;
+  const int64_t *positions;  // [T]; negative = padding
+  const void *q, *k;         // BF16 rows of Hq*D / Hk*D elements
+  int64_t ldq, ldk;
+  void *q_out, *k_out;
+  int64_t ldqo, ldko;
+};
+cudaError_t launch_rope_table(int64_t max_pos, int64_t rot, double theta, int scaling, double factor,
+                              double original_context, double beta_fast, double beta_slow, double amplitude,
+                              float *table, cudaStream_t st);
+cudaError_t launch_rope(const RopeArgs &r, unsigned *status, int sms, cudaStream_t st);
+cudaError_t launch_rope_kv_store(const RopeArgs &r, const KvArgs &kv, unsigned *status, int sms, cudaStream_t st);
+
+// Attention over the mixed KV cache (attn_split.cu: rows in small tiles, the
+// positions split over CTAs).
+struct AttnArgs {
+  int64_t B, T, Hq, H, D;
+  const void *q;
+  int64_t ldq;
+  const int32_t *q_start;
+  int64_t max_q;
+  const int32_t *kv_len;
+  int64_t max_kv;
+  const int32_t *block_table;
+  int64_t max_blocks, block_size, num_slots;
+  const void *k_cache, *k_scale, *v_cache, *v_scale;
+  float scale;
+  int causal;
+  int64_t window;
+  void *out;
+  int64_t ldo;
+};
+struct AttnSplitPlan {
+  int row_tiles;   // row tiles of a (sequence, kv head)
+  int rows;        // rows of a tile: 8 or 16
+  int splits;      // parts of the positions, each a CTA
+  int64_t chunk;   // positions of a part (a multiple of 16)
+  size_t ws_bytes;
+};
+AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
+                              int64_t window, int sms);
+cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, void *ws, unsigned *status,
+                              cudaStream_t st);
 
 // tcgen05 kernels (gemm_tc.cu)
 cudaError_t launch_fp8_gemm(const GemmArgs &g, const DeviceInfo &dev, cudaStream_t st);

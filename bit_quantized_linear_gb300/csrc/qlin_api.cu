@@ -20,7 +20,7 @@ static std::mutex g_dev_mu;
 
 // SM count of the current device for host-side tile choices that name a
 // kernel without launching it: the cached value, else 152 (GB300).
-static int sm_count() {
+int sm_count() {
   int d = -1;
   if (cudaGetDevice(&d) == cudaSuccess && d >= 0 && d < kMaxDevices) {
     std::lock_guard<std::mutex> lk(g_dev_mu);
@@ -31,7 +31,7 @@ static int sm_count() {
 
 // Caches the SM count, compute capability and status-word address of the
 // current device.  Returns QLIN_OK or an error status.
-static qlin_status current_device(DeviceInfo **out) {
+qlin_status current_device(DeviceInfo **out) {
   int d = -1;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return QLIN_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lk(g_dev_mu);
@@ -72,13 +72,8 @@ cudaError_t launch_debug_wait(const uint32_t *flag, uint64_t timeout_ns, unsigne
   return launch_kernel(k_debug_wait, dim3(1), dim3(1), 0, st, 1, (const volatile uint32_t *)flag, timeout_ns, status);
 }
 
-static inline bool al16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-static inline bool valid_qtype(int t) { return t == QLIN_INT8 || t == QLIN_E4M3; }
-static inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-static inline qlin_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QLIN_OK : QLIN_ERR_CUDA; }
-
 // Common shape checks of the linear entry points.
-static qlin_status check_linear_shape(int64_t M, int64_t K, int64_t N) {
+qlin_status check_linear_shape(int64_t M, int64_t K, int64_t N) {
   if (M < 0 || K < 16 || N < 16 || (K % 16) || (N % 16)) return QLIN_ERR_INVALID_ARG;
   if (M > (int64_t)1 << 31 || K > (int64_t)1 << 17 || N > (int64_t)1 << 31) return QLIN_ERR_INVALID_ARG;
   return QLIN_OK;
@@ -107,6 +102,20 @@ qlin_status w8a8_check_args(int qtype, int64_t M, int64_t K, int64_t N, const vo
       ((uintptr_t)input_scale & 3u))
     return QLIN_ERR_INVALID_ARG;
   if (M > 0 && (!x || !y || !al16(x) || !al16(y))) return QLIN_ERR_INVALID_ARG;
+  return QLIN_OK;
+}
+
+// Shape and pointer checks shared by the entry points that write or read the
+// mixed KV cache through a slot per token.
+qlin_status check_kv(int64_t T, int64_t H, int64_t D, const int64_t *slots, int64_t num_slots, const void *k_cache,
+                     const void *k_scale, const void *v_cache, const void *v_scale) {
+  if (T < 0 || H < 1 || num_slots < 0) return QLIN_ERR_INVALID_ARG;
+  if (!(D == 32 || D == 64 || D == 128 || D == 256)) return QLIN_ERR_INVALID_ARG;
+  if (H > 4096 || T > ((int64_t)1 << 40) / H || num_slots > ((int64_t)1 << 40) / H) return QLIN_ERR_INVALID_ARG;
+  if (T == 0) return QLIN_OK;
+  if (!slots || !al16(slots)) return QLIN_ERR_INVALID_ARG;
+  if (!k_cache || !k_scale || !v_cache || !v_scale) return QLIN_ERR_INVALID_ARG;
+  if (!al16(k_cache) || !al16(k_scale) || !al16(v_cache) || !al16(v_scale)) return QLIN_ERR_INVALID_ARG;
   return QLIN_OK;
 }
 
@@ -177,6 +186,25 @@ const char *qlin_kernel_name(qlin_op op, qlin_qtype qtype, int64_t M, int64_t K,
       const int i = K == 32 ? 0 : K == 64 ? 1 : K == 128 ? 2 : 3;
       return op == QLIN_OP_KV_STORE_MIXED ? st[i] : ld[i];
     }
+    case QLIN_OP_RMSNORM:
+    case QLIN_OP_RMSNORM_QUANT:
+      if (M < 0 || K < 16 || (K % 16) || K > kNormMaxK) return "invalid";
+      return M == 0 ? "none" : "k_rmsnorm";
+    case QLIN_OP_ROPE:
+      if (M < 0 || K < 16 || (K % 16) || K > 512 || N < 1) return "invalid";
+      return M == 0 ? "none" : "k_rope";
+    case QLIN_OP_ROPE_KV_STORE_MIXED: {
+      if (M < 0 || N < 1 || !(K == 32 || K == 64 || K == 128 || K == 256)) return "invalid";
+      if (M == 0) return "none";
+      return K == 32   ? "k_rope_kv_store<32>"
+             : K == 64 ? "k_rope_kv_store<64>"
+             : K == 128 ? "k_rope_kv_store<128>" : "k_rope_kv_store<256>";
+    }
+    case QLIN_OP_W8A8_LINEAR_CODES: {
+      if (check_linear_shape(M, K, N)) return "invalid";
+      if (M == 0) return "none";
+      return qtype == QLIN_E4M3 ? "k_fp8_gemm" : qlin_kernel_name(QLIN_OP_I8_GEMM_S32, qtype, M, K, N);
+    }
     case QLIN_OP_W8A8_LINEAR: {
       if (check_linear_shape(M, K, N)) return "invalid";
       if (M == 0) return "none";
@@ -227,7 +255,13 @@ size_t qlin_workspace_bytes(qlin_op op, qlin_qtype qtype, int64_t M, int64_t K, 
       return round_up((size_t)M * (size_t)K * (qtype == QLIN_INT8 ? 2 : 1), 256) + round_up((size_t)M * 4, 256);
     case QLIN_OP_KV_STORE_MIXED:
     case QLIN_OP_KV_LOAD_MIXED:
+    case QLIN_OP_RMSNORM:
+    case QLIN_OP_RMSNORM_QUANT:
+    case QLIN_OP_ROPE:
+    case QLIN_OP_ROPE_KV_STORE_MIXED:
       return 0;
+    // INT8 codes as integer-valued BF16
+    case QLIN_OP_W8A8_LINEAR_CODES: return qtype == QLIN_E4M3 ? 0 : round_up((size_t)M * (size_t)K * 2, 256);
   }
   return (size_t)-1;
 }
@@ -409,19 +443,6 @@ qlin_status qlin_w8a8_gate_up_silu(qlin_qtype qtype, int64_t M, int64_t K, int64
   if (i8_fused_quant(M)) return from_cuda(launch_i8_swap(g, x, false, *dev, st, true));
   if (launch_quantize_act_i8bf16(M, K, x, input_scale, ws, dev->sms, st) != cudaSuccess) return QLIN_ERR_CUDA;
   return from_cuda(launch_i8_swap(g, ws, false, *dev, st));
-}
-
-// Shared argument checks of the two KV-cache entry points.
-static qlin_status check_kv(int64_t T, int64_t H, int64_t D, const int64_t *slots, int64_t num_slots,
-                            const void *k_cache, const void *k_scale, const void *v_cache, const void *v_scale) {
-  if (T < 0 || H < 1 || num_slots < 0) return QLIN_ERR_INVALID_ARG;
-  if (!(D == 32 || D == 64 || D == 128 || D == 256)) return QLIN_ERR_INVALID_ARG;
-  if (H > 4096 || T > ((int64_t)1 << 40) / H || num_slots > ((int64_t)1 << 40) / H) return QLIN_ERR_INVALID_ARG;
-  if (T == 0) return QLIN_OK;
-  if (!slots || !al16(slots)) return QLIN_ERR_INVALID_ARG;
-  if (!k_cache || !k_scale || !v_cache || !v_scale) return QLIN_ERR_INVALID_ARG;
-  if (!al16(k_cache) || !al16(k_scale) || !al16(v_cache) || !al16(v_scale)) return QLIN_ERR_INVALID_ARG;
-  return QLIN_OK;
 }
 
 qlin_status qlin_kv_store_mixed(int64_t T, int64_t H, int64_t D, const void *k, int64_t ldk, const void *v,

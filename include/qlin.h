@@ -34,10 +34,10 @@
  *     early (programmatic dependent launch): a kernel's CTAs take SMs while its
  *     predecessor finishes, and wait for it before they read its outputs.  The
  *     inputs read before that wait are a linear's weights: its codes (`qw`),
- *     their scales (`w_scale`) and its bias.  So none of these may be the
- *     output of the library call right before the linear on its stream, other
- *     than qlin_quantize_weight (which lets no later kernel start before it
- *     completes).  Weights written by any other kernel or copy, or by any
+ *     their scales (`w_scale`) and its bias, and a norm's weight.  So none of
+ *     these may be the output of the library call right before the linear (or
+ *     norm) on its stream, other than qlin_quantize_weight (which lets no later
+ *     kernel start before it completes).  Weights written by any other kernel or copy, or by any
  *     earlier call, are read as written.
  *   - Argument errors are detected on the host before anything is launched and
  *     returned as a status: NULL required pointer, negative sizes, K or N not a
@@ -91,7 +91,12 @@ typedef enum {
   QLIN_OP_KV_STORE_MIXED = 7, /* for qlin_kernel_name: M = tokens, K = head_dim, N = kv heads */
   QLIN_OP_KV_LOAD_MIXED = 8,
   QLIN_OP_W8A16_GATE_UP_SILU = 9, /* N = the intermediate size I (output channels) */
-  QLIN_OP_W8A8_GATE_UP_SILU = 10
+  QLIN_OP_W8A8_GATE_UP_SILU = 10,
+  QLIN_OP_RMSNORM = 11, /* N is ignored */
+  QLIN_OP_RMSNORM_QUANT = 12,
+  QLIN_OP_W8A8_LINEAR_CODES = 13,
+  QLIN_OP_ROPE = 14, /* M = tokens, K = head_dim, N = q and k heads together */
+  QLIN_OP_ROPE_KV_STORE_MIXED = 15 /* M = tokens, K = head_dim, N = kv heads */
 } qlin_op;
 
 /*
@@ -325,6 +330,154 @@ qlin_status qlin_kv_store_mixed(int64_t T, int64_t H, int64_t D, const void *k, 
 qlin_status qlin_kv_load_mixed(int64_t T, int64_t H, int64_t D, const int64_t *slots, int64_t num_slots,
                                const void *k_cache, const void *k_scale, const void *v_cache,
                                const void *v_scale, void *k_out, void *v_out, qlin_stream_t stream);
+
+/*
+ * RMSNorm with the residual's addition, the step between two of a decoder
+ * layer's linears.  Per row m of M:
+ *   h = bf16(x + residual)              (h = x when residual is NULL)
+ *   r = fl32(1 / sqrt(sum_k h[k]^2 / K + eps))
+ *   y = fl32(fl32(h * r) * weight)      (two binary32 products)
+ * The sum does not depend on an order of additions beyond about 2^-46 of its
+ * value, so r, and with it every code below, is reproducible.
+ *   qlin_rmsnorm:       y_out [M,K] BF16 = bf16(y): the input of a W8A16 linear.
+ *   qlin_rmsnorm_quant: qx [M,K] codes of y, without a rounding to BF16 first:
+ *     input_scale given (one fp32 on the device): static codes Q(y / s), as
+ *       qlin_quantize_act_static makes them; x_scale must be NULL;
+ *     input_scale NULL: x_scale[m] = max_k |y| / QMAX (1 if that is 0), codes
+ *       Q(y / x_scale[m]), as qlin_quantize_act_dynamic makes them.
+ *     qlin_w8a8_linear_codes takes the codes and scales.
+ *   x         [M] rows of K BF16, row stride ldx elements (>= K, a multiple of 8).
+ *   residual  likewise with ldr, or NULL.
+ *   weight    [K] BF16; read before the wait for the previous kernel, like a
+ *             linear's weights.
+ *   h_out     [M,K] dense BF16, the sum; required with a residual (which it may
+ *             be, when ldr == K: the stream is then updated in place), NULL
+ *             without one.
+ * Requirements: M >= 0, 16 <= K <= 32768, K % 16 == 0, eps >= 0 and finite,
+ * pointers 16-byte aligned (input_scale 4-byte).  No workspace.
+ */
+qlin_status qlin_rmsnorm(int64_t M, int64_t K, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                         const void *weight, float eps, void *h_out, void *y_out, qlin_stream_t stream);
+qlin_status qlin_rmsnorm_quant(qlin_qtype qtype, int64_t M, int64_t K, const void *x, int64_t ldx,
+                               const void *residual, int64_t ldr, const void *weight, float eps,
+                               const float *input_scale, void *h_out, void *qx, float *x_scale,
+                               qlin_stream_t stream);
+
+/*
+ * W8A8 linear on activations that are codes already (qlin_rmsnorm_quant,
+ * qlin_quantize_act_static or _dynamic made them):
+ *   y[m,n] = bf16( acc[m,n] * (s_x * w_scale[n]) + bias[n] )
+ * with acc as in qlin_w8a8_linear and s_x = x_scale[m] (per_token != 0, x_scale
+ * [M]) or x_scale[0] (per_token == 0).  Given what the linears of the same
+ * names quantize to, the results are theirs, bit for bit.
+ *   ws: qlin_workspace_bytes(QLIN_OP_W8A8_LINEAR_CODES, qtype, M, K, N) bytes
+ *   (INT8 codes as integer-valued BF16; 0 for E4M3).
+ * Requirements as for qlin_w8a16_linear, qx 16-byte aligned.
+ */
+qlin_status qlin_w8a8_linear_codes(qlin_qtype qtype, int64_t M, int64_t K, int64_t N, const void *qx,
+                                   const float *x_scale, int per_token, const void *qw, const float *w_scale,
+                                   const void *bias, void *y, void *ws, size_t ws_bytes, qlin_stream_t stream);
+
+/*
+ * Rotary positions.  A token's head is turned pair by pair:
+ *   a' = a cos - b sin,  b' = b cos + a sin    (binary32, then rounded to BF16)
+ * over its first `rot` dimensions; the others pass unchanged.
+ *   QLIN_ROPE_HALF:  pair i is (i, i + rot/2).
+ *   QLIN_ROPE_PAIRS: pair i is (2i, 2i + 1).
+ *
+ * qlin_rope_table writes the table the other two read: max_pos rows of rot/2
+ * cosines, then rot/2 sines, of pos * f_i, computed in FP64 and multiplied by
+ * `amplitude` (1, or the attention factor of a scaled model).  With
+ * f_i = theta^(-2i/rot):
+ *   QLIN_ROPE_PLAIN:    f_i
+ *   QLIN_ROPE_LINEAR:   f_i / factor
+ *   QLIN_ROPE_NTK:      theta * factor^(rot/(rot-2)) in theta's place
+ *   QLIN_ROPE_BY_PARTS: f_i where the pair turns at least beta_fast times within
+ *     original_context positions, f_i / factor where it turns at most beta_slow
+ *     times, linear in the number of turns between.
+ * (factor is read by the last three; original_context and the betas by the last.)
+ *
+ * qlin_rope turns q [T] rows of Hq heads and k [T] rows of Hk heads (Hk may be
+ * 0, k and k_out then NULL) into q_out and k_out, which may be q and k
+ * themselves, with the same strides.
+ * qlin_rope_kv_store_mixed turns q into q_out and stores k, turned and rounded
+ * to BF16, and v into the mixed cache: the codes and scales are those of
+ * qlin_rope followed by qlin_kv_store_mixed, without k's way through memory.
+ *   positions  int64 [T].  A negative position skips the token (nothing of it
+ *              is written).  A position >= max_pos breaks the contract: the
+ *              token is skipped and the device status word is set to
+ *              QLIN_ERR_INVALID_ARG.
+ *   slots      int64 [T], as for qlin_kv_store_mixed; a token without a slot
+ *              still has its q turned.
+ * Requirements: T >= 0, Hq >= 1, D % 16 == 0 and 16 <= D <= 512 (32, 64, 128 or
+ * 256 with the store), rot % 16 == 0 and 16 <= rot <= D, strides >= heads * D
+ * and multiples of 8 elements, pointers 16-byte aligned.  No workspace.
+ */
+typedef enum { QLIN_ROPE_HALF = 0, QLIN_ROPE_PAIRS = 1 } qlin_rope_layout;
+typedef enum {
+  QLIN_ROPE_PLAIN = 0,
+  QLIN_ROPE_LINEAR = 1,
+  QLIN_ROPE_NTK = 2,
+  QLIN_ROPE_BY_PARTS = 3
+} qlin_rope_scaling;
+qlin_status qlin_rope_table(int64_t max_pos, int64_t rot, double theta, qlin_rope_scaling scaling, double factor,
+                            double original_context, double beta_fast, double beta_slow, double amplitude,
+                            float *table, qlin_stream_t stream);
+qlin_status qlin_rope(qlin_rope_layout layout, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot,
+                      const float *table, int64_t max_pos, const int64_t *positions, const void *q, int64_t ldq,
+                      const void *k, int64_t ldk, void *q_out, int64_t ldqo, void *k_out, int64_t ldko,
+                      qlin_stream_t stream);
+qlin_status qlin_rope_kv_store_mixed(qlin_rope_layout layout, int64_t T, int64_t Hq, int64_t H, int64_t D,
+                                     int64_t rot, const float *table, int64_t max_pos, const int64_t *positions,
+                                     const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                                     int64_t ldv, void *q_out, int64_t ldqo, const int64_t *slots,
+                                     int64_t num_slots, void *k_cache, void *k_scale, void *v_cache, void *v_scale,
+                                     qlin_stream_t stream);
+
+/*
+ * Attention over the mixed KV cache: softmax(scale * q k^T) v with grouped
+ * heads, keys and values being the codes times their scales (no rounding to
+ * BF16 between), ragged sequences and paged slots.
+ *   q, out     BF16 [T] rows of Hq heads of D, row strides ldq, ldo elements.
+ *              Query head h reads kv head h / (Hq / H).
+ *   q_start    int32 [B+1]: rows q_start[b] .. q_start[b+1] - 1 are sequence b's
+ *              new tokens, at the last positions of its context.  max_q is an
+ *              upper bound of a sequence's rows.
+ *   kv_len     int32 [B]: positions 0 .. kv_len[b] - 1 of sequence b are in the
+ *              cache, its new tokens' included.  max_kv is an upper bound.
+ *   block_table int32 [B, max_blocks]: position j of sequence b is in slot
+ *              block_table[b, j / block_size] * block_size + j % block_size.
+ *   causal     != 0: a token at position p sees positions <= p; 0: all of them.
+ *   window     > 0: positions > p - window only (and, without causal,
+ *              < p + window); 0: no window.
+ * A row that sees no position gives +0 (kv_len 0, as in the padding rows of a
+ * captured batch; rows before position 0).  What is stored at positions that a
+ * row does not see (NaN included) does not reach it; a row that sees a NaN value
+ * code has NaN outputs.  Softmax statistics and sums are fp32; P and the scaled
+ * keys and values enter the matrix products as float16 (11 significant bits,
+ * under exponents of their own, so no value of the cache overflows).
+ * A page outside [0, num_slots / block_size), rows or positions beyond T, max_q,
+ * max_kv or max_blocks * block_size break the contract: they are left out and the
+ * device status word is set to QLIN_ERR_INVALID_ARG.
+ *   ws: qlin_attn_mixed_workspace_bytes(B, Hq, H, D, max_q, max_kv, window)
+ *   bytes: partial results where the positions are split over CTAs (few rows).
+ * Requirements: B >= 0, D 32, 64, 128 or 256, Hq a multiple of H, Hq / H <= 128,
+ * block_size >= 1, num_slots a multiple of block_size, window >= 0, scale finite,
+ * strides >= Hq * D and multiples of 8, pointers 16-byte aligned (q_start, kv_len
+ * and block_table 4-byte).  B, T or max_q == 0 enqueues nothing.
+ */
+qlin_status qlin_attn_mixed(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D, const void *q, int64_t ldq,
+                            const int32_t *q_start, int64_t max_q, const int32_t *kv_len, int64_t max_kv,
+                            const int32_t *block_table, int64_t max_blocks, int64_t block_size, int64_t num_slots,
+                            const void *k_cache, const void *k_scale, const void *v_cache, const void *v_scale,
+                            float scale, int causal, int64_t window, void *out, int64_t ldo, void *ws,
+                            size_t ws_bytes, qlin_stream_t stream);
+/* Workspace bytes of qlin_attn_mixed for these bounds ((size_t)-1 for invalid ones) and the name of the kernel
+ * (or sequence, joined by '+') it launches ("invalid", or "none" when it enqueues nothing). */
+size_t qlin_attn_mixed_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
+                                       int64_t window);
+const char *qlin_attn_mixed_kernel_name(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
+                                        int64_t window);
 
 /* Workspace bytes an operation needs for these sizes (0 if none).  Returns
  * (size_t)-1 for invalid arguments. */
