@@ -117,13 +117,14 @@ def _check(status: int, where: str):
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
+    # the handle of torch.cuda.current_stream(), without the 3 us that the Stream object costs
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _qt(qtype):
@@ -241,10 +242,12 @@ def qlin_kv_load_mixed(slots, k_cache, k_scale, v_cache, v_scale, k_out, v_out, 
 
 
 def _row_stride(t, least: int) -> int:
-    """Row stride (elements) of a 2-D tensor whose rows are contiguous."""
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    """Row stride (elements) of a 2-D tensor whose rows are contiguous, of `least` elements or more (a
+    single row's is whatever its tensor says, so at least that)."""
+    row, one = t.stride()
+    if one != 1:
         raise ValueError("rows must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), least)
+    return row if row >= least or t.shape[0] > 1 else least
 
 
 def qlin_rmsnorm(x, residual, weight, eps: float, h_out, y_out, stream=None):

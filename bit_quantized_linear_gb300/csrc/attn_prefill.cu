@@ -1,0 +1,663 @@
+// Attention over the mixed 8-bit KV cache for many rows (prefill, chunks): bound
+// by the tensor cores, 4 D flops for each (row, position).
+//
+// A CTA takes 256 rows of one (sequence, kv head), packed token-major over the
+// heads of the group, as two row tiles A and B of 128, and walks over the
+// positions 128 at a time.  Both tiles use each key and value tile, so the codes
+// are converted to float16 once for 256 rows.  Roles:
+//   * warps 0-3 and 4-7: softmax of tile A and of tile B, a thread per row.  S
+//     comes from tensor memory, P goes back there (over S) as float16.
+//   * warps 8-14: converters.  A unit is 4 KB of key or value codes; a warp loads
+//     its next unit's codes into registers while it converts one.  Keys become
+//     K-major float16 rows, values are transposed to V^T (positions along the
+//     row), both in the 128-byte swizzle the MMA reads.
+//   * warp 15: issues S = Q K^T (both from shared memory) and O += P V (P from
+//     tensor memory).  While one tile's softmax runs, the other's products do.
+//
+// Scaling.  q rows are scaled by powers of two to use float16's range.  A unit's
+// keys are scaled by code scale * 2^-ek and its values by 2^-ev, with one exponent
+// each for the unit's positions, so float16 holds them whatever the cache's
+// scales; 2^ek joins the score's factor and ev the exponent, so that neither
+// costs the softmax an instruction per score.  O is rescaled only where a row's
+// maximum grew by more than 2^6 since its reference; P stays below 2^14.
+#include <algorithm>
+
+#include "attn.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace qlin {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kPos = 128;       // positions of a tile
+constexpr int kRowTile = 128;   // rows of an MMA
+constexpr int kThreads = 512;
+constexpr int kIssuer = 15;     // the MMA warp
+constexpr int kFirstConverter = 8;
+constexpr int kMetaSlots = 4;
+constexpr float kPBias = 8.0f;  // P is 2^8 p: float16's subnormals lie below 2^-22 p
+constexpr float kGrowth = 6.0f;
+constexpr int kValueUp = 5;     // a value's scale becomes 2^5..2^6 (times at most 448: below float16's 65504)
+constexpr int kValueSpan = 8;   // scales of a unit within 2^8 share an exponent: E4M3's 2^-9 stays normal
+
+// What the softmax needs of a position tile beside S, per 32 positions: the
+// exponents of keys and values, positions present, positions with a NaN value, and
+// whether the values have an exponent for each position instead (pos_ev).
+struct TileMeta {
+  int ek[4], ev[4];
+  unsigned valid[4], poison[4], wide[4];
+  float pos_ev[kPos];
+};
+
+template <int D>
+struct Config {
+  static constexpr int kChunks = D / 16;             // 16-byte pieces of a row of codes
+  static constexpr int kUnit = 256 / kChunks;        // positions of a unit (4 KB of codes)
+  static constexpr int kUnits = kPos / kUnit;        // units of a key (or value) tile
+  // Each converter's previous unit lies at most one step back, so a barrier it
+  // waits for is never two phases behind.
+  static constexpr int kConverters = 2 * kUnits < 7 ? 2 * kUnits : 7;
+  static constexpr int kQBytes = kRowTile * D * 2;   // a row tile of q
+  static constexpr int kTileBytes = kPos * D * 2;    // a key or value tile
+  static constexpr int kSub = kRowTile * 128;        // a 128-byte-wide column of a q or key tile
+  static constexpr int kVSub = D * 128;              // 64 positions of V^T
+  static constexpr int kKAt = 2 * kQBytes, kVAt = kKAt + 2 * kTileBytes, kBarAt = kVAt + 2 * kTileBytes;
+  static constexpr int kSmem = kBarAt + 4096 + 1024;  // barriers and metadata; alignment
+  // tensor memory columns: S (P over it) of A and B, then O
+  static constexpr int kS = 0, kO = 2 * kPos, kColumns = 512;
+  static constexpr uint32_t kIdescS = umma_idesc(0, 0, kRowTile, kPos), kIdescO = umma_idesc(0, 0, kRowTile, D);
+};
+
+struct Shared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], meta_full[kMetaSlots];
+  uint32_t tmem;
+  int abort;
+  TileMeta meta[kMetaSlots];
+};
+
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  mma_bf16(d, a, b, idesc, acc);  // kind::f16; the operand type is in the descriptor
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  mma_bf16_ts(d, a, b, idesc, acc);
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float f32x2_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// Byte offset of 16-byte unit `u` of row `r` in a tile of 128-byte rows under the
+// 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
+
+struct PrefillParams : AttnDev {
+  int row_tiles;
+};
+
+// The codes a converter's lane holds of one unit: 16 dimensions (chunk lane % C)
+// of positions 8 * (lane / C) + i, and their scales.
+template <int D>
+struct Unit {
+  uint4 code[8];
+  uint32_t scale[4];  // two float16 each
+  unsigned valid[Config<D>::kUnit / 32];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParams p) {
+  using C = Config<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Shared &sh = *reinterpret_cast<Shared *>(smem + C::kBarAt);
+  static_assert(sizeof(Shared) <= 4096, "barrier area");
+  volatile int *abort_flag = &sh.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // the last row tiles see the most positions: they go first
+  const int heads = p.B * p.H;
+  const int tile = p.row_tiles - 1 - (int)(blockIdx.x / heads);
+  const int b = (int)(blockIdx.x % heads) / p.H, h = (int)(blockIdx.x % heads) % p.H;
+  pdl_wait();
+  pdl_trigger();
+  const Sequence sq = sequence(p, b);
+  if (sq.broken && h == 0 && tile == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
+  const int R = sq.kept * p.G, r0 = tile * 2 * kRowTile;
+  if (r0 >= R || R <= p.few_rows) return;
+
+  // positions any row sees [beg, end), every row sees [all_lo, all_hi)
+  int beg, end, all_lo, all_hi;
+  const int last = min(r0 + 2 * kRowTile, R) - 1;
+  sees(p, sq, r0 / p.G, beg, all_hi);
+  sees(p, sq, last / p.G, all_lo, end);
+  const int lo = beg;
+  beg &= ~31;
+  const int n = end > beg ? (end - beg + kPos - 1) / kPos : 0;
+
+  if (n == 0) {  // rows that see nothing
+    for (int i = threadIdx.x; i < (last - r0 + 1) * (D / 8); i += kThreads) {
+      const int r = r0 + i / (D / 8);
+      uint16_t *dst = p.out + (int64_t)(sq.first + r / p.G) * p.ldo + (int64_t)(h * p.G + r % p.G) * D;
+      reinterpret_cast<uint4 *>(dst)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], C::kUnits);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], C::kUnits);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sh.meta_full[i], 2 * C::kUnits);
+    sh.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kIssuer) tmem_alloc(&sh.tmem, C::kColumns);
+
+  // q rows -> float16 in shared memory, by the softmax threads
+  float row_factor = 0.0f;
+  const int r = r0 + threadIdx.x;  // a softmax thread's row
+  if (warp < kFirstConverter) {
+    uint4 w[D / 8];
+    float top = 0.0f;
+    const uint16_t *src = p.q + (int64_t)(sq.first + r / p.G) * p.ldq + (int64_t)(h * p.G + r % p.G) * D;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      w[i] = r < R ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+    }
+    const int e = q_exponent(top);
+    // a negative softmax scale turns q around, so that the score's factor is positive
+    const float up = p.scale_log2 < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);
+    row_factor = fabsf(p.scale_log2) * pow2i(max(e - 14, -126));
+    const uint32_t at = smem_u32(smem) + (warp >> 2) * C::kQBytes;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = half2_of(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
+      sts128(at + (i / 8) * C::kSub + swizzled(threadIdx.x % kRowTile, i % 8), make_uint4(o[0], o[1], o[2], o[3]));
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp < kFirstConverter) {
+    // ------------------------------------------------------------- softmax
+    const int half = warp >> 2;  // tile A or B
+    const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // lanes 32 * (warp % 4)
+    const uint32_t s_at = at + C::kS + half * kPos, o_at = at + C::kO + half * D;
+    int row_lo = lo, row_hi = end;
+    if (r < R) sees(p, sq, r / p.G, row_lo, row_hi);
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
+           mbar_wait(&sh.s_full[half], j & 1, abort_flag);
+      if (!__all_sync(~0u, ok)) break;
+      tc_fence_after();
+      const TileMeta &tm = sh.meta[j % kMetaSlots];
+      const int j0 = beg + j * kPos;
+      const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
+                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
+                        (tm.wide[0] | tm.wide[1] | tm.wide[2] | tm.wide[3]) == 0;
+      // first pass: the row's largest exponent
+      float now = m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t s[32];
+        tmem_ld32(s_at + c * 32, s);
+        tmem_ld_wait();
+        const float f = row_factor * pow2i(tm.ek[c]);
+        if (full) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+          if (mx > -INFINITY) now = fmaxf(now, fmaf(mx, f, (float)tm.ev[c]));
+        } else {
+          const int d = j0 + c * 32;
+          const unsigned valid = tm.valid[c];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float ev = tm.wide[c] ? tm.pos_ev[c * 32 + i] : (float)tm.ev[c];
+            if (d + i >= row_lo && d + i < row_hi && ((valid >> i) & 1))
+              now = fmaxf(now, fmaf(__uint_as_float(s[i]), f, ev));
+          }
+        }
+      }
+      if (__any_sync(~0u, now > m + kGrowth)) {
+        const float a = now > m + kGrowth ? exp2_approx(m - now) : 1.0f;
+        if (now > m + kGrowth) m = now;
+        if (j > 0) {
+          l *= a;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_at + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            tmem_st32(o_at + c * 32, o);
+          }
+        }
+      }
+      // second pass: P = 2^(s + ev - m + bias), over S
+      const float z = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t s[32];
+        tmem_ld32(s_at + c * 32, s);
+        tmem_ld_wait();
+        const float f = row_factor * pow2i(tm.ek[c]), g = (float)tm.ev[c] + kPBias - z;
+        const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
+        uint32_t o[16];
+        uint64_t sum = 0;
+        if (full) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x =
+                f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
+            const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
+            sum = f32x2_add(sum, f32x2_pack(a, e));
+            o[i] = half2_of(a, e);
+          }
+        } else {
+          const int d = j0 + c * 32;
+          const unsigned valid = tm.valid[c], poison = tm.poison[c];
+          const bool wide = tm.wide[c] != 0;
+          float q[32], t = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const bool seen = d + i >= row_lo && d + i < row_hi && ((valid >> i) & 1);
+            // l counts P without its value's exponent; for a wide unit that is this position's
+            const float dev = wide ? tm.pos_ev[c * 32 + i] - (float)tm.ev[c] : 0.0f;
+            q[i] = seen ? exp2_approx(fmaf(__uint_as_float(s[i]), f, g + dev)) : 0.0f;
+            if (seen && ((poison >> i) & 1)) q[i] = NAN;
+            t += q[i] * pow2i(-(int)dev);
+          }
+          sum = f32x2_pack(t, 0.0f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = half2_of(q[2 * i], q[2 * i + 1]);
+        }
+        l = fmaf(f32x2_lo(sum) + f32x2_hi(sum), pow2i(-tm.ev[c]), l);
+        tmem_st16(s_at + c * 16, o);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.p_full[half]);
+    }
+    if (__all_sync(~0u, ok)) ok = mbar_wait(&sh.o_full[half], 0, abort_flag);
+    if (__all_sync(~0u, ok)) {
+      tc_fence_after();
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      uint16_t *dst = p.out + (int64_t)(sq.first + r / p.G) * p.ldo + (int64_t)(h * p.G + r % p.G) * D;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o_at + c * 32, o);
+        tmem_ld_wait();
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          w[i] = (uint32_t)f32_to_bf16_bits(__uint_as_float(o[2 * i]) * inv) |
+                 ((uint32_t)f32_to_bf16_bits(__uint_as_float(o[2 * i + 1]) * inv) << 16);
+        if (r < R) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(dst + c * 32)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      }
+    } else {
+      *abort_flag = 1;
+    }
+    tc_fence_before();
+  } else if (warp == kIssuer) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      const uint32_t base = smem_u32(smem);
+      const auto scores = [&](int half, int j) {
+        const uint64_t a = umma_desc_sw128(base + half * C::kQBytes);
+        const uint64_t bd = umma_desc_sw128(base + C::kKAt + (j & 1) * C::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t step = (uint64_t)((k / 4) * (C::kSub >> 4) + (k % 4) * 2);
+          mma_f16_ss(tmem + C::kS + half * kPos, a + step, bd + step, C::kIdescS, k > 0);
+        }
+        mma_commit(&sh.s_full[half]);
+      };
+      const auto outputs = [&](int half, int j) {
+        const uint64_t bd = umma_desc_sw128(base + C::kVAt + (j & 1) * C::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < kPos / 16; ++k)
+          mma_f16_ts(tmem + C::kO + half * D, tmem + C::kS + half * kPos + k * 8,
+                     bd + (uint64_t)((k / 4) * (C::kVSub >> 4) + (k % 4) * 2), C::kIdescO, j > 0 || k > 0);
+      };
+      bool ok = mbar_wait(&sh.k_full[0], 0, abort_flag);
+      if (ok) {
+        tc_fence_after();
+        scores(0, 0);
+        scores(1, 0);
+        mma_commit(&sh.k_empty[0]);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        ok = mbar_wait(&sh.v_full[j & 1], (j >> 1) & 1, abort_flag) && mbar_wait(&sh.p_full[0], j & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        outputs(0, j);
+        if (j + 1 < n) {
+          ok = mbar_wait(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          scores(0, j + 1);
+        } else {
+          mma_commit(&sh.o_full[0]);
+        }
+        ok = mbar_wait(&sh.p_full[1], j & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        outputs(1, j);
+        mma_commit(&sh.v_empty[j & 1]);
+        if (j + 1 < n) {
+          scores(1, j + 1);
+          mma_commit(&sh.k_empty[(j + 1) & 1]);
+        } else {
+          mma_commit(&sh.o_full[1]);
+        }
+      }
+      if (!ok) *abort_flag = 1;
+      // every commit's arrival lands before the CTA leaves: the last one covers all
+      if (ok) {
+        mbar_wait_drain(&sh.o_full[1], 0);
+      } else {
+        mma_commit(&sh.o_full[1]);
+        mbar_wait_drain(&sh.o_full[1], 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp - kFirstConverter < C::kConverters) {
+    // ------------------------------------------------------------ converters
+    constexpr int kSteps = 2 * C::kUnits;
+    constexpr int kWords = C::kUnit / 32;  // 32-position words of a unit
+    const int chunk = lane % C::kChunks, octet = lane / C::kChunks;
+    const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
+    const uint32_t base = smem_u32(smem);
+    // unit u: step s = u / kSteps converts key tile s and value tile s - 1
+    const int units = (n + 1) * kSteps;
+    struct Place {
+      int tile, block;  // position tile, unit within it
+      bool value, real;
+    };
+    const auto place = [&](int u) {
+      const int s = u / kSteps, k = u % kSteps;
+      Place q;
+      q.value = k >= C::kUnits;
+      q.block = q.value ? k - C::kUnits : k;
+      q.tile = q.value ? s - 1 : s;
+      q.real = u < units && q.tile >= 0 && q.tile < n;
+      return q;
+    };
+    const auto following = [&](int u) {  // the warp's next unit after u that exists
+      do u += C::kConverters;
+      while (u < units && !place(u).real);
+      return u;
+    };
+    // pages of the lane's positions of unit u (-1: none)
+    const auto lookup = [&](int u, int (&page)[kWords]) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) page[i] = -1;
+      if (u >= units) return;
+      const Place q = place(u);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int j = beg + q.tile * kPos + q.block * C::kUnit + i * 32 + lane;
+        if (j >= lo && j < end) page[i] = __ldg(table + block_of(p, j));
+      }
+    };
+    const auto load = [&](int u, const int (&page)[kWords], Unit<D> &x) {
+      if (u >= units) return;
+      const Place q = place(u);
+      int64_t row[kWords];  // (slot, head) row of the lane's positions
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int j = beg + q.tile * kPos + q.block * C::kUnit + i * 32 + lane;
+        const bool wanted = j >= lo && j < end, ok = wanted && page[i] >= 0 && page[i] < p.num_blocks;
+        if (wanted && !ok) set_status(p.status, QLIN_ERR_INVALID_ARG);
+        x.valid[i] = __ballot_sync(~0u, ok);
+        row[i] = ok ? ((int64_t)page[i] * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
+      }
+      const uint8_t *codes = q.value ? p.vc : p.kc;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = octet * 8 + i;
+        int64_t at = __shfl_sync(~0u, row[0], t & 31);
+        unsigned valid = x.valid[0];
+        if constexpr (kWords == 2) {
+          const int64_t other = __shfl_sync(~0u, row[1], t & 31);
+          if (t >= 32) at = other, valid = x.valid[1];
+        }
+        const bool ok = (valid >> (t & 31)) & 1;
+        x.code[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(codes + at * D) + chunk) : make_uint4(0, 0, 0, 0);
+        const uint16_t *sc = q.value ? p.vs + at : p.ks + at * (D / 32) + chunk / 2;
+        const uint32_t s = ok ? __ldg(sc) : 0u;
+        if (i % 2 == 0) x.scale[i / 2] = s;
+        else x.scale[i / 2] |= s << 16;
+      }
+    };
+    const auto scale_of = [](const Unit<D> &x, int i) {
+      return __half2float(__ushort_as_half((uint16_t)(x.scale[i / 2] >> (16 * (i & 1)))));
+    };
+    // exponent e of a scale, 2^e <= |s| < 2^(e+1); those that are not finite count as the largest
+    const auto exponent = [](uint32_t abs_bits) { return min((int)(abs_bits >> 23) - 127, 15); };
+
+    Unit<D> x, y;
+    int page[kWords];
+    int u = warp - kFirstConverter;
+    if (!place(u).real) u = following(u);
+    lookup(u, page);
+    load(u, page, x);
+    int next = u < units ? following(u) : units;
+    lookup(next, page);
+    bool ok = true;
+    while (u < units) {
+      const Place q = place(u);
+      load(next, page, y);
+      const int after = next < units ? following(next) : units;
+      lookup(after, page);
+      TileMeta &tm = sh.meta[q.tile % kMetaSlots];
+      const int j0 = beg + q.tile * kPos;
+      // exponents of the unit's largest and smallest scale (zeros apart)
+      unsigned top = 0x33800000u, low = 0x7F800000u;  // 2^-24, float16's smallest
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const unsigned a = __float_as_uint(fabsf(scale_of(x, i)));
+        top = max(top, a);
+        low = a ? min(low, a) : low;
+      }
+      const int e = exponent(__reduce_max_sync(~0u, top));
+      if (!q.value) {
+        const float down = pow2i(-e);
+        ok = mbar_wait(&sh.k_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
+        if (!__all_sync(~0u, ok)) break;
+        if (lane < kWords) {
+          tm.ek[q.block * kWords + lane] = e;
+          tm.valid[q.block * kWords + lane] = lane == 0 ? x.valid[0] : x.valid[kWords - 1];
+        }
+        const uint32_t dst = base + C::kKAt + (q.tile & 1) * C::kTileBytes + (chunk / 4) * C::kSub;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __half2 sc = __float2half2_rn(scale_of(x, i) * down);
+          const uint32_t c[4] = {x.code[i].x, x.code[i].y, x.code[i].z, x.code[i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            int8x4_to_half(c[k], o[2 * k], o[2 * k + 1]);
+            o[2 * k] = half2_bits(__hmul2(bits_half2(o[2 * k]), sc));
+            o[2 * k + 1] = half2_bits(__hmul2(bits_half2(o[2 * k + 1]), sc));
+          }
+          const int row = q.block * C::kUnit + octet * 8 + i, unit = (chunk % 4) * 2;
+          const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), z = make_uint4(o[4], o[5], o[6], o[7]);
+          // lanes of the second column store their upper half first: no two of a row's
+          // lanes meet in a bank
+          const bool second = (lane >> 2) & 1;
+          sts128(dst + swizzled(row, unit + (second ? 1 : 0)), second ? z : a);
+          sts128(dst + swizzled(row, unit + (second ? 0 : 1)), second ? a : z);
+        }
+      } else {
+        const bool wide = e - min(exponent(__reduce_min_sync(~0u, low)), e) > kValueSpan;
+        unsigned poison[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) poison[i] = 0;
+        if (!(j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
+              (x.valid[0] & x.valid[kWords - 1]) == ~0u)) {
+          // positions that some row does not see: NaN codes and scales that are not
+          // finite become zeros, which P = 0 leaves alone; rows that do see one get
+          // their NaN from P
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t bad = __vcmpeq4(x.code[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                           __vcmpeq4(x.code[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                           __vcmpeq4(x.code[i].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                           __vcmpeq4(x.code[i].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            const uint32_t s = (x.scale[i / 2] >> (16 * (i & 1))) & 0x7FFFu;
+            const unsigned who = __ballot_sync(~0u, bad != 0 || s >= 0x7C00u);
+            const unsigned mine = (who >> (octet * C::kChunks)) & ((1u << C::kChunks) - 1);
+            if (mine) {
+              x.code[i] = make_uint4(0, 0, 0, 0);
+              x.scale[i / 2] &= (i & 1) ? 0xFFFFu : 0xFFFF0000u;
+            }
+#pragma unroll
+            for (int o = 0; o < 32 / C::kChunks; ++o)
+              if ((who >> (o * C::kChunks)) & ((1u << C::kChunks) - 1)) poison[o / 4] |= 1u << ((o % 4) * 8 + i);
+          }
+        }
+        // (e stands for the scales as loaded: one that is not finite only makes it the largest)
+        if (lane < kWords) {
+          tm.ev[q.block * kWords + lane] = e - kValueUp;
+          tm.poison[q.block * kWords + lane] = lane == 0 ? poison[0] : poison[kWords - 1];
+          tm.wide[q.block * kWords + lane] = wide;
+        }
+        // the octet's scales, two positions at a time
+        __half2 sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s0 = scale_of(x, 2 * i), s1 = scale_of(x, 2 * i + 1);
+          int e0 = e, e1 = e;
+          if (wide) {
+            const unsigned a0 = __float_as_uint(fabsf(s0)), a1 = __float_as_uint(fabsf(s1));
+            e0 = a0 ? exponent(a0) : e;
+            e1 = a1 ? exponent(a1) : e;
+            if (chunk == 0) {
+              float *pos = tm.pos_ev + q.block * C::kUnit + octet * 8 + 2 * i;
+              pos[0] = (float)(e0 - kValueUp);
+              pos[1] = (float)(e1 - kValueUp);
+            }
+          }
+          sc[i] = __floats2half2_rn(s0 * pow2i(kValueUp - e0), s1 * pow2i(kValueUp - e1));
+        }
+        ok = mbar_wait(&sh.v_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
+        if (!__all_sync(~0u, ok)) break;
+        const int first = q.block * C::kUnit + octet * 8;  // position within the tile
+        const uint32_t dst = base + C::kVAt + (q.tile & 1) * C::kTileBytes + (first / 64) * C::kVSub;
+        const int unit = first % 64 / 8;
+        // Eight dimensions at a time.  Lanes turn their eight bytes by lane % 8, so that
+        // the eight lanes that store at once write rows of different remainders mod 8:
+        // the swizzle then spreads them over all banks.
+        const uint32_t turn = lane & 7;
+        uint32_t sel0 = 0, sel1 = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sel0 |= ((k + turn) & 7) << (4 * k);
+          sel1 |= ((k + 4 + turn) & 7) << (4 * k);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t lo8[8], hi8[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t c0 = w ? x.code[i].z : x.code[i].x, c1 = w ? x.code[i].w : x.code[i].y;
+            lo8[i] = __byte_perm(c0, c1, sel0);
+            hi8[i] = __byte_perm(c0, c1, sel1);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {  // byte k of the turned eight: dimension (k + turn) % 8
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t s0 = k < 4 ? lo8[2 * i] : hi8[2 * i], s1 = k < 4 ? lo8[2 * i + 1] : hi8[2 * i + 1];
+              const uint32_t two = __byte_perm(s0, s1, (k & 3) | ((4 + (k & 3)) << 4));
+              o[i] = half2_bits(__hmul2(bits_half2(e4m3x2_to_half((uint16_t)two)), sc[i]));
+            }
+            const int d = chunk * 16 + w * 8 + ((k + turn) & 7);
+            sts128(dst + swizzled(d, unit), make_uint4(o[0], o[1], o[2], o[3]));
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.meta_full[q.tile % kMetaSlots]);
+        mbar_arrive(q.value ? &sh.v_full[q.tile & 1] : &sh.k_full[q.tile & 1]);
+      }
+      u = next;
+      next = after;
+      x = y;
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kIssuer) tmem_dealloc(tmem, C::kColumns);
+  if (threadIdx.x == 0 && *abort_flag) set_status(p.status, QLIN_ERR_TIMEOUT);
+}
+
+template <int D>
+cudaError_t launch_d(const PrefillParams &p, int64_t ctas, cudaStream_t st) {
+  using C = Config<D>;
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(k_attn_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  return launch_kernel(k_attn_prefill<D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, st, 1, p);
+}
+
+}  // namespace
+
+bool attn_prefill_has(int64_t D) { return D == 64 || D == 128; }
+
+cudaError_t launch_attn_prefill(const AttnArgs &a, int few_rows, unsigned *status, cudaStream_t st) {
+  PrefillParams p{};
+  static_cast<AttnDev &>(p) = attn_dev(a, few_rows, status);
+  p.row_tiles = (int)((a.max_q * (a.Hq / a.H) + 2 * kRowTile - 1) / (2 * kRowTile));
+  const int64_t ctas = (int64_t)p.row_tiles * a.B * a.H;
+  if (a.D == 64) return launch_d<64>(p, ctas, st);
+  if (a.D == 128) return launch_d<128>(p, ctas, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace qlin

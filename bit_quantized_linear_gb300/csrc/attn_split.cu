@@ -24,6 +24,7 @@
 // fragments transposed: two movmatrix per 16 positions.
 #include <algorithm>
 
+#include "attn.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "kv_quant.cuh"
@@ -35,53 +36,12 @@ namespace {
 
 constexpr int kAttnWarps = 4;
 constexpr int kTile = 16;    // positions a warp handles at once
-constexpr float kLog2e = 1.44269504088896341f;
 
-struct SplitParams {
-  const uint16_t *q;
-  const int32_t *q_start, *kv_len, *block_table;
-  const uint8_t *kc, *vc;
-  const uint16_t *ks, *vs;
-  uint16_t *out;
+struct SplitParams : AttnDev {
   float *part_o, *part_lse;
-  int64_t ldq, ldo, max_blocks, chunk;
-  int T, H, G, max_q, max_kv, block_size, block_shift, num_blocks, row_tiles, splits, causal, window;
-  float scale_log2;
-  unsigned *status;
+  int64_t chunk;
+  int row_tiles, splits;
 };
-
-// What a CTA (or a row of the join) knows of its sequence.  Counts that break
-// the contract are cut to what is in bounds; `broken` says so.
-struct Sequence {
-  int first, n, kept, kv;  // first row, new tokens, those within max_q, positions
-  bool broken;
-};
-__device__ __forceinline__ Sequence sequence(const SplitParams &p, int b) {
-  Sequence s;
-  const int end = p.q_start[b + 1];
-  s.first = p.q_start[b];
-  s.n = end - s.first;
-  s.kv = p.kv_len[b];
-  const int64_t room = p.max_blocks * p.block_size;
-  const bool rows_ok = s.first >= 0 && end >= s.first && end <= p.T;
-  s.broken = !rows_ok || s.n > p.max_q || s.kv < 0 || s.kv > p.max_kv || s.kv > room;
-  if (!rows_ok) s.n = 0;
-  s.kept = min(s.n, p.max_q);
-  s.kv = max(0, min(s.kv, p.max_kv));
-  if (s.kv > room) s.kv = (int)room;
-  return s;
-}
-// Positions [lo, hi) that the new token `tok` of a sequence sees.
-__device__ __forceinline__ void sees(const SplitParams &p, const Sequence &s, int tok, int &lo, int &hi) {
-  const int pos = s.kv - s.n + tok;
-  lo = 0;
-  hi = s.kv;
-  if (p.causal) hi = min(hi, pos + 1);
-  if (p.window > 0) {
-    lo = max(lo, pos - p.window + 1);
-    if (!p.causal) hi = (int)min((int64_t)hi, (int64_t)pos + p.window);
-  }
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 0 : 16) : "memory");
@@ -102,36 +62,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^e as fp32, e in [-126, 127].
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// Four INT8 codes -> two words of float16: with the sign bit flipped a code is
-// u = c + 128, and the bytes (u, 0x64) are the float16 1024 + u; minus 1152.
-__device__ __forceinline__ void int8x4_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-  const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
-  const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
-  lo = *reinterpret_cast<const uint32_t *>(&x);
-  hi = *reinterpret_cast<const uint32_t *>(&y);
-}
-// Two E4M3 codes -> float16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_half(uint16_t c) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
-  return r;
-}
-
 template <int D, int NT>
 struct Geometry {
   static constexpr int kRows = 8 * NT;
@@ -188,7 +118,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const Sequence sq = sequence(p, b);
   if (sq.broken && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
   const int R = sq.kept * p.G, r0 = tile * kRows;
-  if (r0 >= R) return;
+  if (r0 >= R || R > p.few_rows) return;
 
   // positions of this CTA: what any of its rows sees, cut into parts
   const int last = min(r0 + kRows, R) - 1;
@@ -227,15 +157,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     }
     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-    int e = (int)(__float_as_uint(top) >> 23) - 127;
-    e = top > 0.0f && e < 128 ? max(e, -100) : 14;
+    const int e = q_exponent(top);
     const float up = pow2i(14 - e), factor = p.scale_log2 * pow2i(max(e - 14, -126));
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
       const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        qf[nt][k][j] = half2_bits(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
+        qf[nt][k][j] = half2_of(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -266,10 +195,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const int row16 = lane & 15;
   const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
   const auto position = [&](int n) { return beg + (n * kAttnWarps + warp) * kTile + row16; };
-  const auto block_of = [&](int j) { return p.block_shift >= 0 ? j >> p.block_shift : j / p.block_size; };
   const auto page = [&](int n) {  // page of the lane's position of tile n (-1: none)
     const int j = position(n);
-    return n < mine && j >= lo && j < end ? __ldg(table + block_of(j)) : -1;
+    return n < mine && j >= lo && j < end ? __ldg(table + block_of(p, j)) : -1;
   };
   uint32_t sc[(kGroups + 1) / 2];  // the lane's scales of the tile issued last
   uint32_t sv = 0;
@@ -280,7 +208,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     const bool wanted = n < mine && j >= lo && j < end;
     sok = wanted && blk >= 0 && blk < p.num_blocks;
     if (wanted && !sok && lane < 16) set_status(p.status, QLIN_ERR_INVALID_ARG);
-    const int64_t slot = sok ? (int64_t)blk * p.block_size + (j - block_of(j) * p.block_size) : 0;
+    const int64_t slot = sok ? (int64_t)blk * p.block_size + (j - block_of(p, j) * p.block_size) : 0;
     const int64_t base = slot * p.H + h;
     next_page = page(n + 1);
     if (n < mine) {
@@ -458,8 +386,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
         if (S[nt][2] == -INFINITY) w10 = 0.0f;
         if (S[nt][3] == -INFINITY) w11 = 0.0f;
       }
-      pf[nt][0] = transpose8x8(half2_bits(w00, w01));
-      pf[nt][1] = transpose8x8(half2_bits(w10, w11));
+      pf[nt][0] = transpose8x8(half2_of(w00, w01));
+      pf[nt][1] = transpose8x8(half2_of(w10, w11));
     }
 
     // O^T += V^T P^T: positions 2t, 2t+1 (and +8), dimensions g*D/8 ...
@@ -579,7 +507,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams
   pdl_trigger();
   const Sequence sq = sequence(p, b);
   const int rr = tile * rows + r;
-  if (rr >= sq.kept * p.G) return;
+  if (rr >= sq.kept * p.G || sq.kept * p.G > p.few_rows) return;
   const float *lse = p.part_lse + unit * p.splits * rows + r;
   float top = -INFINITY;
   for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, lse[(int64_t)s * rows]);
@@ -636,16 +564,36 @@ cudaError_t launch_d(const SplitParams &p, int rows, int64_t units, cudaStream_t
 
 }  // namespace
 
+AttnDev attn_dev(const AttnArgs &a, int few_rows, unsigned *status) {
+  AttnDev p{};
+  p.q = (const uint16_t *)a.q, p.q_start = a.q_start, p.kv_len = a.kv_len, p.block_table = a.block_table;
+  p.kc = (const uint8_t *)a.k_cache, p.vc = (const uint8_t *)a.v_cache;
+  p.ks = (const uint16_t *)a.k_scale, p.vs = (const uint16_t *)a.v_scale;
+  p.out = (uint16_t *)a.out, p.ldq = a.ldq, p.ldo = a.ldo, p.max_blocks = a.max_blocks;
+  p.B = (int)a.B, p.T = (int)a.T, p.H = (int)a.H, p.G = (int)(a.Hq / a.H);
+  p.max_q = (int)a.max_q, p.max_kv = (int)a.max_kv;
+  p.block_size = (int)a.block_size;
+  p.block_shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (a.block_size == (int64_t)1 << s) p.block_shift = s;
+  p.num_blocks = (int)(a.num_slots / a.block_size);
+  p.causal = a.causal != 0, p.window = (int)std::min<int64_t>(a.window, 1 << 30);
+  p.few_rows = few_rows;
+  p.scale_log2 = a.scale * kLog2e;
+  p.status = status;
+  return p;
+}
+
 // Rows are tiled by 8 where one tile holds them, else by 16 (each code is then
 // converted for twice the rows).  Positions are split until one wave of CTAs
 // fills the GPU, but not below 128 positions a part; where there are more units
 // than that, into parts of at least 1024 so that ragged sequences even out.
-AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
+AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t rows, int64_t max_kv,
                               int64_t window, int sms) {
   AttnSplitPlan plan{};
-  const int64_t G = Hq / H, R = max_q * G;
-  plan.rows = R <= 8 ? 8 : 16;
-  plan.row_tiles = (int)((R + plan.rows - 1) / plan.rows);
+  const int64_t G = Hq / H;
+  plan.rows = rows <= 8 ? 8 : 16;
+  plan.row_tiles = (int)((rows + plan.rows - 1) / plan.rows);
   int64_t range = max_kv;
   if (window > 0 && window < max_kv) range = std::min(range, window + plan.rows / G + 1);
   range += kTile - 1;  // the first part begins at a multiple of 16; the last one takes what is left
@@ -661,23 +609,11 @@ AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64
   return plan;
 }
 
-cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, void *ws, unsigned *status,
+cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, int few_rows, void *ws, unsigned *status,
                               cudaStream_t st) {
   SplitParams p{};
-  p.q = (const uint16_t *)a.q, p.q_start = a.q_start, p.kv_len = a.kv_len, p.block_table = a.block_table;
-  p.kc = (const uint8_t *)a.k_cache, p.vc = (const uint8_t *)a.v_cache;
-  p.ks = (const uint16_t *)a.k_scale, p.vs = (const uint16_t *)a.v_scale;
-  p.out = (uint16_t *)a.out, p.ldq = a.ldq, p.ldo = a.ldo, p.max_blocks = a.max_blocks;
-  p.T = (int)a.T, p.H = (int)a.H, p.G = (int)(a.Hq / a.H), p.max_q = (int)a.max_q, p.max_kv = (int)a.max_kv;
-  p.block_size = (int)a.block_size;
-  p.block_shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (a.block_size == (int64_t)1 << s) p.block_shift = s;
-  p.num_blocks = (int)(a.num_slots / a.block_size);
+  static_cast<AttnDev &>(p) = attn_dev(a, few_rows, status);
   p.row_tiles = plan.row_tiles, p.splits = plan.splits, p.chunk = plan.chunk;
-  p.causal = a.causal != 0, p.window = (int)std::min<int64_t>(a.window, 1 << 30);
-  p.scale_log2 = a.scale * kLog2e;
-  p.status = status;
   const int64_t units = a.B * a.H * plan.row_tiles;
   p.part_o = (float *)ws;
   p.part_lse = p.part_o ? p.part_o + units * plan.splits * plan.rows * a.D : nullptr;

@@ -252,8 +252,8 @@ cudaError_t launch_rope_table(int64_t max_pos, int64_t rot, double theta, int sc
 cudaError_t launch_rope(const RopeArgs &r, unsigned *status, int sms, cudaStream_t st);
 cudaError_t launch_rope_kv_store(const RopeArgs &r, const KvArgs &kv, unsigned *status, int sms, cudaStream_t st);
 
-// Attention over the mixed KV cache (attn_split.cu: rows in small tiles, the
-// positions split over CTAs).
+// Attention over the mixed KV cache.  attn_split.cu: sequences of few rows, the
+// positions split over CTAs.  attn_prefill.cu: sequences of many rows, on tcgen05.
 struct AttnArgs {
   int64_t B, T, Hq, H, D;
   const void *q;
@@ -278,10 +278,14 @@ struct AttnSplitPlan {
   int64_t chunk;   // positions of a part (a multiple of 16)
   size_t ws_bytes;
 };
-AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
+// `rows`: the most rows (new tokens times heads of a group) a sequence has for this kernel; sequences of more
+// than few_rows are left to the other one.
+AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t rows, int64_t max_kv,
                               int64_t window, int sms);
-cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, void *ws, unsigned *status,
+cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, int few_rows, void *ws, unsigned *status,
                               cudaStream_t st);
+bool attn_prefill_has(int64_t D);
+cudaError_t launch_attn_prefill(const AttnArgs &a, int few_rows, unsigned *status, cudaStream_t st);
 
 // tcgen05 kernels (gemm_tc.cu)
 cudaError_t launch_fp8_gemm(const GemmArgs &g, const DeviceInfo &dev, cudaStream_t st);

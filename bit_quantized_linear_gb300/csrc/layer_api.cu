@@ -48,9 +48,30 @@ qlin_status check_attn_sizes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_
   if (B < 0 || B > 1 << 20 || H < 1 || H > 4096 || Hq < 1 || Hq % H || Hq / H > 128 || !valid_kv_dim(D))
     return QLIN_ERR_INVALID_ARG;
   if (max_q < 0 || max_kv < 0 || max_q > 1 << 30 || max_kv > 1 << 30 || window < 0) return QLIN_ERR_INVALID_ARG;
-  // grid sizes stay below 2^31
+  // rows of a sequence and grid sizes stay below 2^31
+  if (max_q * (Hq / H) > 1 << 30) return QLIN_ERR_INVALID_ARG;
   if (B * H > ((int64_t)1 << 31) / (max_q * (Hq / H) / 8 + 1)) return QLIN_ERR_INVALID_ARG;
   return QLIN_OK;
+}
+
+// Which kernel takes which sequences: where some may have more than kFewRows rows
+// for a kv head, those go to the tcgen05 kernel and the others of the batch to
+// the split kernel; each kernel leaves the other's sequences.  A lone sequence
+// goes to one kernel by its bound.
+constexpr int64_t kFewRows = 64;
+struct AttnRoute {
+  bool few, many;  // the split kernel, the tcgen05 kernel
+  int few_rows;
+  AttnSplitPlan split;
+};
+AttnRoute attn_route(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv, int64_t window) {
+  AttnRoute r{};
+  const int64_t rows = max_q * (Hq / H);
+  r.many = attn_prefill_has(D) && rows > kFewRows;
+  r.few = !r.many || B > 1;
+  r.few_rows = r.many ? (r.few ? (int)kFewRows : 0) : (int)rows;
+  if (r.few) r.split = attn_split_plan(B, Hq, H, D, r.few_rows, max_kv, window, sm_count());
+  return r;
 }
 
 }  // namespace
@@ -156,15 +177,17 @@ size_t qlin_attn_mixed_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t
                                        int64_t window) {
   if (check_attn_sizes(B, Hq, H, D, max_q, max_kv, window)) return (size_t)-1;
   if (B == 0 || max_q == 0) return 0;
-  return attn_split_plan(B, Hq, H, D, max_q, max_kv, window, sm_count()).ws_bytes;
+  return attn_route(B, Hq, H, D, max_q, max_kv, window).split.ws_bytes;
 }
 
 const char *qlin_attn_mixed_kernel_name(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
                                         int64_t window) {
   if (check_attn_sizes(B, Hq, H, D, max_q, max_kv, window)) return "invalid";
   if (B == 0 || max_q == 0) return "none";
-  return attn_split_plan(B, Hq, H, D, max_q, max_kv, window, sm_count()).splits > 1 ? "k_attn_split+k_attn_join"
-                                                                                   : "k_attn_split";
+  const AttnRoute r = attn_route(B, Hq, H, D, max_q, max_kv, window);
+  if (!r.few) return "k_attn_prefill";
+  if (r.many) return r.split.splits > 1 ? "k_attn_prefill+k_attn_split+k_attn_join" : "k_attn_prefill+k_attn_split";
+  return r.split.splits > 1 ? "k_attn_split+k_attn_join" : "k_attn_split";
 }
 
 qlin_status qlin_attn_mixed(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t D, const void *q, int64_t ldq,
@@ -194,8 +217,11 @@ qlin_status qlin_attn_mixed(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t
   if (!work) return QLIN_OK;
   AttnArgs a{B,         T,          Hq,        H,       D,       q,       ldq,     q_start, max_q, kv_len, max_kv, block_table,
              max_blocks, block_size, num_slots, k_cache, k_scale, v_cache, v_scale, scale,   causal, window, out,   ldo};
-  const AttnSplitPlan plan = attn_split_plan(B, Hq, H, D, max_q, max_kv, window, sm_count());
-  return from_cuda(launch_attn_split(a, plan, ws, dev->status, (cudaStream_t)stream));
+  const AttnRoute r = attn_route(B, Hq, H, D, max_q, max_kv, window);
+  if (r.many && launch_attn_prefill(a, r.few_rows, dev->status, (cudaStream_t)stream) != cudaSuccess)
+    return QLIN_ERR_CUDA;
+  if (!r.few) return QLIN_OK;
+  return from_cuda(launch_attn_split(a, r.split, r.few_rows, ws, dev->status, (cudaStream_t)stream));
 }
 
 }  // extern "C"
