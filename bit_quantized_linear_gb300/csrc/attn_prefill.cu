@@ -7,8 +7,8 @@
 // are converted to float16 once for 256 rows.  Roles:
 //   * warps 0-3 and 4-7: softmax of tile A and of tile B, a thread per row.  S
 //     comes from tensor memory, P goes back there (over S) as float16.
-//   * warps 8-14: converters.  A unit is 4 KB of key or value codes; a warp loads
-//     its next unit's codes into registers while it converts one.  Keys become
+//   * warps 8-14: converters.  A unit is 4 KB of key or value codes; while a warp
+//     converts one, cp.async brings the next one's codes to the same lanes.  Keys become
 //     K-major float16 rows, values are transposed to V^T (positions along the
 //     row), both in the 128-byte swizzle the MMA reads.
 //   * warp 15: issues S = Q K^T (both from shared memory) and O += P V (P from
@@ -66,7 +66,9 @@ struct Config {
   static constexpr int kSub = kRowTile * 128;        // a 128-byte-wide column of a q or key tile
   static constexpr int kVSub = D * 128;              // 64 positions of V^T
   static constexpr int kKAt = 2 * kQBytes, kVAt = kKAt + 2 * kTileBytes, kBarAt = kVAt + 2 * kTileBytes;
-  static constexpr int kSmem = kBarAt + 4096 + 1024;  // barriers and metadata; alignment
+  static constexpr int kRawAt = kBarAt + 4096;       // barriers and metadata before; 4 KB for each converter
+  static constexpr int kSmem = kRawAt + kConverters * 4096 + 1024;  // 1024: alignment
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
   // tensor memory columns: S (P over it) of A and B, then O
   static constexpr int kS = 0, kO = 2 * kPos, kColumns = 512;
   static constexpr uint32_t kIdescS = umma_idesc(0, 0, kRowTile, kPos), kIdescO = umma_idesc(0, 0, kRowTile, D);
@@ -101,14 +103,20 @@ struct PrefillParams : AttnDev {
   int row_tiles;
 };
 
-// The codes a converter's lane holds of one unit: 16 dimensions (chunk lane % C)
-// of positions 8 * (lane / C) + i, and their scales.
+// What a converter's lane holds of one unit beside its codes: the scales of the
+// positions lane (and lane + 32) as they are in the cache, and which positions are
+// there.
 template <int D>
 struct Unit {
-  uint4 code[8];
-  uint32_t scale[4];  // two float16 each
+  uint32_t scale[2];
   unsigned valid[Config<D>::kUnit / 32];
 };
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 0 : 16) : "memory");
+}
+__device__ __forceinline__ float half_at(uint32_t w, int i) {
+  return __half2float(__ushort_as_half((uint16_t)(w >> (16 * i))));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParams p) {
@@ -218,39 +226,63 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       const TileMeta &tm = sh.meta[j % kMetaSlots];
       const int j0 = beg + j * kPos;
       const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
-                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
-                        (tm.wide[0] | tm.wide[1] | tm.wide[2] | tm.wide[3]) == 0;
+                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u;
+      // Scores this row does not see become -inf, those of a NaN value NaN (32 columns
+      // from c * 32 on).
+      const auto mask = [&](int c, uint32_t (&s)[32]) {
+        const int from = row_lo - (j0 + c * 32), to = row_hi - (j0 + c * 32);
+        unsigned seen = tm.valid[c];
+        seen &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+        seen &= to <= 0 ? 0u : to >= 32 ? ~0u : ~(~0u << to);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1 ? s[i] : 0xFF800000u;
+        const unsigned bad = tm.poison[c] & seen;
+        if (bad) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i] = (bad >> i) & 1 ? 0x7FFFFFFFu : s[i];
+        }
+      };
+      // a score's factor (never 0, so that -inf stays -inf)
+      const auto factor = [&](int c) { return fmaxf(row_factor * pow2i(tm.ek[c]), 0x1p-100f); };
+
       // first pass: the row's largest exponent
       float now = m;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t s[32];
-        tmem_ld32(s_at + c * 32, s);
+#pragma unroll 1
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t s0[32], s1[32];
+        tmem_ld32(s_at + c * 32, s0);
+        tmem_ld32(s_at + c * 32 + 32, s1);
         tmem_ld_wait();
-        const float f = row_factor * pow2i(tm.ek[c]);
-        if (full) {
-          float mx = -INFINITY;
+        if (!full) {
+          mask(c, s0);
+          mask(c + 1, s1);
+        }
+        float m0 = -INFINITY, m1 = -INFINITY;
+        if ((tm.wide[c] | tm.wide[c + 1]) == 0) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx = fmaxf(mx, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-          if (mx > -INFINITY) now = fmaxf(now, fmaf(mx, f, (float)tm.ev[c]));
+          for (int i = 0; i < 32; i += 2) {
+            m0 = fmaxf(m0, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])));
+            m1 = fmaxf(m1, fmaxf(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])));
+          }
+          m0 = fmaf(m0, factor(c), (float)tm.ev[c]);
+          m1 = fmaf(m1, factor(c + 1), (float)tm.ev[c + 1]);
         } else {
-          const int d = j0 + c * 32;
-          const unsigned valid = tm.valid[c];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float ev = tm.wide[c] ? tm.pos_ev[c * 32 + i] : (float)tm.ev[c];
-            if (d + i >= row_lo && d + i < row_hi && ((valid >> i) & 1))
-              now = fmaxf(now, fmaf(__uint_as_float(s[i]), f, ev));
+            const float e0 = tm.wide[c] ? tm.pos_ev[c * 32 + i] : (float)tm.ev[c];
+            const float e1 = tm.wide[c + 1] ? tm.pos_ev[c * 32 + 32 + i] : (float)tm.ev[c + 1];
+            m0 = fmaxf(m0, fmaf(__uint_as_float(s0[i]), factor(c), e0));
+            m1 = fmaxf(m1, fmaf(__uint_as_float(s1[i]), factor(c + 1), e1));
           }
         }
+        now = fmaxf(now, fmaxf(m0, m1));
       }
       if (__any_sync(~0u, now > m + kGrowth)) {
         const float a = now > m + kGrowth ? exp2_approx(m - now) : 1.0f;
         if (now > m + kGrowth) m = now;
         if (j > 0) {
           l *= a;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(o_at + c * 32, o);
@@ -262,45 +294,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         }
       }
       // second pass: P = 2^(s + ev - m + bias), over S
-      const float z = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t s[32];
-        tmem_ld32(s_at + c * 32, s);
-        tmem_ld_wait();
-        const float f = row_factor * pow2i(tm.ek[c]), g = (float)tm.ev[c] + kPBias - z;
-        const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
+      const float z = kPBias - (m == -INFINITY ? 0.0f : m);
+      const auto probabilities = [&](int c, uint32_t (&s)[32]) {
+        if (!full) mask(c, s);
+        const float f = factor(c), g = (float)tm.ev[c] + z;
         uint32_t o[16];
-        uint64_t sum = 0;
-        if (full) {
+        float sum;
+        if (!tm.wide[c]) {
+          const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const uint64_t x =
-                f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
+            const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
             const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
-            sum = f32x2_add(sum, f32x2_pack(a, e));
+            sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
             o[i] = half2_of(a, e);
           }
+          sum2[0] = f32x2_add(sum2[0], sum2[1]);
+          sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * pow2i(-tm.ev[c]);
         } else {
-          const int d = j0 + c * 32;
-          const unsigned valid = tm.valid[c], poison = tm.poison[c];
-          const bool wide = tm.wide[c] != 0;
-          float q[32], t = 0.0f;
+          // an exponent for each position; l counts P without it
+          sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const bool seen = d + i >= row_lo && d + i < row_hi && ((valid >> i) & 1);
-            // l counts P without its value's exponent; for a wide unit that is this position's
-            const float dev = wide ? tm.pos_ev[c * 32 + i] - (float)tm.ev[c] : 0.0f;
-            q[i] = seen ? exp2_approx(fmaf(__uint_as_float(s[i]), f, g + dev)) : 0.0f;
-            if (seen && ((poison >> i) & 1)) q[i] = NAN;
-            t += q[i] * pow2i(-(int)dev);
+          for (int i = 0; i < 16; ++i) {
+            const float e0 = tm.pos_ev[c * 32 + 2 * i], e1 = tm.pos_ev[c * 32 + 2 * i + 1];
+            const float a = exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, e0 + z));
+            const float e = exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, e1 + z));
+            sum += a * pow2i(-(int)e0) + e * pow2i(-(int)e1);
+            o[i] = half2_of(a, e);
           }
-          sum = f32x2_pack(t, 0.0f);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = half2_of(q[2 * i], q[2 * i + 1]);
         }
-        l = fmaf(f32x2_lo(sum) + f32x2_hi(sum), pow2i(-tm.ev[c]), l);
+        l += sum;
         tmem_st16(s_at + c * 16, o);
+      };
+      uint32_t s0[32], s1[32];
+      tmem_ld32(s_at, s0);
+#pragma unroll 1
+      for (int c = 0; c < 4; c += 2) {  // the next 32 columns arrive during these
+        tmem_ld_wait();
+        tmem_ld32(s_at + c * 32 + 32, s1);
+        probabilities(c, s0);
+        tmem_ld_wait();
+        if (c == 0) tmem_ld32(s_at + 64, s0);
+        probabilities(c + 1, s1);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -402,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     const int chunk = lane % C::kChunks, octet = lane / C::kChunks;
     const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
     const uint32_t base = smem_u32(smem);
+    const uint32_t raw = base + C::kRawAt + (warp - kFirstConverter) * 4096 + lane * 16;  // this lane's codes
     // unit u: step s = u / kSteps converts key tile s and value tile s - 1
     const int units = (n + 1) * kSteps;
     struct Place {
@@ -446,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         x.valid[i] = __ballot_sync(~0u, ok);
         row[i] = ok ? ((int64_t)page[i] * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
       }
-      const uint8_t *codes = q.value ? p.vc : p.kc;
+      const uint8_t *codes = (q.value ? p.vc : p.kc) + chunk * 16;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int t = octet * 8 + i;
@@ -457,20 +494,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           if (t >= 32) at = other, valid = x.valid[1];
         }
         const bool ok = (valid >> (t & 31)) & 1;
-        x.code[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(codes + at * D) + chunk) : make_uint4(0, 0, 0, 0);
-        const uint16_t *sc = q.value ? p.vs + at : p.ks + at * (D / 32) + chunk / 2;
-        const uint32_t s = ok ? __ldg(sc) : 0u;
-        if (i % 2 == 0) x.scale[i / 2] = s;
-        else x.scale[i / 2] |= s << 16;
+        cp_async16(raw + i * 512, codes + at * D, !ok);  // where it is not there: zeros
       }
-    };
-    const auto scale_of = [](const Unit<D> &x, int i) {
-      return __half2float(__ushort_as_half((uint16_t)(x.scale[i / 2] >> (16 * (i & 1)))));
+      x.scale[0] = x.scale[1] = 0;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if (!((x.valid[i] >> lane) & 1)) continue;
+        if (q.value) {
+          x.scale[i] = __ldg(p.vs + row[i]);
+        } else if constexpr (kWords == 1) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.ks + row[0] * (D / 32)));
+          x.scale[0] = w.x, x.scale[1] = w.y;
+        } else {
+          x.scale[i] = __ldg(reinterpret_cast<const uint32_t *>(p.ks + row[i] * (D / 32)));
+        }
+      }
     };
     // exponent e of a scale, 2^e <= |s| < 2^(e+1); those that are not finite count as the largest
     const auto exponent = [](uint32_t abs_bits) { return min((int)(abs_bits >> 23) - 127, 15); };
 
-    Unit<D> x, y;
+    Unit<D> x;
     int page[kWords];
     int u = warp - kFirstConverter;
     if (!place(u).real) u = following(u);
@@ -481,6 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     bool ok = true;
     while (u < units) {
       const Place q = place(u);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      uint4 code[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) code[i] = lds128(raw + i * 512);
+      Unit<D> y;
       load(next, page, y);
       const int after = next < units ? following(next) : units;
       lookup(after, page);
@@ -489,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       // exponents of the unit's largest and smallest scale (zeros apart)
       unsigned top = 0x33800000u, low = 0x7F800000u;  // 2^-24, float16's smallest
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const unsigned a = __float_as_uint(fabsf(scale_of(x, i)));
+      for (int i = 0; i < 4; ++i) {
+        const unsigned a = __float_as_uint(fabsf(half_at(x.scale[i / 2], i % 2)));
         top = max(top, a);
         low = a ? min(low, a) : low;
       }
@@ -504,10 +552,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           tm.valid[q.block * kWords + lane] = lane == 0 ? x.valid[0] : x.valid[kWords - 1];
         }
         const uint32_t dst = base + C::kKAt + (q.tile & 1) * C::kTileBytes + (chunk / 4) * C::kSub;
+        uint32_t sw[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) sw[i] = half2_of(half_at(x.scale[i], 0) * down, half_at(x.scale[i], 1) * down);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const __half2 sc = __float2half2_rn(scale_of(x, i) * down);
-          const uint32_t c[4] = {x.code[i].x, x.code[i].y, x.code[i].z, x.code[i].w};
+          const int t = octet * 8 + i;
+          const uint32_t w0 = __shfl_sync(~0u, sw[0], t & 31), w1 = __shfl_sync(~0u, sw[1], t & 31);
+          const uint32_t w = (kWords == 1 ? chunk >= 4 : t >= 32) ? w1 : w0;
+          const __half2 sc = bits_half2(__byte_perm(w, w, chunk & 2 ? 0x3232 : 0x1010));
+          const uint32_t c[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
           uint32_t o[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -534,22 +588,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           // finite become zeros, which P = 0 leaves alone; rows that do see one get
           // their NaN from P
 #pragma unroll
+          for (int i = 0; i < kWords; ++i) poison[i] = __ballot_sync(~0u, (x.scale[i] & 0x7FFFu) >= 0x7C00u);
+#pragma unroll
           for (int i = 0; i < 8; ++i) {
-            uint32_t bad = __vcmpeq4(x.code[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                           __vcmpeq4(x.code[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                           __vcmpeq4(x.code[i].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                           __vcmpeq4(x.code[i].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            const uint32_t s = (x.scale[i / 2] >> (16 * (i & 1))) & 0x7FFFu;
-            const unsigned who = __ballot_sync(~0u, bad != 0 || s >= 0x7C00u);
-            const unsigned mine = (who >> (octet * C::kChunks)) & ((1u << C::kChunks) - 1);
-            if (mine) {
-              x.code[i] = make_uint4(0, 0, 0, 0);
-              x.scale[i / 2] &= (i & 1) ? 0xFFFFu : 0xFFFF0000u;
-            }
+            const uint32_t bad = __vcmpeq4(code[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                                 __vcmpeq4(code[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                                 __vcmpeq4(code[i].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                                 __vcmpeq4(code[i].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            const unsigned who = __ballot_sync(~0u, bad != 0);
+            if ((who >> (octet * C::kChunks)) & ((1u << C::kChunks) - 1)) code[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int o = 0; o < 32 / C::kChunks; ++o)
               if ((who >> (o * C::kChunks)) & ((1u << C::kChunks) - 1)) poison[o / 4] |= 1u << ((o % 4) * 8 + i);
           }
+#pragma unroll
+          for (int i = 0; i < kWords; ++i)
+            if ((poison[i] >> lane) & 1) x.scale[i] = 0;
         }
         // (e stands for the scales as loaded: one that is not finite only makes it the largest)
         if (lane < kWords) {
@@ -557,23 +611,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           tm.poison[q.block * kWords + lane] = lane == 0 ? poison[0] : poison[kWords - 1];
           tm.wide[q.block * kWords + lane] = wide;
         }
-        // the octet's scales, two positions at a time
+        // scales as float16, the octet's then two positions at a time
+        uint32_t sw[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const float s = half_at(x.scale[i], 0);
+          int es = e;
+          if (wide) {
+            const unsigned a = __float_as_uint(fabsf(s));
+            es = a ? exponent(a) : e;
+            tm.pos_ev[q.block * C::kUnit + i * 32 + lane] = (float)(es - kValueUp);
+          }
+          const uint32_t w = __half_as_ushort(__float2half_rn(s * pow2i(kValueUp - es)));
+          sw[i] = w | (__shfl_down_sync(~0u, w, 1) << 16);
+        }
         __half2 sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float s0 = scale_of(x, 2 * i), s1 = scale_of(x, 2 * i + 1);
-          int e0 = e, e1 = e;
-          if (wide) {
-            const unsigned a0 = __float_as_uint(fabsf(s0)), a1 = __float_as_uint(fabsf(s1));
-            e0 = a0 ? exponent(a0) : e;
-            e1 = a1 ? exponent(a1) : e;
-            if (chunk == 0) {
-              float *pos = tm.pos_ev + q.block * C::kUnit + octet * 8 + 2 * i;
-              pos[0] = (float)(e0 - kValueUp);
-              pos[1] = (float)(e1 - kValueUp);
-            }
+          const int t = octet * 8 + 2 * i;
+          uint32_t w = __shfl_sync(~0u, sw[0], t & 31);
+          if constexpr (kWords == 2) {
+            const uint32_t other = __shfl_sync(~0u, sw[1], t & 31);
+            if (t >= 32) w = other;
           }
-          sc[i] = __floats2half2_rn(s0 * pow2i(kValueUp - e0), s1 * pow2i(kValueUp - e1));
+          sc[i] = bits_half2(w);
         }
         ok = mbar_wait(&sh.v_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
         if (!__all_sync(~0u, ok)) break;
@@ -595,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           uint32_t lo8[8], hi8[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t c0 = w ? x.code[i].z : x.code[i].x, c1 = w ? x.code[i].w : x.code[i].y;
+            const uint32_t c0 = w ? code[i].z : code[i].x, c1 = w ? code[i].w : code[i].y;
             lo8[i] = __byte_perm(c0, c1, sel0);
             hi8[i] = __byte_perm(c0, c1, sel1);
           }
