@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
-           mbar_wait(&sh.s_full[half], j & 1, abort_flag);
+      ok = mbar_wait_asleep(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
+           mbar_wait_asleep(&sh.s_full[half], j & 1, abort_flag);
       if (!__all_sync(~0u, ok)) break;
       tc_fence_after();
       const TileMeta &tm = sh.meta[j % kMetaSlots];
@@ -243,107 +243,108 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         }
       };
       // a score's factor (never 0, so that -inf stays -inf)
-      const auto factor = [&](int c) { return fmaxf(row_factor * pow2i(tm.ek[c]), 0x1p-100f); };
+      const auto factor = [&](int ek) { return fmaxf(row_factor * pow2i(ek), 0x1p-100f); };
 
-      // first pass: the row's largest exponent
-      float now = m;
+      // 64 columns at a time: S into registers, the row's largest exponent, then
+      // P = 2^(s + ev - m + bias) over columns that were read
 #pragma unroll 1
       for (int c = 0; c < 4; c += 2) {
         uint32_t s0[32], s1[32];
         tmem_ld32(s_at + c * 32, s0);
         tmem_ld32(s_at + c * 32 + 32, s1);
+        const float f0 = factor(tm.ek[c]), f1 = factor(tm.ek[c + 1]);
+        const int v0 = tm.ev[c], v1 = tm.ev[c + 1];
+        const unsigned w0 = tm.wide[c], w1 = tm.wide[c + 1];
         tmem_ld_wait();
-        if (!full) {
+        if (__builtin_expect(!full, 0)) {
           mask(c, s0);
           mask(c + 1, s1);
         }
         float m0 = -INFINITY, m1 = -INFINITY;
-        if ((tm.wide[c] | tm.wide[c + 1]) == 0) {
+        if (__builtin_expect((w0 | w1) == 0, 1)) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             m0 = fmaxf(m0, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])));
             m1 = fmaxf(m1, fmaxf(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])));
           }
-          m0 = fmaf(m0, factor(c), (float)tm.ev[c]);
-          m1 = fmaf(m1, factor(c + 1), (float)tm.ev[c + 1]);
+          m0 = fmaf(m0, f0, (float)v0);
+          m1 = fmaf(m1, f1, (float)v1);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float e0 = tm.wide[c] ? tm.pos_ev[c * 32 + i] : (float)tm.ev[c];
-            const float e1 = tm.wide[c + 1] ? tm.pos_ev[c * 32 + 32 + i] : (float)tm.ev[c + 1];
-            m0 = fmaxf(m0, fmaf(__uint_as_float(s0[i]), factor(c), e0));
-            m1 = fmaxf(m1, fmaf(__uint_as_float(s1[i]), factor(c + 1), e1));
+            m0 = fmaxf(m0, fmaf(__uint_as_float(s0[i]), f0, w0 ? tm.pos_ev[c * 32 + i] : (float)v0));
+            m1 = fmaxf(m1, fmaf(__uint_as_float(s1[i]), f1, w1 ? tm.pos_ev[c * 32 + 32 + i] : (float)v1));
           }
         }
-        now = fmaxf(now, fmaxf(m0, m1));
-      }
-      if (__any_sync(~0u, now > m + kGrowth)) {
-        const float a = now > m + kGrowth ? exp2_approx(m - now) : 1.0f;
-        if (now > m + kGrowth) m = now;
-        if (j > 0) {
+        const float now = fmaxf(m, fmaxf(m0, m1));
+        if (__any_sync(~0u, now > m + kGrowth)) {
+          // a new reference: what was summed under the old one is scaled down
+          const float a = now > m + kGrowth ? exp2_approx(m - now) : 1.0f;
+          if (now > m + kGrowth) m = now;
           l *= a;
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          if (c > 0) {  // P of the first 64 columns
             uint32_t o[32];
-            tmem_ld32(o_at + c * 32, o);
+            tmem_st_wait();
+            tmem_ld32(s_at, o);
             tmem_ld_wait();
+            const __half2 a2 = __float2half2_rn(a);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-            tmem_st32(o_at + c * 32, o);
+            for (int i = 0; i < 32; ++i) o[i] = half2_bits(__hmul2(bits_half2(o[i]), a2));
+            tmem_st32(s_at, o);
           }
-        }
-      }
-      // second pass: P = 2^(s + ev - m + bias), over S
-      const float z = kPBias - (m == -INFINITY ? 0.0f : m);
-      const auto probabilities = [&](int c, uint32_t (&s)[32]) {
-        if (!full) mask(c, s);
-        const float f = factor(c), g = (float)tm.ev[c] + z;
-        uint32_t o[16];
-        float sum;
-        if (!tm.wide[c]) {
-          const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
-          uint64_t sum2[2] = {0, 0};
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
-            const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
-            sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
-            o[i] = half2_of(a, e);
-          }
-          sum2[0] = f32x2_add(sum2[0], sum2[1]);
-          sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * pow2i(-tm.ev[c]);
-        } else {
-          // an exponent for each position; l counts P without it
-          sum = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float e0 = tm.pos_ev[c * 32 + 2 * i], e1 = tm.pos_ev[c * 32 + 2 * i + 1];
-            const float a = exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, e0 + z));
-            const float e = exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, e1 + z));
-            sum += a * pow2i(-(int)e0) + e * pow2i(-(int)e1);
-            o[i] = half2_of(a, e);
-          }
-        }
-        l += sum;
-        tmem_st16(s_at + c * 16, o);
-      };
-      uint32_t s0[32], s1[32];
-      tmem_ld32(s_at, s0);
+          if (j > 0) {
 #pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {  // the next 32 columns arrive during these
-        tmem_ld_wait();
-        tmem_ld32(s_at + c * 32 + 32, s1);
-        probabilities(c, s0);
-        tmem_ld_wait();
-        if (c == 0) tmem_ld32(s_at + 64, s0);
-        probabilities(c + 1, s1);
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t o[32];
+              tmem_ld32(o_at + k * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st32(o_at + k * 32, o);
+            }
+          }
+        }
+        const float z = kPBias - (m == -INFINITY ? 0.0f : m);
+        const auto probabilities = [&](int k, const uint32_t (&s)[32], float f, int ev, unsigned wide) {
+          uint32_t o[16];
+          float sum;
+          if (__builtin_expect(wide == 0, 1)) {
+            const float g = (float)ev + z;
+            const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
+              const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
+              sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
+              o[i] = half2_of(a, e);
+            }
+            sum2[0] = f32x2_add(sum2[0], sum2[1]);
+            sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * pow2i(-ev);
+          } else {
+            // an exponent for each position; l counts P without it
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float e0 = tm.pos_ev[k * 32 + 2 * i], e1 = tm.pos_ev[k * 32 + 2 * i + 1];
+              const float a = exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, e0 + z));
+              const float e = exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, e1 + z));
+              sum += a * pow2i(-(int)e0) + e * pow2i(-(int)e1);
+              o[i] = half2_of(a, e);
+            }
+          }
+          l += sum;
+          tmem_st16(s_at + k * 16, o);
+        };
+        probabilities(c, s0, f0, v0, w0);
+        probabilities(c + 1, s1, f1, v1, w1);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[half]);
     }
-    if (__all_sync(~0u, ok)) ok = mbar_wait(&sh.o_full[half], 0, abort_flag);
+    if (__all_sync(~0u, ok)) ok = mbar_wait_asleep(&sh.o_full[half], 0, abort_flag);
     if (__all_sync(~0u, ok)) {
       tc_fence_after();
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           mma_f16_ts(tmem + C::kO + half * D, tmem + C::kS + half * kPos + k * 8,
                      bd + (uint64_t)((k / 4) * (C::kVSub >> 4) + (k % 4) * 2), C::kIdescO, j > 0 || k > 0);
       };
-      bool ok = mbar_wait(&sh.k_full[0], 0, abort_flag);
+      bool ok = mbar_wait_asleep(&sh.k_full[0], 0, abort_flag);
       if (ok) {
         tc_fence_after();
         scores(0, 0);
@@ -397,19 +398,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         mma_commit(&sh.k_empty[0]);
       }
       for (int j = 0; j < n && ok; ++j) {
-        ok = mbar_wait(&sh.v_full[j & 1], (j >> 1) & 1, abort_flag) && mbar_wait(&sh.p_full[0], j & 1, abort_flag);
+        ok = mbar_wait_asleep(&sh.v_full[j & 1], (j >> 1) & 1, abort_flag) && mbar_wait_asleep(&sh.p_full[0], j & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         outputs(0, j);
         if (j + 1 < n) {
-          ok = mbar_wait(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag);
+          ok = mbar_wait_asleep(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           scores(0, j + 1);
         } else {
           mma_commit(&sh.o_full[0]);
         }
-        ok = mbar_wait(&sh.p_full[1], j & 1, abort_flag);
+        ok = mbar_wait_asleep(&sh.p_full[1], j & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         outputs(1, j);
@@ -439,25 +440,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
     const uint32_t base = smem_u32(smem);
     const uint32_t raw = base + C::kRawAt + (warp - kFirstConverter) * 4096 + lane * 16;  // this lane's codes
-    // unit u: step s = u / kSteps converts key tile s and value tile s - 1
-    const int units = (n + 1) * kSteps;
+    // units in the order they are needed: a tile's keys, then its values
+    const int units = n * kSteps;
     struct Place {
       int tile, block;  // position tile, unit within it
-      bool value, real;
+      bool value;
     };
     const auto place = [&](int u) {
-      const int s = u / kSteps, k = u % kSteps;
       Place q;
-      q.value = k >= C::kUnits;
-      q.block = q.value ? k - C::kUnits : k;
-      q.tile = q.value ? s - 1 : s;
-      q.real = u < units && q.tile >= 0 && q.tile < n;
+      q.tile = u / kSteps;
+      q.block = u % kSteps;
+      q.value = q.block >= C::kUnits;
+      if (q.value) q.block -= C::kUnits;
       return q;
-    };
-    const auto following = [&](int u) {  // the warp's next unit after u that exists
-      do u += C::kConverters;
-      while (u < units && !place(u).real);
-      return u;
     };
     // pages of the lane's positions of unit u (-1: none)
     const auto lookup = [&](int u, int (&page)[kWords]) {
@@ -471,6 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         if (j >= lo && j < end) page[i] = __ldg(table + block_of(p, j));
       }
     };
+    // pages of a multiple of 32 positions: 32 positions from a multiple of 32 on are
+    // rows at one distance, so that their addresses need no exchange between lanes
+    const bool even_pages = p.block_size % 32 == 0;
+    const int64_t row_bytes = (int64_t)p.H * D;
     const auto load = [&](int u, const int (&page)[kWords], Unit<D> &x) {
       if (u >= units) return;
       const Place q = place(u);
@@ -479,22 +478,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       for (int i = 0; i < kWords; ++i) {
         const int j = beg + q.tile * kPos + q.block * C::kUnit + i * 32 + lane;
         const bool wanted = j >= lo && j < end, ok = wanted && page[i] >= 0 && page[i] < p.num_blocks;
-        if (wanted && !ok) set_status(p.status, QLIN_ERR_INVALID_ARG);
+        if (__builtin_expect(wanted && !ok, 0)) set_status(p.status, QLIN_ERR_INVALID_ARG);
         x.valid[i] = __ballot_sync(~0u, ok);
         row[i] = ok ? ((int64_t)page[i] * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
       }
       const uint8_t *codes = (q.value ? p.vc : p.kc) + chunk * 16;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = octet * 8 + i;
-        int64_t at = __shfl_sync(~0u, row[0], t & 31);
-        unsigned valid = x.valid[0];
+      if (__builtin_expect(even_pages && (x.valid[0] & x.valid[kWords - 1]) == ~0u, 1)) {
+        // the octet's first row, then one row after the other
+        int64_t at = __shfl_sync(~0u, row[0], (octet * 8) & 31);
         if constexpr (kWords == 2) {
-          const int64_t other = __shfl_sync(~0u, row[1], t & 31);
-          if (t >= 32) at = other, valid = x.valid[1];
+          const int64_t other = __shfl_sync(~0u, row[1], (octet * 8) & 31);
+          if (octet >= 4) at = other;
         }
-        const bool ok = (valid >> (t & 31)) & 1;
-        cp_async16(raw + i * 512, codes + at * D, !ok);  // where it is not there: zeros
+        const uint8_t *src = codes + at * D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cp_async16(raw + i * 512, src + i * row_bytes, false);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int t = octet * 8 + i;
+          int64_t at = __shfl_sync(~0u, row[0], t & 31);
+          unsigned valid = x.valid[0];
+          if constexpr (kWords == 2) {
+            const int64_t other = __shfl_sync(~0u, row[1], t & 31);
+            if (t >= 32) at = other, valid = x.valid[1];
+          }
+          cp_async16(raw + i * 512, codes + at * D, !((valid >> (t & 31)) & 1));  // not there: zeros
+        }
       }
       x.scale[0] = x.scale[1] = 0;
 #pragma unroll
@@ -516,11 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     Unit<D> x;
     int page[kWords];
     int u = warp - kFirstConverter;
-    if (!place(u).real) u = following(u);
     lookup(u, page);
     load(u, page, x);
-    int next = u < units ? following(u) : units;
-    lookup(next, page);
+    lookup(u + C::kConverters, page);
     bool ok = true;
     while (u < units) {
       const Place q = place(u);
@@ -529,9 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
 #pragma unroll
       for (int i = 0; i < 8; ++i) code[i] = lds128(raw + i * 512);
       Unit<D> y;
-      load(next, page, y);
-      const int after = next < units ? following(next) : units;
-      lookup(after, page);
+      load(u + C::kConverters, page, y);
+      lookup(u + 2 * C::kConverters, page);
       TileMeta &tm = sh.meta[q.tile % kMetaSlots];
       const int j0 = beg + q.tile * kPos;
       // exponents of the unit's largest and smallest scale (zeros apart)
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       const int e = exponent(__reduce_max_sync(~0u, top));
       if (!q.value) {
         const float down = pow2i(-e);
-        ok = mbar_wait(&sh.k_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
+        ok = mbar_wait_asleep(&sh.k_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
         if (!__all_sync(~0u, ok)) break;
         if (lane < kWords) {
           tm.ek[q.block * kWords + lane] = e;
@@ -582,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         unsigned poison[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i) poison[i] = 0;
-        if (!(j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
-              (x.valid[0] & x.valid[kWords - 1]) == ~0u)) {
+        if (__builtin_expect(!(j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
+                               (x.valid[0] & x.valid[kWords - 1]) == ~0u), 0)) {
           // positions that some row does not see: NaN codes and scales that are not
           // finite become zeros, which P = 0 leaves alone; rows that do see one get
           // their NaN from P
@@ -636,7 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           }
           sc[i] = bits_half2(w);
         }
-        ok = mbar_wait(&sh.v_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meta_full[q.tile % kMetaSlots]);  // the softmax waits for no values
+        ok = mbar_wait_asleep(&sh.v_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
         if (!__all_sync(~0u, ok)) break;
         const int first = q.block * C::kUnit + octet * 8;  // position within the tile
         const uint32_t dst = base + C::kVAt + (q.tile & 1) * C::kTileBytes + (first / 64) * C::kVSub;
@@ -677,11 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sh.meta_full[q.tile % kMetaSlots]);
+        if (!q.value) mbar_arrive(&sh.meta_full[q.tile % kMetaSlots]);
         mbar_arrive(q.value ? &sh.v_full[q.tile & 1] : &sh.k_full[q.tile & 1]);
       }
-      u = next;
-      next = after;
+      u += C::kConverters;
       x = y;
     }
     if (!ok) *abort_flag = 1;
