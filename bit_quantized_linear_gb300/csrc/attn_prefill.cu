@@ -562,27 +562,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         uint32_t sw[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) sw[i] = half2_of(half_at(x.scale[i], 0) * down, half_at(x.scale[i], 1) * down);
+        const int row0 = q.block * C::kUnit + octet * 8, unit = (chunk % 4) * 2;
+        // lanes of the second column store their upper half first: no two of a row's
+        // lanes meet in a bank
+        const uint32_t second = ((lane >> 2) & 1) << 4;
+        // (two rows of code, walked over four times: straight-line code for eight rows
+        // costs more in instruction fetches than the moves)
+#pragma unroll 1
+        for (int i = 0; i < 8; i += 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int t = octet * 8 + i;
-          const uint32_t w0 = __shfl_sync(~0u, sw[0], t & 31), w1 = __shfl_sync(~0u, sw[1], t & 31);
-          const uint32_t w = (kWords == 1 ? chunk >= 4 : t >= 32) ? w1 : w0;
-          const __half2 sc = bits_half2(__byte_perm(w, w, chunk & 2 ? 0x3232 : 0x1010));
-          const uint32_t c[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-          uint32_t o[8];
+          for (int v = 0; v < 2; ++v) {
+            const int t = octet * 8 + i + v;
+            const uint32_t w0 = __shfl_sync(~0u, sw[0], t & 31), w1 = __shfl_sync(~0u, sw[1], t & 31);
+            const uint32_t w = (kWords == 1 ? chunk >= 4 : t >= 32) ? w1 : w0;
+            const __half2 sc = bits_half2(__byte_perm(w, w, chunk & 2 ? 0x3232 : 0x1010));
+            const uint32_t c[4] = {code[v].x, code[v].y, code[v].z, code[v].w};
+            uint32_t o[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            int8x4_to_half(c[k], o[2 * k], o[2 * k + 1]);
-            o[2 * k] = half2_bits(__hmul2(bits_half2(o[2 * k]), sc));
-            o[2 * k + 1] = half2_bits(__hmul2(bits_half2(o[2 * k + 1]), sc));
+            for (int k = 0; k < 4; ++k) {
+              int8x4_to_half(c[k], o[2 * k], o[2 * k + 1]);
+              o[2 * k] = half2_bits(__hmul2(bits_half2(o[2 * k]), sc));
+              o[2 * k + 1] = half2_bits(__hmul2(bits_half2(o[2 * k + 1]), sc));
+            }
+            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), z = make_uint4(o[4], o[5], o[6], o[7]);
+            const uint32_t at = dst + swizzled(row0 + i + v, unit);
+            sts128(at ^ second, second ? z : a);
+            sts128(at ^ second ^ 16, second ? a : z);
           }
-          const int row = q.block * C::kUnit + octet * 8 + i, unit = (chunk % 4) * 2;
-          const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), z = make_uint4(o[4], o[5], o[6], o[7]);
-          // lanes of the second column store their upper half first: no two of a row's
-          // lanes meet in a bank
-          const bool second = (lane >> 2) & 1;
-          sts128(dst + swizzled(row, unit + (second ? 1 : 0)), second ? z : a);
-          sts128(dst + swizzled(row, unit + (second ? 0 : 1)), second ? a : z);
+#pragma unroll
+          for (int k = 0; k < 6; ++k) code[k] = code[k + 2];
         }
       } else {
         const bool wide = e - min(exponent(__reduce_min_sync(~0u, low)), e) > kValueSpan;
@@ -660,15 +668,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           sel0 |= ((k + turn) & 7) << (4 * k);
           sel1 |= ((k + 4 + turn) & 7) << (4 * k);
         }
-#pragma unroll
+#pragma unroll 1
         for (int w = 0; w < 2; ++w) {
           uint32_t lo8[8], hi8[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t c0 = w ? code[i].z : code[i].x, c1 = w ? code[i].w : code[i].y;
-            lo8[i] = __byte_perm(c0, c1, sel0);
-            hi8[i] = __byte_perm(c0, c1, sel1);
+            lo8[i] = __byte_perm(code[i].x, code[i].y, sel0);
+            hi8[i] = __byte_perm(code[i].x, code[i].y, sel1);
+            code[i].x = code[i].z, code[i].y = code[i].w;
           }
+          const int d0 = chunk * 16 + w * 8;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {  // byte k of the turned eight: dimension (k + turn) % 8
             uint32_t o[4];
@@ -678,8 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
               const uint32_t two = __byte_perm(s0, s1, (k & 3) | ((4 + (k & 3)) << 4));
               o[i] = half2_bits(__hmul2(bits_half2(e4m3x2_to_half((uint16_t)two)), sc[i]));
             }
-            const int d = chunk * 16 + w * 8 + ((k + turn) & 7);
-            sts128(dst + swizzled(d, unit), make_uint4(o[0], o[1], o[2], o[3]));
+            sts128(dst + swizzled(d0 + ((k + turn) & 7), unit), make_uint4(o[0], o[1], o[2], o[3]));
           }
         }
       }
