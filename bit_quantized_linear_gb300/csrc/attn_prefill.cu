@@ -1,25 +1,31 @@
 // Attention over the mixed 8-bit KV cache for many rows (prefill, chunks): bound
 // by the tensor cores, 4 D flops for each (row, position).
 //
-// A CTA takes 256 rows of one (sequence, kv head), packed token-major over the
-// heads of the group, as two row tiles A and B of 128, and walks over the
-// positions 128 at a time.  Both tiles use each key and value tile, so the codes
-// are converted to float16 once for 256 rows.  Roles:
+// k_attn_unpack converts the positions that some row sees to float16 once, into
+// the workspace, as the very images of shared memory that the products read: per
+// 128 positions a K-major key tile and a V^T tile (positions along the row), both
+// in the 128-byte swizzle, and what the softmax needs beside them.  (Converting
+// in the product kernel, by warps of its own, cost 2.3 times the time at 8192 x
+// 16384: every row tile converts the same codes again, and the two kinds of code
+// drive one another out of the instruction cache.)
+//
+// k_attn_prefill: a CTA takes 256 rows of one (sequence, kv head), packed
+// token-major over the heads of the group, as two row tiles A and B of 128, and
+// walks over the position tiles, each one contiguous bulk copy.  Roles:
 //   * warps 0-3 and 4-7: softmax of tile A and of tile B, a thread per row.  S
 //     comes from tensor memory, P goes back there (over S) as float16.
-//   * warps 8-14: converters.  A unit is 4 KB of key or value codes; while a warp
-//     converts one, cp.async brings the next one's codes to the same lanes.  Keys become
-//     K-major float16 rows, values are transposed to V^T (positions along the
-//     row), both in the 128-byte swizzle the MMA reads.
-//   * warp 15: issues S = Q K^T (both from shared memory) and O += P V (P from
-//     tensor memory).  While one tile's softmax runs, the other's products do.
+//   * warp 8: copies; warp 9: issues S = Q K^T (both from shared memory) and
+//     O += P V (P from tensor memory).  While one tile's softmax runs, the other's
+//     products do.
 //
-// Scaling.  q rows are scaled by powers of two to use float16's range.  A unit's
-// keys are scaled by code scale * 2^-ek and its values by 2^-ev, with one exponent
-// each for the unit's positions, so float16 holds them whatever the cache's
-// scales; 2^ek joins the score's factor and ev the exponent, so that neither
-// costs the softmax an instruction per score.  O is rescaled only where a row's
-// maximum grew by more than 2^6 since its reference; P stays below 2^14.
+// Scaling.  q rows are scaled by powers of two to use float16's range.  The keys
+// of 32 (D 128) or 64 (D 64) positions, a unit, are scaled by code scale * 2^-ek
+// and the values by 2^-ev, with one exponent each for the unit (where its value
+// scales lie too far apart for float16, one for each position), so float16 holds
+// them whatever the cache's scales; 2^ek joins the score's factor and ev the
+// exponent, so that neither costs the softmax an instruction per score.  O is
+// rescaled only where a row's maximum grew by more than 2^6 since its reference;
+// P stays below 2^14.
 #include <algorithm>
 
 #include "attn.cuh"
@@ -35,9 +41,9 @@ using namespace tc;
 
 constexpr int kPos = 128;       // positions of a tile
 constexpr int kRowTile = 128;   // rows of an MMA
-constexpr int kThreads = 512;
-constexpr int kIssuer = 15;     // the MMA warp
-constexpr int kFirstConverter = 8;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kCopier = 8, kIssuer = 9;
+constexpr int kThreads = 320;
 constexpr int kMetaSlots = 4;
 constexpr float kPBias = 8.0f;  // P is 2^8 p: float16's subnormals lie below 2^-22 p
 constexpr float kGrowth = 6.0f;
@@ -45,9 +51,10 @@ constexpr int kValueUp = 5;     // a value's scale becomes 2^5..2^6 (times at mo
 constexpr int kValueSpan = 8;   // scales of a unit within 2^8 share an exponent: E4M3's 2^-9 stays normal
 
 // What the softmax needs of a position tile beside S, per 32 positions: the
-// exponents of keys and values, positions present, positions with a NaN value, and
+// exponents of keys and values, positions present, positions whose value is not
+// finite (zero in the tile, so that P = 0 leaves it alone), and
 // whether the values have an exponent for each position instead (pos_ev).
-struct TileMeta {
+struct __align__(16) TileMeta {
   int ek[4], ev[4];
   unsigned valid[4], poison[4], wide[4];
   float pos_ev[kPos];
@@ -58,16 +65,13 @@ struct Config {
   static constexpr int kChunks = D / 16;             // 16-byte pieces of a row of codes
   static constexpr int kUnit = 256 / kChunks;        // positions of a unit (4 KB of codes)
   static constexpr int kUnits = kPos / kUnit;        // units of a key (or value) tile
-  // Each converter's previous unit lies at most one step back, so a barrier it
-  // waits for is never two phases behind.
-  static constexpr int kConverters = 2 * kUnits < 7 ? 2 * kUnits : 7;
   static constexpr int kQBytes = kRowTile * D * 2;   // a row tile of q
   static constexpr int kTileBytes = kPos * D * 2;    // a key or value tile
   static constexpr int kSub = kRowTile * 128;        // a 128-byte-wide column of a q or key tile
   static constexpr int kVSub = D * 128;              // 64 positions of V^T
   static constexpr int kKAt = 2 * kQBytes, kVAt = kKAt + 2 * kTileBytes, kBarAt = kVAt + 2 * kTileBytes;
-  static constexpr int kRawAt = kBarAt + 4096;       // barriers and metadata before; 4 KB for each converter
-  static constexpr int kSmem = kRawAt + kConverters * 4096 + 1024;  // 1024: alignment
+  static constexpr int kSmem = kBarAt + 4096 + 1024;  // barriers and metadata; alignment
+  static constexpr int kImage = 2 * kTileBytes;       // a position tile in the workspace
   static_assert(kSmem <= 232448, "shared memory of a CTA");
   // tensor memory columns: S (P over it) of A and B, then O
   static constexpr int kS = 0, kO = 2 * kPos, kColumns = 512;
@@ -100,22 +104,196 @@ __device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float((
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
 struct PrefillParams : AttnDev {
-  int row_tiles;
+  int row_tiles, tiles;      // row tiles and position tiles of a sequence
+  int head0, heads;          // kv heads of this pass
+  uint8_t *images;           // [B, heads, tiles] key and value tile
+  TileMeta *meta;            // [B, heads, tiles]
 };
 
-// What a converter's lane holds of one unit beside its codes: the scales of the
-// positions lane (and lane + 32) as they are in the cache, and which positions are
-// there.
-template <int D>
-struct Unit {
-  uint32_t scale[2];
-  unsigned valid[Config<D>::kUnit / 32];
-};
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 0 : 16) : "memory");
-}
 __device__ __forceinline__ float half_at(uint32_t w, int i) {
   return __half2float(__ushort_as_half((uint16_t)(w >> (16 * i))));
+}
+
+// One position tile of one (sequence, kv head): a warp for each unit of keys and
+// of values.  A lane holds the codes of 16 dimensions (chunk lane % C) of positions
+// 8 * (lane / C) + i.
+template <int D>
+__global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const PrefillParams p) {
+  using C = Config<D>;
+  constexpr int kWords = C::kUnit / 32;  // 32-position words of a unit
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = (int)(blockIdx.x % p.tiles);
+  const int hh = (int)(blockIdx.x / p.tiles % p.heads), b = (int)(blockIdx.x / p.tiles / p.heads);
+  const int h = p.head0 + hh;
+  pdl_wait();
+  pdl_trigger();
+  const Sequence sq = sequence(p, b);
+  if (sq.kept * p.G <= p.few_rows || sq.kept == 0) return;
+  int lo, hi, unused;  // positions that some row sees
+  sees(p, sq, 0, lo, unused);
+  sees(p, sq, sq.kept - 1, unused, hi);
+  if ((tile + 1) * kPos <= lo || tile * kPos >= hi) return;
+
+  const bool value = warp >= C::kUnits;
+  const int block = value ? warp - C::kUnits : warp;
+  const int chunk = lane % C::kChunks, octet = lane / C::kChunks;
+  const int64_t at_tile = ((int64_t)b * p.heads + hh) * p.tiles + tile;
+  uint8_t *image = p.images + at_tile * C::kImage + (value ? C::kTileBytes : 0);
+  TileMeta &tm = p.meta[at_tile];
+
+  // rows (slot, head) of the lane's positions, and which are there
+  const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
+  int64_t row[kWords];
+  unsigned valid[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const int j = tile * kPos + block * C::kUnit + i * 32 + lane, blk = block_of(p, j);
+    const bool wanted = j >= lo && j < hi;
+    const int page = wanted ? __ldg(table + blk) : -1;
+    const bool ok = page >= 0 && page < p.num_blocks;
+    if (wanted && !ok) set_status(p.status, QLIN_ERR_INVALID_ARG);
+    valid[i] = __ballot_sync(~0u, ok);
+    row[i] = ok ? ((int64_t)page * p.block_size + (j - blk * p.block_size)) * p.H + h : 0;
+  }
+  const uint8_t *codes = (value ? p.vc : p.kc) + chunk * 16;
+  uint4 code[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int t = octet * 8 + i;
+    int64_t at = __shfl_sync(~0u, row[0], t & 31);
+    unsigned there = valid[0];
+    if constexpr (kWords == 2) {
+      const int64_t other = __shfl_sync(~0u, row[1], t & 31);
+      if (t >= 32) at = other, there = valid[1];
+    }
+    code[i] = (there >> (t & 31)) & 1 ? __ldg(reinterpret_cast<const uint4 *>(codes + at * D)) : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t scale[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    if (!((valid[i] >> lane) & 1)) continue;
+    if (value) {
+      scale[i] = __ldg(p.vs + row[i]);
+    } else if constexpr (kWords == 1) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.ks + row[0] * (D / 32)));
+      scale[0] = w.x, scale[1] = w.y;
+    } else {
+      scale[i] = __ldg(reinterpret_cast<const uint32_t *>(p.ks + row[i] * (D / 32)));
+    }
+  }
+  // exponent e of a scale, 2^e <= |s| < 2^(e+1); those that are not finite count as the largest
+  const auto exponent = [](uint32_t abs_bits) { return min((int)(abs_bits >> 23) - 127, 15); };
+  // of the unit's largest and smallest scale (zeros apart)
+  unsigned top = 0x33800000u, low = 0x7F800000u;  // 2^-24, float16's smallest
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned a = __float_as_uint(fabsf(half_at(scale[i / 2], i % 2)));
+    top = max(top, a);
+    low = a ? min(low, a) : low;
+  }
+  const int e = exponent(__reduce_max_sync(~0u, top));
+
+  if (!value) {
+    const float down = pow2i(-e);
+    if (lane < kWords) {
+      tm.ek[block * kWords + lane] = e;
+      tm.valid[block * kWords + lane] = lane == 0 ? valid[0] : valid[kWords - 1];
+    }
+    uint32_t sw[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sw[i] = half2_of(half_at(scale[i], 0) * down, half_at(scale[i], 1) * down);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = octet * 8 + i, r = block * C::kUnit + t;
+      const uint32_t w0 = __shfl_sync(~0u, sw[0], t & 31), w1 = __shfl_sync(~0u, sw[1], t & 31);
+      const uint32_t w = (kWords == 1 ? chunk >= 4 : t >= 32) ? w1 : w0;
+      const __half2 sc = bits_half2(__byte_perm(w, w, chunk & 2 ? 0x3232 : 0x1010));
+      const uint32_t c[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        int8x4_to_half(c[k], o[2 * k], o[2 * k + 1]);
+        o[2 * k] = half2_bits(__hmul2(bits_half2(o[2 * k]), sc));
+        o[2 * k + 1] = half2_bits(__hmul2(bits_half2(o[2 * k + 1]), sc));
+      }
+      uint8_t *dst = image + (chunk / 4) * C::kSub;
+      *reinterpret_cast<uint4 *>(dst + swizzled(r, (chunk % 4) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4 *>(dst + swizzled(r, (chunk % 4) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+    return;
+  }
+
+  const bool wide = e - min(exponent(__reduce_min_sync(~0u, low)), e) > kValueSpan;
+  // Values that are not finite: zeros in the tile, and a mark.
+  unsigned poison[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) poison[i] = __ballot_sync(~0u, (scale[i] & 0x7FFFu) >= 0x7C00u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t bad = __vcmpeq4(code[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                         __vcmpeq4(code[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                         __vcmpeq4(code[i].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                         __vcmpeq4(code[i].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    const unsigned who = __ballot_sync(~0u, bad != 0);
+    if (who == 0) continue;
+    if ((who >> (octet * C::kChunks)) & ((1u << C::kChunks) - 1)) code[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int o = 0; o < 32 / C::kChunks; ++o)
+      if ((who >> (o * C::kChunks)) & ((1u << C::kChunks) - 1)) poison[o / 4] |= 1u << ((o % 4) * 8 + i);
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    if ((poison[i] >> lane) & 1) scale[i] = 0;
+  // (e stands for the scales as loaded: one that is not finite only makes it the largest)
+  if (lane < kWords) {
+    tm.ev[block * kWords + lane] = e - kValueUp;
+    tm.poison[block * kWords + lane] = lane == 0 ? poison[0] : poison[kWords - 1];
+    tm.wide[block * kWords + lane] = wide;
+  }
+  // scales as float16, the octet's then two positions at a time
+  uint32_t sw[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const float s = half_at(scale[i], 0);
+    int es = e;
+    if (wide) {
+      const unsigned a = __float_as_uint(fabsf(s));
+      es = a ? exponent(a) : e;
+    }
+    tm.pos_ev[block * C::kUnit + i * 32 + lane] = (float)(es - kValueUp);
+    const uint32_t w = __half_as_ushort(__float2half_rn(s * pow2i(kValueUp - es)));
+    sw[i] = w | (__shfl_down_sync(~0u, w, 1) << 16);
+  }
+  __half2 sc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = octet * 8 + 2 * i;
+    uint32_t w = __shfl_sync(~0u, sw[0], t & 31);
+    if constexpr (kWords == 2) {
+      const uint32_t other = __shfl_sync(~0u, sw[1], t & 31);
+      if (t >= 32) w = other;
+    }
+    sc[i] = bits_half2(w);
+  }
+  const int first = block * C::kUnit + octet * 8;  // position within the tile
+  uint8_t *dst = image + (first / 64) * C::kVSub;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 &c0 = code[2 * i], &c1 = code[2 * i + 1];
+        const uint32_t s0 = w == 0 ? c0.x : w == 1 ? c0.y : w == 2 ? c0.z : c0.w;
+        const uint32_t s1 = w == 0 ? c1.x : w == 1 ? c1.y : w == 2 ? c1.z : c1.w;
+        const uint32_t two = __byte_perm(s0, s1, k | ((4 + k) << 4));
+        o[i] = half2_bits(__hmul2(bits_half2(e4m3x2_to_half((uint16_t)two)), sc[i]));
+      }
+      *reinterpret_cast<uint4 *>(dst + swizzled(chunk * 16 + w * 4 + k, first % 64 / 8)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
 }
 
 template <int D>
@@ -129,9 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // the last row tiles see the most positions: they go first
-  const int heads = p.B * p.H;
+  const int heads = p.B * p.heads;
   const int tile = p.row_tiles - 1 - (int)(blockIdx.x / heads);
-  const int b = (int)(blockIdx.x % heads) / p.H, h = (int)(blockIdx.x % heads) % p.H;
+  const int b = (int)(blockIdx.x % heads) / p.heads, h = p.head0 + (int)(blockIdx.x % heads) % p.heads;
   pdl_wait();
   pdl_trigger();
   const Sequence sq = sequence(p, b);
@@ -144,9 +322,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   const int last = min(r0 + 2 * kRowTile, R) - 1;
   sees(p, sq, r0 / p.G, beg, all_hi);
   sees(p, sq, last / p.G, all_lo, end);
-  const int lo = beg;
-  beg &= ~31;
-  const int n = end > beg ? (end - beg + kPos - 1) / kPos : 0;
+  const int lo = beg, tile0 = beg / kPos;
+  beg = tile0 * kPos;
+  const int n = end > lo ? (end - beg + kPos - 1) / kPos : 0;
 
   if (n == 0) {  // rows that see nothing
     for (int i = threadIdx.x; i < (last - r0 + 1) * (D / 8); i += kThreads) {
@@ -159,15 +337,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.k_full[i], C::kUnits);
+      mbar_init(&sh.k_full[i], 1);
       mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], C::kUnits);
+      mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.o_full[i], 1);
     }
-    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sh.meta_full[i], 2 * C::kUnits);
+    for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sh.meta_full[i], 1);
     sh.abort = 0;
     fence_barrier_init();
   }
@@ -176,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   // q rows -> float16 in shared memory, by the softmax threads
   float row_factor = 0.0f;
   const int r = r0 + threadIdx.x;  // a softmax thread's row
-  if (warp < kFirstConverter) {
+  if (warp < kSoftmaxWarps) {
     uint4 w[D / 8];
     float top = 0.0f;
     const uint16_t *src = p.q + (int64_t)(sq.first + r / p.G) * p.ldq + (int64_t)(h * p.G + r % p.G) * D;
@@ -209,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp < kFirstConverter) {
+  if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------- softmax
     const int half = warp >> 2;  // tile A or B
     const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // lanes 32 * (warp % 4)
@@ -219,14 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      ok = mbar_wait_asleep(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
-           mbar_wait_asleep(&sh.s_full[half], j & 1, abort_flag);
+      ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
+           mbar_wait(&sh.s_full[half], j & 1, abort_flag);
       if (!__all_sync(~0u, ok)) break;
       tc_fence_after();
       const TileMeta &tm = sh.meta[j % kMetaSlots];
       const int j0 = beg + j * kPos;
       const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
-                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u;
+                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
+                        (tm.poison[0] | tm.poison[1] | tm.poison[2] | tm.poison[3]) == 0;
       // Scores this row does not see become -inf, those of a NaN value NaN (32 columns
       // from c * 32 on).
       const auto mask = [&](int c, uint32_t (&s)[32]) {
@@ -245,65 +424,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       // a score's factor (never 0, so that -inf stays -inf)
       const auto factor = [&](int ek) { return fmaxf(row_factor * pow2i(ek), 0x1p-100f); };
 
-      // 64 columns at a time: S into registers, the row's largest exponent, then
-      // P = 2^(s + ev - m + bias) over columns that were read
-#pragma unroll 1
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t s0[32], s1[32];
-        tmem_ld32(s_at + c * 32, s0);
-        tmem_ld32(s_at + c * 32 + 32, s1);
-        const float f0 = factor(tm.ek[c]), f1 = factor(tm.ek[c + 1]);
-        const int v0 = tm.ev[c], v1 = tm.ev[c + 1];
-        const unsigned w0 = tm.wide[c], w1 = tm.wide[c + 1];
-        tmem_ld_wait();
-        if (__builtin_expect(!full, 0)) {
-          mask(c, s0);
-          mask(c + 1, s1);
-        }
-        float m0 = -INFINITY, m1 = -INFINITY;
-        if (__builtin_expect((w0 | w1) == 0, 1)) {
+      // S into registers and the row's largest exponent
+      uint32_t s[4][32];
+      float f[4];
+      int ev[4];
+      unsigned wide[4];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            m0 = fmaxf(m0, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])));
-            m1 = fmaxf(m1, fmaxf(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])));
-          }
-          m0 = fmaf(m0, f0, (float)v0);
-          m1 = fmaf(m1, f1, (float)v1);
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld32(s_at + c * 32, s[c]);
+        f[c] = factor(tm.ek[c]);
+        ev[c] = tm.ev[c];
+        wide[c] = tm.wide[c];
+      }
+      tmem_ld_wait();
+      if (__builtin_expect(!full, 0)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mask(c, s[c]);
+      }
+      float now = m;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float mx = -INFINITY;
+        if (__builtin_expect(wide[c] == 0, 1)) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            mx = fmaxf(mx, fmaxf(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])));
+          mx = fmaf(mx, f[c], (float)ev[c]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            m0 = fmaxf(m0, fmaf(__uint_as_float(s0[i]), f0, w0 ? tm.pos_ev[c * 32 + i] : (float)v0));
-            m1 = fmaxf(m1, fmaf(__uint_as_float(s1[i]), f1, w1 ? tm.pos_ev[c * 32 + 32 + i] : (float)v1));
-          }
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaf(__uint_as_float(s[c][i]), f[c], tm.pos_ev[c * 32 + i]));
         }
-        const float now = fmaxf(m, fmaxf(m0, m1));
-        if (__any_sync(~0u, now > m + kGrowth)) {
-          // a new reference: what was summed under the old one is scaled down
-          const float a = now > m + kGrowth ? exp2_approx(m - now) : 1.0f;
-          if (now > m + kGrowth) m = now;
-          l *= a;
-          if (c > 0) {  // P of the first 64 columns
-            uint32_t o[32];
-            tmem_st_wait();
-            tmem_ld32(s_at, o);
-            tmem_ld_wait();
-            const __half2 a2 = __float2half2_rn(a);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = half2_bits(__hmul2(bits_half2(o[i]), a2));
-            tmem_st32(s_at, o);
-          }
-          if (j > 0) {
+        now = fmaxf(now, mx);
+      }
+      if (__any_sync(~0u, now > m + kGrowth)) {
+        // a new reference: what was summed under the old one is scaled down
+        const float a = now > m + kGrowth ? exp2_approx(m - now) : 1.0f;
+        if (now > m + kGrowth) m = now;
+        l *= a;
+        if (j > 0) {
 #pragma unroll 1
-            for (int k = 0; k < D / 32; ++k) {
-              uint32_t o[32];
-              tmem_ld32(o_at + k * 32, o);
-              tmem_ld_wait();
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t o[16];
+            tmem_ld16(o_at + k * 16, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st32(o_at + k * 32, o);
-            }
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            tmem_st16(o_at + k * 16, o);
           }
         }
+      }
+      // P = 2^(s + ev - m + bias), over S
+      {
         const float z = kPBias - (m == -INFINITY ? 0.0f : m);
         const auto probabilities = [&](int k, const uint32_t (&s)[32], float f, int ev, unsigned wide) {
           uint32_t o[16];
@@ -336,15 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           l += sum;
           tmem_st16(s_at + k * 16, o);
         };
-        probabilities(c, s0, f0, v0, w0);
-        probabilities(c + 1, s1, f1, v1, w1);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) probabilities(c, s[c], f[c], ev[c], wide[c]);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_full[half]);
     }
-    if (__all_sync(~0u, ok)) ok = mbar_wait_asleep(&sh.o_full[half], 0, abort_flag);
+    if (__all_sync(~0u, ok)) ok = mbar_wait(&sh.o_full[half], 0, abort_flag);
     if (__all_sync(~0u, ok)) {
       tc_fence_after();
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -390,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           mma_f16_ts(tmem + C::kO + half * D, tmem + C::kS + half * kPos + k * 8,
                      bd + (uint64_t)((k / 4) * (C::kVSub >> 4) + (k % 4) * 2), C::kIdescO, j > 0 || k > 0);
       };
-      bool ok = mbar_wait_asleep(&sh.k_full[0], 0, abort_flag);
+      bool ok = mbar_wait(&sh.k_full[0], 0, abort_flag);
       if (ok) {
         tc_fence_after();
         scores(0, 0);
@@ -398,19 +569,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         mma_commit(&sh.k_empty[0]);
       }
       for (int j = 0; j < n && ok; ++j) {
-        ok = mbar_wait_asleep(&sh.v_full[j & 1], (j >> 1) & 1, abort_flag) && mbar_wait_asleep(&sh.p_full[0], j & 1, abort_flag);
+        ok = mbar_wait(&sh.v_full[j & 1], (j >> 1) & 1, abort_flag) && mbar_wait(&sh.p_full[0], j & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         outputs(0, j);
         if (j + 1 < n) {
-          ok = mbar_wait_asleep(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag);
+          ok = mbar_wait(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
           scores(0, j + 1);
         } else {
           mma_commit(&sh.o_full[0]);
         }
-        ok = mbar_wait_asleep(&sh.p_full[1], j & 1, abort_flag);
+        ok = mbar_wait(&sh.p_full[1], j & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         outputs(1, j);
@@ -432,275 +603,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       }
     }
     __syncwarp();
-  } else if (warp - kFirstConverter < C::kConverters) {
-    // ------------------------------------------------------------ converters
-    constexpr int kSteps = 2 * C::kUnits;
-    constexpr int kWords = C::kUnit / 32;  // 32-position words of a unit
-    const int chunk = lane % C::kChunks, octet = lane / C::kChunks;
-    const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
-    const uint32_t base = smem_u32(smem);
-    const uint32_t raw = base + C::kRawAt + (warp - kFirstConverter) * 4096 + lane * 16;  // this lane's codes
-    // units in the order they are needed: a tile's keys, then its values
-    const int units = n * kSteps;
-    struct Place {
-      int tile, block;  // position tile, unit within it
-      bool value;
-    };
-    const auto place = [&](int u) {
-      Place q;
-      q.tile = u / kSteps;
-      q.block = u % kSteps;
-      q.value = q.block >= C::kUnits;
-      if (q.value) q.block -= C::kUnits;
-      return q;
-    };
-    // pages of the lane's positions of unit u (-1: none)
-    const auto lookup = [&](int u, int (&page)[kWords]) {
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) page[i] = -1;
-      if (u >= units) return;
-      const Place q = place(u);
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const int j = beg + q.tile * kPos + q.block * C::kUnit + i * 32 + lane;
-        if (j >= lo && j < end) page[i] = __ldg(table + block_of(p, j));
+  } else if (warp == kCopier) {
+    // --------------------------------------------------------------- copies
+    if (lane == 0) {
+      const int64_t first = ((int64_t)b * p.heads + (h - p.head0)) * p.tiles + tile0;
+      const uint8_t *src = p.images + first * C::kImage;
+      bool ok = true;
+      int j = 0;
+      for (; j < n && ok; ++j) {
+        const int s = j & 1;
+        const uint32_t parity = ((j >> 1) & 1) ^ 1;
+        ok = mbar_wait(&sh.k_empty[s], parity, abort_flag);
+        if (!ok) break;
+        uint64_t *mb = &sh.meta_full[j % kMetaSlots];
+        mbar_arrive_expect_tx(mb, sizeof(TileMeta));
+        bulk_load(&sh.meta[j % kMetaSlots], p.meta + first + j, sizeof(TileMeta), mb);
+        mbar_arrive_expect_tx(&sh.k_full[s], C::kTileBytes);
+        bulk_load(smem + C::kKAt + s * C::kTileBytes, src + (int64_t)j * C::kImage, C::kTileBytes, &sh.k_full[s]);
+        ok = mbar_wait(&sh.v_empty[s], parity, abort_flag);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&sh.v_full[s], C::kTileBytes);
+        bulk_load(smem + C::kVAt + s * C::kTileBytes, src + (int64_t)j * C::kImage + C::kTileBytes, C::kTileBytes,
+                  &sh.v_full[s]);
       }
-    };
-    // pages of a multiple of 32 positions: 32 positions from a multiple of 32 on are
-    // rows at one distance, so that their addresses need no exchange between lanes
-    const bool even_pages = p.block_size % 32 == 0;
-    const int64_t row_bytes = (int64_t)p.H * D;
-    const auto load = [&](int u, const int (&page)[kWords], Unit<D> &x) {
-      if (u >= units) return;
-      const Place q = place(u);
-      int64_t row[kWords];  // (slot, head) row of the lane's positions
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const int j = beg + q.tile * kPos + q.block * C::kUnit + i * 32 + lane;
-        const bool wanted = j >= lo && j < end, ok = wanted && page[i] >= 0 && page[i] < p.num_blocks;
-        if (__builtin_expect(wanted && !ok, 0)) set_status(p.status, QLIN_ERR_INVALID_ARG);
-        x.valid[i] = __ballot_sync(~0u, ok);
-        row[i] = ok ? ((int64_t)page[i] * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
+      if (!ok) {  // what was started lands before the CTA leaves (tile j: keys and metadata at most)
+        *abort_flag = 1;
+        drain_ring(sh.meta_full, kMetaSlots, j + 1, kMetaSlots);
+        drain_ring(sh.k_full, 2, j + 1, 2);
+        drain_ring(sh.v_full, 2, j, 2);
       }
-      const uint8_t *codes = (q.value ? p.vc : p.kc) + chunk * 16;
-      if (__builtin_expect(even_pages && (x.valid[0] & x.valid[kWords - 1]) == ~0u, 1)) {
-        // the octet's first row, then one row after the other
-        int64_t at = __shfl_sync(~0u, row[0], (octet * 8) & 31);
-        if constexpr (kWords == 2) {
-          const int64_t other = __shfl_sync(~0u, row[1], (octet * 8) & 31);
-          if (octet >= 4) at = other;
-        }
-        const uint8_t *src = codes + at * D;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) cp_async16(raw + i * 512, src + i * row_bytes, false);
-      } else {
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          const int t = octet * 8 + i;
-          int64_t at = __shfl_sync(~0u, row[0], t & 31);
-          unsigned valid = x.valid[0];
-          if constexpr (kWords == 2) {
-            const int64_t other = __shfl_sync(~0u, row[1], t & 31);
-            if (t >= 32) at = other, valid = x.valid[1];
-          }
-          cp_async16(raw + i * 512, codes + at * D, !((valid >> (t & 31)) & 1));  // not there: zeros
-        }
-      }
-      x.scale[0] = x.scale[1] = 0;
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        if (!((x.valid[i] >> lane) & 1)) continue;
-        if (q.value) {
-          x.scale[i] = __ldg(p.vs + row[i]);
-        } else if constexpr (kWords == 1) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.ks + row[0] * (D / 32)));
-          x.scale[0] = w.x, x.scale[1] = w.y;
-        } else {
-          x.scale[i] = __ldg(reinterpret_cast<const uint32_t *>(p.ks + row[i] * (D / 32)));
-        }
-      }
-    };
-    // exponent e of a scale, 2^e <= |s| < 2^(e+1); those that are not finite count as the largest
-    const auto exponent = [](uint32_t abs_bits) { return min((int)(abs_bits >> 23) - 127, 15); };
-
-    Unit<D> x;
-    int page[kWords];
-    int u = warp - kFirstConverter;
-    lookup(u, page);
-    load(u, page, x);
-    lookup(u + C::kConverters, page);
-    bool ok = true;
-    while (u < units) {
-      const Place q = place(u);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      uint4 code[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) code[i] = lds128(raw + i * 512);
-      Unit<D> y;
-      load(u + C::kConverters, page, y);
-      lookup(u + 2 * C::kConverters, page);
-      TileMeta &tm = sh.meta[q.tile % kMetaSlots];
-      const int j0 = beg + q.tile * kPos;
-      // exponents of the unit's largest and smallest scale (zeros apart)
-      unsigned top = 0x33800000u, low = 0x7F800000u;  // 2^-24, float16's smallest
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const unsigned a = __float_as_uint(fabsf(half_at(x.scale[i / 2], i % 2)));
-        top = max(top, a);
-        low = a ? min(low, a) : low;
-      }
-      const int e = exponent(__reduce_max_sync(~0u, top));
-      if (!q.value) {
-        const float down = pow2i(-e);
-        ok = mbar_wait_asleep(&sh.k_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
-        if (!__all_sync(~0u, ok)) break;
-        if (lane < kWords) {
-          tm.ek[q.block * kWords + lane] = e;
-          tm.valid[q.block * kWords + lane] = lane == 0 ? x.valid[0] : x.valid[kWords - 1];
-        }
-        const uint32_t dst = base + C::kKAt + (q.tile & 1) * C::kTileBytes + (chunk / 4) * C::kSub;
-        uint32_t sw[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) sw[i] = half2_of(half_at(x.scale[i], 0) * down, half_at(x.scale[i], 1) * down);
-        const int row0 = q.block * C::kUnit + octet * 8, unit = (chunk % 4) * 2;
-        // lanes of the second column store their upper half first: no two of a row's
-        // lanes meet in a bank
-        const uint32_t second = ((lane >> 2) & 1) << 4;
-        // (two rows of code, walked over four times: straight-line code for eight rows
-        // costs more in instruction fetches than the moves)
-#pragma unroll 1
-        for (int i = 0; i < 8; i += 2) {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int t = octet * 8 + i + v;
-            const uint32_t w0 = __shfl_sync(~0u, sw[0], t & 31), w1 = __shfl_sync(~0u, sw[1], t & 31);
-            const uint32_t w = (kWords == 1 ? chunk >= 4 : t >= 32) ? w1 : w0;
-            const __half2 sc = bits_half2(__byte_perm(w, w, chunk & 2 ? 0x3232 : 0x1010));
-            const uint32_t c[4] = {code[v].x, code[v].y, code[v].z, code[v].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              int8x4_to_half(c[k], o[2 * k], o[2 * k + 1]);
-              o[2 * k] = half2_bits(__hmul2(bits_half2(o[2 * k]), sc));
-              o[2 * k + 1] = half2_bits(__hmul2(bits_half2(o[2 * k + 1]), sc));
-            }
-            const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), z = make_uint4(o[4], o[5], o[6], o[7]);
-            const uint32_t at = dst + swizzled(row0 + i + v, unit);
-            sts128(at ^ second, second ? z : a);
-            sts128(at ^ second ^ 16, second ? a : z);
-          }
-#pragma unroll
-          for (int k = 0; k < 6; ++k) code[k] = code[k + 2];
-        }
-      } else {
-        const bool wide = e - min(exponent(__reduce_min_sync(~0u, low)), e) > kValueSpan;
-        unsigned poison[kWords];
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) poison[i] = 0;
-        if (__builtin_expect(!(j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
-                               (x.valid[0] & x.valid[kWords - 1]) == ~0u), 0)) {
-          // positions that some row does not see: NaN codes and scales that are not
-          // finite become zeros, which P = 0 leaves alone; rows that do see one get
-          // their NaN from P
-#pragma unroll
-          for (int i = 0; i < kWords; ++i) poison[i] = __ballot_sync(~0u, (x.scale[i] & 0x7FFFu) >= 0x7C00u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t bad = __vcmpeq4(code[i].x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                                 __vcmpeq4(code[i].y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                                 __vcmpeq4(code[i].z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
-                                 __vcmpeq4(code[i].w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            const unsigned who = __ballot_sync(~0u, bad != 0);
-            if ((who >> (octet * C::kChunks)) & ((1u << C::kChunks) - 1)) code[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int o = 0; o < 32 / C::kChunks; ++o)
-              if ((who >> (o * C::kChunks)) & ((1u << C::kChunks) - 1)) poison[o / 4] |= 1u << ((o % 4) * 8 + i);
-          }
-#pragma unroll
-          for (int i = 0; i < kWords; ++i)
-            if ((poison[i] >> lane) & 1) x.scale[i] = 0;
-        }
-        // (e stands for the scales as loaded: one that is not finite only makes it the largest)
-        if (lane < kWords) {
-          tm.ev[q.block * kWords + lane] = e - kValueUp;
-          tm.poison[q.block * kWords + lane] = lane == 0 ? poison[0] : poison[kWords - 1];
-          tm.wide[q.block * kWords + lane] = wide;
-        }
-        // scales as float16, the octet's then two positions at a time
-        uint32_t sw[kWords];
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          const float s = half_at(x.scale[i], 0);
-          int es = e;
-          if (wide) {
-            const unsigned a = __float_as_uint(fabsf(s));
-            es = a ? exponent(a) : e;
-            tm.pos_ev[q.block * C::kUnit + i * 32 + lane] = (float)(es - kValueUp);
-          }
-          const uint32_t w = __half_as_ushort(__float2half_rn(s * pow2i(kValueUp - es)));
-          sw[i] = w | (__shfl_down_sync(~0u, w, 1) << 16);
-        }
-        __half2 sc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = octet * 8 + 2 * i;
-          uint32_t w = __shfl_sync(~0u, sw[0], t & 31);
-          if constexpr (kWords == 2) {
-            const uint32_t other = __shfl_sync(~0u, sw[1], t & 31);
-            if (t >= 32) w = other;
-          }
-          sc[i] = bits_half2(w);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.meta_full[q.tile % kMetaSlots]);  // the softmax waits for no values
-        ok = mbar_wait_asleep(&sh.v_empty[q.tile & 1], ((q.tile >> 1) & 1) ^ 1, abort_flag);
-        if (!__all_sync(~0u, ok)) break;
-        const int first = q.block * C::kUnit + octet * 8;  // position within the tile
-        const uint32_t dst = base + C::kVAt + (q.tile & 1) * C::kTileBytes + (first / 64) * C::kVSub;
-        const int unit = first % 64 / 8;
-        // Eight dimensions at a time.  Lanes turn their eight bytes by lane % 8, so that
-        // the eight lanes that store at once write rows of different remainders mod 8:
-        // the swizzle then spreads them over all banks.
-        const uint32_t turn = lane & 7;
-        uint32_t sel0 = 0, sel1 = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sel0 |= ((k + turn) & 7) << (4 * k);
-          sel1 |= ((k + 4 + turn) & 7) << (4 * k);
-        }
-#pragma unroll 1
-        for (int w = 0; w < 2; ++w) {
-          uint32_t lo8[8], hi8[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            lo8[i] = __byte_perm(code[i].x, code[i].y, sel0);
-            hi8[i] = __byte_perm(code[i].x, code[i].y, sel1);
-            code[i].x = code[i].z, code[i].y = code[i].w;
-          }
-          const int d0 = chunk * 16 + w * 8;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {  // byte k of the turned eight: dimension (k + turn) % 8
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t s0 = k < 4 ? lo8[2 * i] : hi8[2 * i], s1 = k < 4 ? lo8[2 * i + 1] : hi8[2 * i + 1];
-              const uint32_t two = __byte_perm(s0, s1, (k & 3) | ((4 + (k & 3)) << 4));
-              o[i] = half2_bits(__hmul2(bits_half2(e4m3x2_to_half((uint16_t)two)), sc[i]));
-            }
-            sts128(dst + swizzled(d0 + ((k + turn) & 7), unit), make_uint4(o[0], o[1], o[2], o[3]));
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (!q.value) mbar_arrive(&sh.meta_full[q.tile % kMetaSlots]);
-        mbar_arrive(q.value ? &sh.v_full[q.tile & 1] : &sh.k_full[q.tile & 1]);
-      }
-      u += C::kConverters;
-      x = y;
     }
-    if (!ok) *abort_flag = 1;
+    __syncwarp();
   }
   __syncthreads();
   tc_fence_after();
@@ -709,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
 }
 
 template <int D>
-cudaError_t launch_d(const PrefillParams &p, int64_t ctas, cudaStream_t st) {
+cudaError_t launch_d(PrefillParams p, int64_t group, cudaStream_t st) {
   using C = Config<D>;
   static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
   int dev = 0;
@@ -720,20 +653,43 @@ cudaError_t launch_d(const PrefillParams &p, int64_t ctas, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  return launch_kernel(k_attn_prefill<D>, dim3((unsigned)ctas), dim3(kThreads), C::kSmem, st, 1, p);
+  for (p.head0 = 0; p.head0 < p.H; p.head0 += p.heads) {
+    p.heads = (int)std::min<int64_t>(group, p.H - p.head0);  // the increment sees it, too
+    p.meta = reinterpret_cast<TileMeta *>(p.images + (int64_t)p.B * p.heads * p.tiles * C::kImage);
+    const int64_t pairs = (int64_t)p.B * p.heads;
+    e = launch_kernel(k_attn_unpack<D>, dim3((unsigned)(pairs * p.tiles)), dim3(64 * C::kUnits), 0, st, 1, p);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(k_attn_prefill<D>, dim3((unsigned)(pairs * p.row_tiles)), dim3(kThreads), C::kSmem, st, 1, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
 bool attn_prefill_has(int64_t D) { return D == 64 || D == 128; }
 
-cudaError_t launch_attn_prefill(const AttnArgs &a, int few_rows, unsigned *status, cudaStream_t st) {
+// kv heads are unpacked together until their images reach 2 GB (a quarter of
+// the positions of a full GPU of 8-bit cache), then in groups one after the other.
+AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t D, int64_t max_kv) {
+  AttnPrefillPlan plan{};
+  const int64_t tiles = std::max<int64_t>(1, (max_kv + kPos - 1) / kPos);
+  const int64_t head = B * tiles * (4 * kPos * D + (int64_t)sizeof(TileMeta));
+  plan.heads = std::max<int64_t>(1, std::min(H, ((int64_t)2 << 30) / head));
+  plan.ws_bytes = round_up((size_t)(head * plan.heads), 256);
+  return plan;
+}
+
+cudaError_t launch_attn_prefill(const AttnArgs &a, const AttnPrefillPlan &plan, int few_rows, void *ws,
+                                unsigned *status, cudaStream_t st) {
   PrefillParams p{};
   static_cast<AttnDev &>(p) = attn_dev(a, few_rows, status);
   p.row_tiles = (int)((a.max_q * (a.Hq / a.H) + 2 * kRowTile - 1) / (2 * kRowTile));
-  const int64_t ctas = (int64_t)p.row_tiles * a.B * a.H;
-  if (a.D == 64) return launch_d<64>(p, ctas, st);
-  if (a.D == 128) return launch_d<128>(p, ctas, st);
+  p.tiles = (int)std::max<int64_t>(1, (a.max_kv + kPos - 1) / kPos);
+  p.images = (uint8_t *)ws;
+  p.heads = (int)plan.heads;
+  if (a.D == 64) return launch_d<64>(p, plan.heads, st);
+  if (a.D == 128) return launch_d<128>(p, plan.heads, st);
   return cudaErrorInvalidValue;
 }
 

@@ -285,7 +285,13 @@ AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64
 cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, int few_rows, void *ws, unsigned *status,
                               cudaStream_t st);
 bool attn_prefill_has(int64_t D);
-cudaError_t launch_attn_prefill(const AttnArgs &a, int few_rows, unsigned *status, cudaStream_t st);
+struct AttnPrefillPlan {
+  int64_t heads;  // kv heads whose keys and values are in the workspace at once
+  size_t ws_bytes;
+};
+AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t D, int64_t max_kv);
+cudaError_t launch_attn_prefill(const AttnArgs &a, const AttnPrefillPlan &plan, int few_rows, void *ws,
+                                unsigned *status, cudaStream_t st);
 
 // tcgen05 kernels (gemm_tc.cu)
 cudaError_t launch_fp8_gemm(const GemmArgs &g, const DeviceInfo &dev, cudaStream_t st);

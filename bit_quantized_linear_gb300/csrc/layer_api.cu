@@ -63,6 +63,8 @@ struct AttnRoute {
   bool few, many;  // the split kernel, the tcgen05 kernel
   int few_rows;
   AttnSplitPlan split;
+  AttnPrefillPlan prefill;
+  size_t ws_bytes() const { return split.ws_bytes + prefill.ws_bytes; }
 };
 AttnRoute attn_route(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv, int64_t window) {
   AttnRoute r{};
@@ -70,6 +72,7 @@ AttnRoute attn_route(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q,
   r.many = attn_prefill_has(D) && rows > kFewRows;
   r.few = !r.many || B > 1;
   r.few_rows = r.many ? (r.few ? (int)kFewRows : 0) : (int)rows;
+  if (r.many) r.prefill = attn_prefill_plan(B, H, D, max_kv);
   if (r.few) r.split = attn_split_plan(B, Hq, H, D, r.few_rows, max_kv, window, sm_count());
   return r;
 }
@@ -177,7 +180,7 @@ size_t qlin_attn_mixed_workspace_bytes(int64_t B, int64_t Hq, int64_t H, int64_t
                                        int64_t window) {
   if (check_attn_sizes(B, Hq, H, D, max_q, max_kv, window)) return (size_t)-1;
   if (B == 0 || max_q == 0) return 0;
-  return attn_route(B, Hq, H, D, max_q, max_kv, window).split.ws_bytes;
+  return attn_route(B, Hq, H, D, max_q, max_kv, window).ws_bytes();
 }
 
 const char *qlin_attn_mixed_kernel_name(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv,
@@ -185,8 +188,8 @@ const char *qlin_attn_mixed_kernel_name(int64_t B, int64_t Hq, int64_t H, int64_
   if (check_attn_sizes(B, Hq, H, D, max_q, max_kv, window)) return "invalid";
   if (B == 0 || max_q == 0) return "none";
   const AttnRoute r = attn_route(B, Hq, H, D, max_q, max_kv, window);
-  if (!r.few) return "k_attn_prefill";
-  if (r.many) return r.split.splits > 1 ? "k_attn_prefill+k_attn_split+k_attn_join" : "k_attn_prefill+k_attn_split";
+  if (!r.few) return "k_attn_unpack+k_attn_prefill";
+  if (r.many) return r.split.splits > 1 ? "k_attn_unpack+k_attn_prefill+k_attn_split+k_attn_join" : "k_attn_unpack+k_attn_prefill+k_attn_split";
   return r.split.splits > 1 ? "k_attn_split+k_attn_join" : "k_attn_split";
 }
 
@@ -218,10 +221,11 @@ qlin_status qlin_attn_mixed(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t
   AttnArgs a{B,         T,          Hq,        H,       D,       q,       ldq,     q_start, max_q, kv_len, max_kv, block_table,
              max_blocks, block_size, num_slots, k_cache, k_scale, v_cache, v_scale, scale,   causal, window, out,   ldo};
   const AttnRoute r = attn_route(B, Hq, H, D, max_q, max_kv, window);
-  if (r.many && launch_attn_prefill(a, r.few_rows, dev->status, (cudaStream_t)stream) != cudaSuccess)
+  if (r.many && launch_attn_prefill(a, r.prefill, r.few_rows, ws, dev->status, (cudaStream_t)stream) != cudaSuccess)
     return QLIN_ERR_CUDA;
   if (!r.few) return QLIN_OK;
-  return from_cuda(launch_attn_split(a, r.split, r.few_rows, ws, dev->status, (cudaStream_t)stream));
+  void *parts = r.split.ws_bytes ? (char *)ws + r.prefill.ws_bytes : nullptr;
+  return from_cuda(launch_attn_split(a, r.split, r.few_rows, parts, dev->status, (cudaStream_t)stream));
 }
 
 }  // extern "C"

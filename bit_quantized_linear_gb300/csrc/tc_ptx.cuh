@@ -134,6 +134,15 @@ __device__ __forceinline__ void tma_load_2d(const CUtensorMap *tm, uint64_t *bar
       : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16) contiguous bytes into shared memory;
+// both addresses 16-byte aligned; completion is counted on `bar` in bytes.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // L2 policy for data read once (streamed): its lines are the first evicted.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t pol;
