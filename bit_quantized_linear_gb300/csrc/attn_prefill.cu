@@ -79,7 +79,8 @@ struct Config {
 };
 
 struct Shared {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], meta_full[kMetaSlots];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], meta_full[kMetaSlots];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2];  // of row tiles A and B
   uint32_t tmem;
   int abort;
   TileMeta meta[kMetaSlots];
@@ -342,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_half[i], kSoftmaxWarps / 2);
+      mbar_init(&sh.p_full[i], kSoftmaxWarps / 2);
       mbar_init(&sh.o_full[i], 1);
     }
     for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sh.meta_full[i], 1);
@@ -446,10 +448,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       for (int c = 0; c < 4; ++c) {
         float mx = -INFINITY;
         if (__builtin_expect(wide[c] == 0, 1)) {
+          float t[4];  // four chains
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            mx = fmaxf(mx, fmaxf(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])));
-          mx = fmaf(mx, f[c], (float)ev[c]);
+          for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[c][i]);
+#pragma unroll
+          for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[c][i]));
+          mx = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaf(__uint_as_float(s[c][i]), f[c], tm.pos_ev[c * 32 + i]));
@@ -508,7 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           tmem_st16(s_at + k * 16, o);
         };
 #pragma unroll
-        for (int c = 0; c < 4; ++c) probabilities(c, s[c], f[c], ev[c], wide[c]);
+        for (int c = 0; c < 4; ++c) {
+          probabilities(c, s[c], f[c], ev[c], wide[c]);
+          if (c == 1) {  // the first half of P: its products start
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_half[half]);
+          }
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -554,12 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         }
         mma_commit(&sh.s_full[half]);
       };
-      const auto outputs = [&](int half, int j) {
-        const uint64_t bd = umma_desc_sw128(base + C::kVAt + (j & 1) * C::kTileBytes);
+      // O += P V over 64 of the positions
+      const auto outputs = [&](int half, int j, int part) {
+        const uint64_t bd = umma_desc_sw128(base + C::kVAt + (j & 1) * C::kTileBytes + part * C::kVSub);
 #pragma unroll
-        for (int k = 0; k < kPos / 16; ++k)
-          mma_f16_ts(tmem + C::kO + half * D, tmem + C::kS + half * kPos + k * 8,
-                     bd + (uint64_t)((k / 4) * (C::kVSub >> 4) + (k % 4) * 2), C::kIdescO, j > 0 || k > 0);
+        for (int k = 0; k < 4; ++k)
+          mma_f16_ts(tmem + C::kO + half * D, tmem + C::kS + half * kPos + (part * 4 + k) * 8, bd + (uint64_t)(k * 2),
+                     C::kIdescO, j > 0 || part > 0 || k > 0);
       };
       bool ok = mbar_wait(&sh.k_full[0], 0, abort_flag);
       if (ok) {
@@ -569,28 +582,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         mma_commit(&sh.k_empty[0]);
       }
       for (int j = 0; j < n && ok; ++j) {
-        ok = mbar_wait(&sh.v_full[j & 1], (j >> 1) & 1, abort_flag) && mbar_wait(&sh.p_full[0], j & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        outputs(0, j);
-        if (j + 1 < n) {
-          ok = mbar_wait(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag);
+        const bool more = j + 1 < n;
+        ok = mbar_wait(&sh.v_full[j & 1], (j >> 1) & 1, abort_flag);
+        for (int half = 0; half < 2 && ok; ++half) {
+          ok = mbar_wait(&sh.p_half[half], j & 1, abort_flag);
           if (!ok) break;
           tc_fence_after();
-          scores(0, j + 1);
-        } else {
-          mma_commit(&sh.o_full[0]);
-        }
-        ok = mbar_wait(&sh.p_full[1], j & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        outputs(1, j);
-        mma_commit(&sh.v_empty[j & 1]);
-        if (j + 1 < n) {
-          scores(1, j + 1);
-          mma_commit(&sh.k_empty[(j + 1) & 1]);
-        } else {
-          mma_commit(&sh.o_full[1]);
+          outputs(half, j, 0);
+          ok = mbar_wait(&sh.p_full[half], j & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          outputs(half, j, 1);
+          if (half) mma_commit(&sh.v_empty[j & 1]);
+          if (more) {
+            ok = half || mbar_wait(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            scores(half, j + 1);  // over P: products run in the order of issue
+            if (half) mma_commit(&sh.k_empty[(j + 1) & 1]);
+          } else {
+            mma_commit(&sh.o_full[half]);
+          }
         }
       }
       if (!ok) *abort_flag = 1;
