@@ -78,13 +78,19 @@ __device__ __forceinline__ int q_exponent(float top) {
   return top > 0.0f && e < 128 ? max(e, -100) : 14;
 }
 
-// Four INT8 codes -> two words of float16: with the sign bit flipped a code is
-// u = c + 128, and the bytes (u, 0x64) are the float16 1024 + u; minus 1152.
-__device__ __forceinline__ void int8x4_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+// Four INT8 codes c -> two words of float16 holding 1152 + c: with the sign bit
+// flipped a code is u = c + 128, and the bytes (u, 0x64) are the float16 1024 + u.
+__device__ __forceinline__ void int8x4_to_offset_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
   const uint32_t u = w ^ 0x80808080u;
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));
-  lo = half2_bits(__hsub2(bits_half2(__byte_perm(u, 0x64646464u, 0x4140)), bias));
-  hi = half2_bits(__hsub2(bits_half2(__byte_perm(u, 0x64646464u, 0x4342)), bias));
+  lo = __byte_perm(u, 0x64646464u, 0x4140);
+  hi = __byte_perm(u, 0x64646464u, 0x4342);
+}
+// The codes themselves.
+__device__ __forceinline__ void int8x4_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const __half2 offset = __half2half2(__ushort_as_half(0x6480));
+  int8x4_to_offset_half(w, lo, hi);
+  lo = half2_bits(__hsub2(bits_half2(lo), offset));
+  hi = half2_bits(__hsub2(bits_half2(hi), offset));
 }
 // Two E4M3 codes -> float16 (exact).
 __device__ __forceinline__ uint32_t e4m3x2_to_half(uint16_t c) {

@@ -4,9 +4,9 @@
 //
 // Rows and positions.  The rows of a sequence that read one kv head (its new
 // tokens times the Hq/H query heads of the group) are tiled by 8*NT.  Each CTA
-// takes one row tile and one part of the positions; its four warps take 16
-// positions at a time, each with a ring of its own in shared memory that it
-// fills with 16-byte cp.async, so nothing but the end of the part makes warps
+// takes one row tile and one part of the positions; its four warps take 32 (D
+// 256: 16) positions at a time, each with a ring of its own in shared memory that
+// it fills with 16-byte cp.async, so nothing but the end of the part makes warps
 // wait for one another.
 //
 // Arithmetic.  Scores and outputs are transposed, S^T = K q^T and O^T = V^T P^T,
@@ -15,13 +15,18 @@
 // the heads of one group would leave half of the 16 rows empty.  tcgen05 would
 // want 128 rows of one operand staged in shared memory as 16-bit values; here
 // codes go from the ring to registers once and the tensor pipe is far from its
-// limit.  Codes become float16 exactly (INT8 by a byte permute and a
-// subtraction, E4M3 by conversion); q is scaled by a power of two per row to
+// limit.  Codes become float16 exactly: INT8 as 1152 + code by a byte permute (the
+// sums start at -1152 times the sum of q, in fp32, which takes the offset out
+// again), E4M3 by conversion; q is scaled by a power of two per row to
 // use float16's whole range; the products of one 32-dimension key group are
 // summed in fp32 and then scaled by the group's scale in fp32.  P is multiplied
 // by the value scales (and a power of two that keeps the product below 2^15)
 // in fp32 and rounded once to float16.  P^T as the second operand needs P's
 // fragments transposed: two movmatrix per 16 positions.
+//
+// What bounds it beside HBM is the instructions of the conversions, so positions
+// of whole pages take their addresses from one table entry and one multiplication
+// per 32, and the maxima of 32 positions are reduced at once.
 #include <algorithm>
 
 #include "attn.cuh"
@@ -35,7 +40,7 @@ namespace qlin {
 namespace {
 
 constexpr int kAttnWarps = 4;
-constexpr int kTile = 16;    // positions a warp handles at once
+constexpr int kAlign = 32;   // parts begin at multiples of this: the most positions a warp handles at once
 
 struct SplitParams : AttnDev {
   float *part_o, *part_lse;
@@ -43,7 +48,10 @@ struct SplitParams : AttnDev {
   int row_tiles, splits;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool fill) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool fill) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 0 : 16) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -64,11 +72,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 }
 template <int D, int NT>
 struct Geometry {
+  static constexpr int kTile = D >= 256 ? 16 : 32;  // positions a warp handles at once
   static constexpr int kRows = 8 * NT;
   static constexpr int kGroups = D / 32;
-  static constexpr int kChunks = D / 16;  // 16-byte pieces of a row of codes
+  static constexpr int kChunks = D / 16;               // 16-byte pieces of a row of codes
+  static constexpr int kPieces = kTile * kChunks / 32;  // pieces a lane copies
+  static constexpr int kRowStep = 32 / kChunks;         // rows the warp copies at once
   static constexpr int kCodes = kTile * D;
-  static constexpr int kStages = D >= 256 ? 3 : 4;  // tiles in a warp's ring
+  static constexpr int kStages = D >= 128 ? 2 : 3;  // tiles in a warp's ring
   // one stage: key codes, value codes, key scales, value scales, {valid, largest value scale}
   static constexpr int kScaleAt = 2 * kCodes;
   static constexpr int kVScaleAt = kScaleAt + kTile * kGroups * 4;
@@ -101,6 +112,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_attn_split(const SplitParams p) {
   using Geo = Geometry<D, NT>;
   constexpr int kGroups = Geo::kGroups, kRows = Geo::kRows, kStages = Geo::kStages;
+  constexpr int kTile = Geo::kTile, kHalves = kTile / 16;  // 16 positions are the rows of an MMA
   constexpr int kDims = D / 8;  // dimensions of a value row a lane holds
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -127,13 +139,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     int unused;
     sees(p, sq, r0 / p.G, lo, unused);
     sees(p, sq, last / p.G, unused, hi);
-    const int64_t from = (int64_t)(lo & ~(kTile - 1)) + (int64_t)split * p.chunk;
+    const int64_t from = (int64_t)(lo & ~(kAlign - 1)) + (int64_t)split * p.chunk;
     beg = (int)min(from, (int64_t)max(hi, 0));
     end = split == p.splits - 1 ? max(hi, beg) : (int)min(from + p.chunk, (int64_t)max(hi, beg));
   }
 
   // q: row 8*nt + g, as the second operand; its largest magnitude becomes 2^14..2^15
   uint32_t qf[NT][kGroups][4];
+  float qoff[NT][kGroups][2];    // -1152 times the sums of columns 2t and 2t + 1 over a key group
   float cf[NT][2];               // score factors of columns 2t and 2t + 1
   int vlo[NT][2], vhi[NT][2];    // positions those columns see
   int all_lo = lo, all_hi = hi;  // positions every row sees
@@ -165,6 +178,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         qf[nt][k][j] = half2_of(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = __half22float2(bits_half2(qf[nt][k][j]));
+        sum += x.x + x.y;
+      }
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) qoff[nt][k][c] = -1152.0f * __shfl_sync(~0u, sum, (2 * t + c) * 4);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -190,49 +213,71 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   int vexp = -1000;  // O is sum p v 2^-vexp
 
   // ---- the ring: tile n covers positions beg + (n * warps + warp) * 16 ...
-  const int tiles = (end - beg + kTile - 1) / kTile;
+  const int tiles = (end - beg + kTile - 1) / kTile;  // beg is a multiple of it
   const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
-  const int row16 = lane & 15;
   const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
-  const auto position = [&](int n) { return beg + (n * kAttnWarps + warp) * kTile + row16; };
+  const int own = lane & (kTile - 1);  // the position of a tile whose scales (and page) a lane sees to
+  const bool even = p.block_size % kTile == 0;  // a tile lies in one page
+  const auto first_of = [&](int n) { return beg + (n * kAttnWarps + warp) * kTile; };
+  const auto whole = [&](int n) { return even && n < mine && first_of(n) >= lo && first_of(n) + kTile <= end; };
   const auto page = [&](int n) {  // page of the lane's position of tile n (-1: none)
-    const int j = position(n);
-    return n < mine && j >= lo && j < end ? __ldg(table + block_of(p, j)) : -1;
+    const int j = first_of(n) + (even ? 0 : own);
+    return n < mine && (whole(n) || (j + (even ? own : 0) >= lo && j + (even ? own : 0) < end))
+               ? __ldg(table + block_of(p, j)) : -1;
   };
+  const int piece_row = lane / Geo::kChunks, piece = lane % Geo::kChunks;
+  const int64_t row_bytes = (int64_t)p.H * D;
+  const int64_t lane_off = piece_row * row_bytes + (int64_t)h * D + piece * 16;
   uint32_t sc[(kGroups + 1) / 2];  // the lane's scales of the tile issued last
   uint32_t sv = 0;
-  bool sok = false;
+  unsigned there = 0;  // which positions of that tile are there
   int next_page = page(0);
+  const auto load_scales = [&](int64_t row) {  // row: (slot, head) of the lane's position
+    sv = __ldg(p.vs + row);
+    if constexpr (kGroups == 1) {
+      sc[0] = __ldg(p.ks + row);
+    } else {
+      load_words<kGroups / 2>(p.ks + row * kGroups, sc);
+    }
+  };
   const auto issue = [&](int n) {
-    const int j = position(n), blk = next_page;
-    const bool wanted = n < mine && j >= lo && j < end;
-    sok = wanted && blk >= 0 && blk < p.num_blocks;
-    if (wanted && !sok && lane < 16) set_status(p.status, QLIN_ERR_INVALID_ARG);
-    const int64_t slot = sok ? (int64_t)blk * p.block_size + (j - block_of(p, j) * p.block_size) : 0;
-    const int64_t base = slot * p.H + h;
+    const int blk = next_page, j0 = first_of(n);
     next_page = page(n + 1);
-    if (n < mine) {
-      const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
-      const unsigned ok = __ballot_sync(~0u, sok);
+    const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
+    if (whole(n) && (unsigned)blk < (unsigned)p.num_blocks) {
+      // one page: rows at one distance
+      const int64_t slot = (int64_t)blk * p.block_size + (j0 - block_of(p, j0) * p.block_size);
+      const int64_t off = slot * row_bytes + lane_off, step = Geo::kRowStep * row_bytes;
+      const uint8_t *k = p.kc + off, *v = p.vc + off;
 #pragma unroll
-      for (int i = 0; i < Geo::kChunks / 2; ++i) {
-        const int piece = i * 32 + lane, r = piece / Geo::kChunks, c = piece % Geo::kChunks;
-        const int64_t off = __shfl_sync(~0u, base, r) * D + c * 16;
-        const bool fill = !((ok >> r) & 1);
-        cp_async16(at + r * D + key_chunk<D>(r, c) * 16, p.kc + off, fill);
-        cp_async16(at + Geo::kCodes + r * D + value_chunk<D>(r, c) * 16, p.vc + off, fill);
+      for (int i = 0; i < Geo::kPieces; ++i) {
+        const int r = i * Geo::kRowStep + piece_row;
+        cp_async16(at + r * D + key_chunk<D>(r, piece) * 16, k);
+        cp_async16(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, v);
+        k += step;
+        v += step;
+      }
+      if (kTile == 32 || lane < kTile) load_scales((slot + own) * p.H + h);
+      there = ~0u >> (32 - kTile);
+    } else if (n < mine) {
+      // positions that are not there (before lo, from end on, without a page): zeros
+      const int j = j0 + own;
+      const bool wanted = j >= lo && j < end, ok = wanted && (unsigned)blk < (unsigned)p.num_blocks;
+      if (wanted && !ok && lane < kTile) set_status(p.status, QLIN_ERR_INVALID_ARG);
+      const int64_t row = ok ? ((int64_t)blk * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
+      there = __ballot_sync(~0u, ok) & (~0u >> (32 - kTile));
+#pragma unroll 1
+      for (int i = 0; i < Geo::kPieces; ++i) {
+        const int r = i * Geo::kRowStep + piece_row;
+        const int64_t off = __shfl_sync(~0u, row, r) * D + piece * 16;
+        const bool fill = !((there >> r) & 1);
+        cp_async16_or_zero(at + r * D + key_chunk<D>(r, piece) * 16, p.kc + off, fill);
+        cp_async16_or_zero(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, p.vc + off, fill);
       }
       sv = 0;
 #pragma unroll
       for (int k = 0; k < (kGroups + 1) / 2; ++k) sc[k] = 0;
-      if (sok && lane < 16) {
-        sv = __ldg(p.vs + base);
-        if constexpr (kGroups == 1) {
-          sc[0] = __ldg(p.ks + base);
-        } else {
-          load_words<kGroups / 2>(p.ks + base * kGroups, sc);
-        }
-      }
+      if (ok && lane < kTile) load_scales(row);
     }
     cp_async_commit();
   };
@@ -241,15 +286,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     if (n >= mine) return;
     uint8_t *at = ring + (n % kStages) * Geo::kStageBytes;
     const float v = half_bits_to_f32((uint16_t)sv);
-    const unsigned ok = __ballot_sync(~0u, sok);
     const unsigned top = __reduce_max_sync(~0u, min(__float_as_uint(fabsf(v)), 0x7F7FFFFFu));
-    if (lane < 16) {
+    if (kTile == 32 || lane < kTile) {
       float *k = reinterpret_cast<float *>(at + Geo::kScaleAt) + lane * kGroups;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) k[i] = half_bits_to_f32((uint16_t)(sc[i / 2] >> (16 * (i & 1))));
       reinterpret_cast<float *>(at + Geo::kVScaleAt)[lane] = v;
     }
-    if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(ok & 0xFFFFu, top);
+    if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(there, top);
   };
 
   for (int n = 0; n < kStages - 1; ++n) {
@@ -258,77 +302,89 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   }
   for (int n = 0; n < mine; ++n) {
     cp_async_wait<kStages - 2>();
-    __syncwarp();
     put_scales(n + kStages - 2);
+    __syncwarp();
     issue(n + kStages - 1);
     const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
     uint8_t *stage = ring + (n % kStages) * Geo::kStageBytes;
     const uint2 info = *reinterpret_cast<const uint2 *>(stage + Geo::kInfoAt);
-    const int j0 = beg + (n * kAttnWarps + warp) * kTile;
-    const bool full = info.x == 0xFFFFu && j0 >= all_lo && j0 + kTile <= all_hi;
-    float vs0 = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[g];
-    float vs1 = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[g + 8];
+    const int j0 = first_of(n);
+    const bool full = info.x == (~0u >> (32 - kTile)) && j0 >= all_lo && j0 + kTile <= all_hi;
+    float vs[kHalves][2];  // of positions g and g + 8 of each half
 
-    // scores of positions g, g + 8 and columns 2t, 2t + 1
-    float S[NT][4];
+    // scores of those positions and columns 2t, 2t + 1
+    float S[kHalves][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) S[nt][0] = S[nt][1] = S[nt][2] = S[nt][3] = 0.0f;
+    for (int f = 0; f < kHalves; ++f) {
+      const int r0 = 16 * f + g, r1 = r0 + 8;
+      vs[f][0] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r0];
+      vs[f][1] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r1];
 #pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      uint32_t w0[2], w1[2];
-      const uint32_t a0 = at + g * D + key_chunk<D>(g, 2 * k) * 16 + t * 8;
-      const uint32_t a1 = at + (g + 8) * D + key_chunk<D>(g + 8, 2 * k) * 16 + t * 8;
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(a0));
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(a1));
-      float acc[NT][4];
+      for (int nt = 0; nt < NT; ++nt) S[f][nt][0] = S[f][nt][1] = S[f][nt][2] = S[f][nt][3] = 0.0f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+      for (int k = 0; k < kGroups; ++k) {
+        uint32_t w0[2], w1[2];
+        const uint32_t a0 = at + r0 * D + key_chunk<D>(r0, 2 * k) * 16 + t * 8;
+        const uint32_t a1 = at + r1 * D + key_chunk<D>(r1, 2 * k) * 16 + t * 8;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(a0));
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(a1));
+        float acc[NT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t a[4];
-        int8x4_to_half(w0[j], a[0], a[2]);
-        int8x4_to_half(w1[j], a[1], a[3]);
+        for (int nt = 0; nt < NT; ++nt) {
+          acc[nt][0] = acc[nt][2] = qoff[nt][k][0];
+          acc[nt][1] = acc[nt][3] = qoff[nt][k][1];
+        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a, qf[nt][k][2 * j], qf[nt][k][2 * j + 1]);
+        for (int j = 0; j < 2; ++j) {
+          uint32_t a[4];
+          int8x4_to_offset_half(w0[j], a[0], a[2]);
+          int8x4_to_offset_half(w1[j], a[1], a[3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a, qf[nt][k][2 * j], qf[nt][k][2 * j + 1]);
+        }
+        const float k0 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[r0 * kGroups + k];
+        const float k1 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[r1 * kGroups + k];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          S[f][nt][0] = fmaf(acc[nt][0], k0, S[f][nt][0]);
+          S[f][nt][1] = fmaf(acc[nt][1], k0, S[f][nt][1]);
+          S[f][nt][2] = fmaf(acc[nt][2], k1, S[f][nt][2]);
+          S[f][nt][3] = fmaf(acc[nt][3], k1, S[f][nt][3]);
+        }
       }
-      const float k0 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[g * kGroups + k];
-      const float k1 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[(g + 8) * kGroups + k];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        S[nt][0] = fmaf(acc[nt][0], k0, S[nt][0]);
-        S[nt][1] = fmaf(acc[nt][1], k0, S[nt][1]);
-        S[nt][2] = fmaf(acc[nt][2], k1, S[nt][2]);
-        S[nt][3] = fmaf(acc[nt][3], k1, S[nt][3]);
+        S[f][nt][0] *= cf[nt][0], S[f][nt][2] *= cf[nt][0];
+        S[f][nt][1] *= cf[nt][1], S[f][nt][3] *= cf[nt][1];
       }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      S[nt][0] *= cf[nt][0], S[nt][2] *= cf[nt][0];
-      S[nt][1] *= cf[nt][1], S[nt][3] *= cf[nt][1];
     }
     if (!full) {
-      const bool ok0 = (info.x >> g) & 1, ok1 = (info.x >> (g + 8)) & 1;
-      const int p0 = j0 + g, p1 = p0 + 8;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (!ok0 || p0 < vlo[nt][c] || p0 >= vhi[nt][c]) S[nt][c] = -INFINITY;
-          if (!ok1 || p1 < vlo[nt][c] || p1 >= vhi[nt][c]) S[nt][2 + c] = -INFINITY;
-        }
       // A NaN value code times P = 0 would reach rows that do not see it: such
       // codes become 0 and their position's scale NaN.  (Two lanes to a row.)
-      unsigned bad = 0;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        uint32_t *w = reinterpret_cast<uint32_t *>(stage + Geo::kCodes + (lane >> 1) * D + (lane & 1) * (D / 2)) + i;
-        const uint32_t nan = __vcmpeq4(*w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        if (nan) *w &= ~nan;
-        bad |= nan;
+      for (int f = 0; f < kHalves; ++f) {
+        const int r0 = 16 * f + g, r1 = r0 + 8;
+        const bool ok0 = (info.x >> r0) & 1, ok1 = (info.x >> r1) & 1;
+        const int p0 = j0 + r0, p1 = p0 + 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (!ok0 || p0 < vlo[nt][c] || p0 >= vhi[nt][c]) S[f][nt][c] = -INFINITY;
+            if (!ok1 || p1 < vlo[nt][c] || p1 >= vhi[nt][c]) S[f][nt][2 + c] = -INFINITY;
+          }
+        unsigned bad = 0;
+        uint32_t *w = reinterpret_cast<uint32_t *>(stage + Geo::kCodes + (16 * f + (lane >> 1)) * D + (lane & 1) * (D / 2));
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t nan = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+          if (nan) w[i] &= ~nan;
+          bad |= nan;
+        }
+        const unsigned rows = __ballot_sync(~0u, bad != 0);
+        if ((rows >> (2 * g)) & 3) vs[f][0] = NAN;
+        if ((rows >> (2 * g + 16)) & 3) vs[f][1] = NAN;
       }
-      const unsigned rows = __ballot_sync(~0u, bad != 0);
-      if ((rows >> (2 * g)) & 3) vs0 = NAN;
-      if ((rows >> (2 * g + 16)) & 3) vs1 = NAN;
       __syncwarp();
     }
 
@@ -345,14 +401,21 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
           for (int c = 0; c < 4; ++c) O[nt][i][c] *= down;
       vexp = e - 7;
     }
-    vs0 *= pow2i(-vexp);
-    vs1 *= pow2i(-vexp);
+#pragma unroll
+    for (int f = 0; f < kHalves; ++f) {
+      vs[f][0] *= pow2i(-vexp);
+      vs[f][1] *= pow2i(-vexp);
+    }
 
     // online softmax per column
-    uint32_t pf[NT][2];
+    uint32_t pf[kHalves][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float mx[2] = {fmaxf(S[nt][0], S[nt][2]), fmaxf(S[nt][1], S[nt][3])};
+      float mx[2] = {fmaxf(S[0][nt][0], S[0][nt][2]), fmaxf(S[0][nt][1], S[0][nt][3])};
+      if constexpr (kHalves == 2) {
+        mx[0] = fmaxf(mx[0], fmaxf(S[kHalves - 1][nt][0], S[kHalves - 1][nt][2]));
+        mx[1] = fmaxf(mx[1], fmaxf(S[kHalves - 1][nt][1], S[kHalves - 1][nt][3]));
+      }
 #pragma unroll
       for (int o = 4; o < 32; o *= 2) {
         mx[0] = fmaxf(mx[0], __shfl_xor_sync(~0u, mx[0], o));
@@ -375,55 +438,62 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
         }
       }
       const float z0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], z1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
-      const float p00 = exp2_approx(S[nt][0] - z0), p01 = exp2_approx(S[nt][1] - z1);
-      const float p10 = exp2_approx(S[nt][2] - z0), p11 = exp2_approx(S[nt][3] - z1);
-      l[nt][0] += p00 + p10;
-      l[nt][1] += p01 + p11;
-      float w00 = p00 * vs0, w01 = p01 * vs0, w10 = p10 * vs1, w11 = p11 * vs1;
-      if (!full) {  // an unseen position adds nothing, whatever its scale
-        if (S[nt][0] == -INFINITY) w00 = 0.0f;
-        if (S[nt][1] == -INFINITY) w01 = 0.0f;
-        if (S[nt][2] == -INFINITY) w10 = 0.0f;
-        if (S[nt][3] == -INFINITY) w11 = 0.0f;
+#pragma unroll
+      for (int f = 0; f < kHalves; ++f) {
+        const float(&s)[4] = S[f][nt];
+        const float p00 = exp2_approx(s[0] - z0), p01 = exp2_approx(s[1] - z1);
+        const float p10 = exp2_approx(s[2] - z0), p11 = exp2_approx(s[3] - z1);
+        l[nt][0] += p00 + p10;
+        l[nt][1] += p01 + p11;
+        float w00 = p00 * vs[f][0], w01 = p01 * vs[f][0], w10 = p10 * vs[f][1], w11 = p11 * vs[f][1];
+        if (!full) {  // an unseen position adds nothing, whatever its scale
+          if (s[0] == -INFINITY) w00 = 0.0f;
+          if (s[1] == -INFINITY) w01 = 0.0f;
+          if (s[2] == -INFINITY) w10 = 0.0f;
+          if (s[3] == -INFINITY) w11 = 0.0f;
+        }
+        pf[f][nt][0] = transpose8x8(half2_of(w00, w01));
+        pf[f][nt][1] = transpose8x8(half2_of(w10, w11));
       }
-      pf[nt][0] = transpose8x8(half2_of(w00, w01));
-      pf[nt][1] = transpose8x8(half2_of(w10, w11));
     }
 
-    // O^T += V^T P^T: positions 2t, 2t+1 (and +8), dimensions g*D/8 ...
+    // O^T += V^T P^T: positions 2t, 2t+1 (and +8) of each half, dimensions g*D/8 ...
     constexpr int kW = kDims / 4;  // words of a lane's piece of a value row
-    uint32_t v[4][kW];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 2 * t + (i & 1) + 8 * (i >> 1);
-      const uint8_t *row = stage + Geo::kCodes + r * D;
-      if constexpr (kDims >= 16) {
+    for (int f = 0; f < kHalves; ++f) {
+      uint32_t v[4][kW];
 #pragma unroll
-        for (int c = 0; c < kDims / 16; ++c) {
-          const uint4 x =
-              *reinterpret_cast<const uint4 *>(row + value_chunk<D>(r, g * (kDims / 16) + c) * 16);
-          v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
+      for (int i = 0; i < 4; ++i) {
+        const int r = 16 * f + 2 * t + (i & 1) + 8 * (i >> 1);
+        const uint8_t *row = stage + Geo::kCodes + r * D;
+        if constexpr (kDims >= 16) {
+#pragma unroll
+          for (int c = 0; c < kDims / 16; ++c) {
+            const uint4 x =
+                *reinterpret_cast<const uint4 *>(row + value_chunk<D>(r, g * (kDims / 16) + c) * 16);
+            v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
+          }
+        } else if constexpr (kDims == 8) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(row + value_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
+          v[i][0] = x.x, v[i][1] = x.y;
+        } else {
+          v[i][0] = *reinterpret_cast<const uint32_t *>(row + g * 4);
         }
-      } else if constexpr (kDims == 8) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(row + value_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
-        v[i][0] = x.x, v[i][1] = x.y;
-      } else {
-        v[i][0] = *reinterpret_cast<const uint32_t *>(row + g * 4);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      // (position 2t, 2t+1) byte pairs of dimensions 4i, 4i+1 | 4i+2, 4i+3
-      const uint32_t x0 = __byte_perm(v[0][i], v[1][i], 0x5140), x1 = __byte_perm(v[0][i], v[1][i], 0x7362);
-      const uint32_t y0 = __byte_perm(v[2][i], v[3][i], 0x5140), y1 = __byte_perm(v[2][i], v[3][i], 0x7362);
-      const uint32_t a0[4] = {e4m3x2_to_half((uint16_t)x0), e4m3x2_to_half((uint16_t)(x0 >> 16)),
-                              e4m3x2_to_half((uint16_t)y0), e4m3x2_to_half((uint16_t)(y0 >> 16))};
-      const uint32_t a1[4] = {e4m3x2_to_half((uint16_t)x1), e4m3x2_to_half((uint16_t)(x1 >> 16)),
-                              e4m3x2_to_half((uint16_t)y1), e4m3x2_to_half((uint16_t)(y1 >> 16))};
+      for (int i = 0; i < kW; ++i) {
+        // (position 2t, 2t+1) byte pairs of dimensions 4i, 4i+1 | 4i+2, 4i+3
+        const uint32_t x0 = __byte_perm(v[0][i], v[1][i], 0x5140), x1 = __byte_perm(v[0][i], v[1][i], 0x7362);
+        const uint32_t y0 = __byte_perm(v[2][i], v[3][i], 0x5140), y1 = __byte_perm(v[2][i], v[3][i], 0x7362);
+        const uint32_t a0[4] = {e4m3x2_to_half((uint16_t)x0), e4m3x2_to_half((uint16_t)(x0 >> 16)),
+                                e4m3x2_to_half((uint16_t)y0), e4m3x2_to_half((uint16_t)(y0 >> 16))};
+        const uint32_t a1[4] = {e4m3x2_to_half((uint16_t)x1), e4m3x2_to_half((uint16_t)(x1 >> 16)),
+                                e4m3x2_to_half((uint16_t)y1), e4m3x2_to_half((uint16_t)(y1 >> 16))};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma_f16(O[nt][2 * i], a0, pf[nt][0], pf[nt][1]);
-        mma_f16(O[nt][2 * i + 1], a1, pf[nt][0], pf[nt][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16(O[nt][2 * i], a0, pf[f][nt][0], pf[f][nt][1]);
+          mma_f16(O[nt][2 * i + 1], a1, pf[f][nt][0], pf[f][nt][1]);
+        }
       }
     }
   }
@@ -491,24 +561,28 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
 }
 
 // Joins the parts of one row: out = sum_s w_s o_s / sum_s w_s with
-// w_s = 2^(lse_s - max lse).  A CTA per row, its warps over the parts.
-constexpr int kJoinWarps = 8;
-template <int D>
+// w_s = 2^(lse_s - max lse).  Many parts: a CTA per row, its eight warps over the
+// parts; few: a warp per row.
+constexpr int kJoinWarps = 8, kFewParts = 16;
+template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams p, int rows) {
   constexpr int V = D / 32;  // floats of a lane
-  __shared__ float s_o[kJoinWarps][D];
+  __shared__ float s_o[WPR > 1 ? WPR : 1][D];
   __shared__ float s_w[kJoinWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t unit = blockIdx.x / rows;
-  const int r = blockIdx.x % rows;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = WPR > 1 ? warp : 0;
+  const int64_t row = WPR > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kJoinWarps + warp;
+  const int64_t unit = row / rows;
+  const int r = (int)(row % rows);
   const int tile = (int)(unit % p.row_tiles);
   const int h = (int)(unit / p.row_tiles % p.H), b = (int)(unit / p.row_tiles / p.H);
   pdl_wait();
   pdl_trigger();
+  if (b >= p.B) return;
   const Sequence sq = sequence(p, b);
   const int rr = tile * rows + r;
   if (rr >= sq.kept * p.G || sq.kept * p.G > p.few_rows) return;
   const float *lse = p.part_lse + unit * p.splits * rows + r;
+  const float *src = p.part_o + (unit * p.splits * rows + r) * D + lane * V;
   float top = -INFINITY;
   for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, lse[(int64_t)s * rows]);
   top = warp_max(top);
@@ -517,44 +591,67 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
 #pragma unroll 4
-  for (int s = warp; s < p.splits; s += kJoinWarps) {
+  for (int s = part; s < p.splits; s += WPR) {
     const float w = exp2_approx(lse[(int64_t)s * rows] - z);
-    const float *src = p.part_o + ((unit * p.splits + s) * rows + r) * D + lane * V;
     W += w;
     uint32_t x[V];
-    load_words<V>(src, x);
+    load_words<V>(src + (int64_t)s * rows * D, x);
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = fmaf(w, __uint_as_float(x[i]), o[i]);
   }
+  uint16_t *dst = p.out + (int64_t)(sq.first + rr / p.G) * p.ldo + (int64_t)(h * p.G + rr % p.G) * D;
+  if constexpr (WPR > 1) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
-  if (lane == 0) s_w[warp] = W;
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    const int d = 2 * threadIdx.x;
-    float a = 0.0f, c = 0.0f, w = 0.0f;
+    for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
+    if (lane == 0) s_w[warp] = W;
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+      const int d = 2 * threadIdx.x;
+      float a = 0.0f, c = 0.0f, w = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) {
-      a += s_o[k][d];
-      c += s_o[k][d + 1];
-      w += s_w[k];
+      for (int k = 0; k < WPR; ++k) {
+        a += s_o[k][d];
+        c += s_o[k][d + 1];
+        w += s_w[k];
+      }
+      const float inv = w == 0.0f ? 0.0f : 1.0f / w;
+      *reinterpret_cast<uint32_t *>(dst + d) =
+          (uint32_t)f32_to_bf16_bits(a * inv) | ((uint32_t)f32_to_bf16_bits(c * inv) << 16);
     }
-    const float inv = w == 0.0f ? 0.0f : 1.0f / w;
-    uint16_t *dst = p.out + (int64_t)(sq.first + rr / p.G) * p.ldo + (int64_t)(h * p.G + rr % p.G) * D + d;
-    *reinterpret_cast<uint32_t *>(dst) =
-        (uint32_t)f32_to_bf16_bits(a * inv) | ((uint32_t)f32_to_bf16_bits(c * inv) << 16);
+  } else {
+    const float inv = W == 0.0f ? 0.0f : 1.0f / W;
+    if constexpr (V == 1) {
+      dst[lane] = f32_to_bf16_bits(o[0] * inv);
+    } else {
+      uint32_t x[V / 2];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i)
+        x[i] = (uint32_t)f32_to_bf16_bits(o[2 * i] * inv) | ((uint32_t)f32_to_bf16_bits(o[2 * i + 1] * inv) << 16);
+      store_words<V / 2>(dst + lane * V, x);
+    }
   }
 }
 
 template <int D, int NT>
 cudaError_t launch_nt(const SplitParams &p, int64_t units, cudaStream_t st) {
   using Geo = Geometry<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+  static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(k_attn_split<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   e = launch_kernel(k_attn_split<D, NT>, dim3((unsigned)(units * p.splits)), dim3(32 * kAttnWarps), Geo::kSmem, st, 1,
                     p);
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_kernel(k_attn_join<D>, dim3((unsigned)(units * Geo::kRows)), dim3(32 * kJoinWarps), 0, st, 1, p,
+  const int64_t rows = units * Geo::kRows;
+  if (p.splits <= kFewParts)
+    return launch_kernel(k_attn_join<D, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
+                         dim3(32 * kJoinWarps), 0, st, 1, p, (int)Geo::kRows);
+  return launch_kernel(k_attn_join<D, kJoinWarps>, dim3((unsigned)rows), dim3(32 * kJoinWarps), 0, st, 1, p,
                        (int)Geo::kRows);
 }
 template <int D>
@@ -596,12 +693,12 @@ AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64
   plan.row_tiles = (int)((rows + plan.rows - 1) / plan.rows);
   int64_t range = max_kv;
   if (window > 0 && window < max_kv) range = std::min(range, window + plan.rows / G + 1);
-  range += kTile - 1;  // the first part begins at a multiple of 16; the last one takes what is left
   const int64_t units = B * H * plan.row_tiles, slots = (int64_t)sms * (plan.rows == 8 ? 3 : 2);
   const int64_t fill = std::min((slots + units - 1) / units, (range + 127) / 128);
   const int64_t even = std::min((4 * slots + units - 1) / units, range / 1024);
   const int64_t want = std::max<int64_t>(1, std::max(fill, even));
-  constexpr int64_t step = kTile * kAttnWarps;
+  range += kAlign - 1;  // the first part begins at a multiple of 32; the last one takes what is left
+  constexpr int64_t step = kAlign * kAttnWarps;
   plan.chunk = std::max(step, (range + want * step - 1) / (want * step) * step);
   plan.splits = (int)std::max<int64_t>(1, (range + plan.chunk - 1) / plan.chunk);
   plan.ws_bytes = plan.splits > 1 ? (size_t)(units * plan.splits * plan.rows * (D + 1) * 4) : 0;
