@@ -65,11 +65,42 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same with sums that start at (c0, c1) in both rows.
+__device__ __forceinline__ void mma_f16_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                             float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+// base + i * step (one instruction).
+__device__ __forceinline__ const uint8_t *step_from(const uint8_t *base, uint32_t step, uint32_t i) {
+  uint64_t r;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(r) : "r"(step), "r"(i), "l"(reinterpret_cast<uint64_t>(base)));
+  return reinterpret_cast<const uint8_t *>(r);
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
+// N consecutive floats of shared memory (aligned to 4 min(N, 4) bytes).
+template <int N>
+__device__ __forceinline__ void load_shared(float (&v)[N], const float *p) {
+  if constexpr (N == 1) {
+    v[0] = *p;
+  } else if constexpr (N == 2) {
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    v[0] = x.x, v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(p + i);
+      v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+    }
+  }
+}
+
 template <int D, int NT>
 struct Geometry {
   static constexpr int kTile = D >= 256 ? 16 : 32;  // positions a warp handles at once
@@ -227,6 +258,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   };
   const int piece_row = lane / Geo::kChunks, piece = lane % Geo::kChunks;
   const int64_t row_bytes = (int64_t)p.H * D;
+  const uint32_t step_bytes = (uint32_t)(Geo::kRowStep * row_bytes);  // at most 16 * 4096 * 256
   const int64_t lane_off = piece_row * row_bytes + (int64_t)h * D + piece * 16;
   uint32_t sc[(kGroups + 1) / 2];  // the lane's scales of the tile issued last
   uint32_t sv = 0;
@@ -247,15 +279,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     if (whole(n) && (unsigned)blk < (unsigned)p.num_blocks) {
       // one page: rows at one distance
       const int64_t slot = (int64_t)blk * p.block_size + (j0 - block_of(p, j0) * p.block_size);
-      const int64_t off = slot * row_bytes + lane_off, step = Geo::kRowStep * row_bytes;
+      const int64_t off = slot * row_bytes + lane_off;
       const uint8_t *k = p.kc + off, *v = p.vc + off;
 #pragma unroll
       for (int i = 0; i < Geo::kPieces; ++i) {
         const int r = i * Geo::kRowStep + piece_row;
-        cp_async16(at + r * D + key_chunk<D>(r, piece) * 16, k);
-        cp_async16(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, v);
-        k += step;
-        v += step;
+        cp_async16(at + r * D + key_chunk<D>(r, piece) * 16, step_from(k, step_bytes, i));
+        cp_async16(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, step_from(v, step_bytes, i));
       }
       if (kTile == 32 || lane < kTile) load_scales((slot + own) * p.H + h);
       there = ~0u >> (32 - kTile);
@@ -319,8 +349,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
       const int r0 = 16 * f + g, r1 = r0 + 8;
       vs[f][0] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r0];
       vs[f][1] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r1];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) S[f][nt][0] = S[f][nt][1] = S[f][nt][2] = S[f][nt][3] = 0.0f;
+      float ks[2][kGroups];
+      load_shared<kGroups>(ks[0], reinterpret_cast<const float *>(stage + Geo::kScaleAt) + r0 * kGroups);
+      load_shared<kGroups>(ks[1], reinterpret_cast<const float *>(stage + Geo::kScaleAt) + r1 * kGroups);
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
         uint32_t w0[2], w1[2];
@@ -330,26 +361,23 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(a1));
         float acc[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          acc[nt][0] = acc[nt][2] = qoff[nt][k][0];
-          acc[nt][1] = acc[nt][3] = qoff[nt][k][1];
-        }
-#pragma unroll
         for (int j = 0; j < 2; ++j) {
           uint32_t a[4];
           int8x4_to_offset_half(w0[j], a[0], a[2]);
           int8x4_to_offset_half(w1[j], a[1], a[3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a, qf[nt][k][2 * j], qf[nt][k][2 * j + 1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if (j == 0) mma_f16_from(acc[nt], a, qf[nt][k][0], qf[nt][k][1], qoff[nt][k][0], qoff[nt][k][1]);
+            else mma_f16(acc[nt], a, qf[nt][k][2], qf[nt][k][3]);
+          }
         }
-        const float k0 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[r0 * kGroups + k];
-        const float k1 = reinterpret_cast<const float *>(stage + Geo::kScaleAt)[r1 * kGroups + k];
+        const float k0 = ks[0][k], k1 = ks[1][k];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          S[f][nt][0] = fmaf(acc[nt][0], k0, S[f][nt][0]);
-          S[f][nt][1] = fmaf(acc[nt][1], k0, S[f][nt][1]);
-          S[f][nt][2] = fmaf(acc[nt][2], k1, S[f][nt][2]);
-          S[f][nt][3] = fmaf(acc[nt][3], k1, S[f][nt][3]);
+          S[f][nt][0] = k ? fmaf(acc[nt][0], k0, S[f][nt][0]) : acc[nt][0] * k0;
+          S[f][nt][1] = k ? fmaf(acc[nt][1], k0, S[f][nt][1]) : acc[nt][1] * k0;
+          S[f][nt][2] = k ? fmaf(acc[nt][2], k1, S[f][nt][2]) : acc[nt][2] * k1;
+          S[f][nt][3] = k ? fmaf(acc[nt][3], k1, S[f][nt][3]) : acc[nt][3] * k1;
         }
       }
 #pragma unroll
