@@ -156,8 +156,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const int64_t unit = cta / p.splits;
   const int tile = (int)(unit % p.row_tiles);
   const int h = (int)(unit / p.row_tiles % p.H), b = (int)(unit / p.row_tiles / p.H);
+  const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
+  const int own = lane & (kTile - 1);  // the position of a tile whose scales (and page) a lane sees to
+  const bool even = p.block_size % kTile == 0;  // a tile lies in one page
   pdl_wait();
   pdl_trigger();
+  // without a window a part's first position does not wait for the sequence's counts: nor does its page
+  const int64_t guess = (int64_t)split * p.chunk + warp * kTile + (even ? 0 : own);
+  int guessed = -1;
+  if (p.window == 0 && guess < p.max_kv && block_of(p, (int)guess) < p.max_blocks)
+    guessed = __ldg(table + block_of(p, (int)guess));
   const Sequence sq = sequence(p, b);
   if (sq.broken && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
   const int R = sq.kept * p.G, r0 = tile * kRows;
@@ -173,6 +181,92 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     const int64_t from = (int64_t)(lo & ~(kAlign - 1)) + (int64_t)split * p.chunk;
     beg = (int)min(from, (int64_t)max(hi, 0));
     end = split == p.splits - 1 ? max(hi, beg) : (int)min(from + p.chunk, (int64_t)max(hi, beg));
+  }
+
+  // ---- the ring: tile n covers positions beg + (n * warps + warp) * 16 ...
+  const int tiles = (end - beg + kTile - 1) / kTile;  // beg is a multiple of it
+  const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
+  const auto first_of = [&](int n) { return beg + (n * kAttnWarps + warp) * kTile; };
+  const auto whole = [&](int n) { return even && n < mine && first_of(n) >= lo && first_of(n) + kTile <= end; };
+  const auto page = [&](int n) {  // page of the lane's position of tile n (-1: none)
+    const int j = first_of(n) + (even ? 0 : own);
+    return n < mine && (whole(n) || (j + (even ? own : 0) >= lo && j + (even ? own : 0) < end))
+               ? __ldg(table + block_of(p, j)) : -1;
+  };
+  const int piece_row = lane / Geo::kChunks, piece = lane % Geo::kChunks;
+  const int64_t row_bytes = (int64_t)p.H * D;
+  const uint32_t step_bytes = (uint32_t)(Geo::kRowStep * row_bytes);  // at most 16 * 4096 * 256
+  const int64_t lane_off = piece_row * row_bytes + (int64_t)h * D + piece * 16;
+  uint32_t sc[(kGroups + 1) / 2];  // the lane's scales of the tile issued last
+  uint32_t sv = 0;
+  unsigned there = 0;  // which positions of that tile are there
+  int next_page = p.window == 0 && mine > 0 ? guessed : page(0);
+  const auto load_scales = [&](int64_t row) {  // row: (slot, head) of the lane's position
+    sv = __ldg(p.vs + row);
+    if constexpr (kGroups == 1) {
+      sc[0] = __ldg(p.ks + row);
+    } else {
+      load_words<kGroups / 2>(p.ks + row * kGroups, sc);
+    }
+  };
+  const auto issue = [&](int n) {
+    const int blk = next_page, j0 = first_of(n);
+    next_page = page(n + 1);
+    const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
+    if (whole(n) && (unsigned)blk < (unsigned)p.num_blocks) {
+      // one page: rows at one distance
+      const int64_t slot = (int64_t)blk * p.block_size + (j0 - block_of(p, j0) * p.block_size);
+      const int64_t off = slot * row_bytes + lane_off;
+      const uint8_t *k = p.kc + off, *v = p.vc + off;
+#pragma unroll
+      for (int i = 0; i < Geo::kPieces; ++i) {
+        const int r = i * Geo::kRowStep + piece_row;
+        cp_async16(at + r * D + key_chunk<D>(r, piece) * 16, step_from(k, step_bytes, i));
+        cp_async16(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, step_from(v, step_bytes, i));
+      }
+      if (kTile == 32 || lane < kTile) load_scales((slot + own) * p.H + h);
+      there = ~0u >> (32 - kTile);
+    } else if (n < mine) {
+      // positions that are not there (before lo, from end on, without a page): zeros
+      const int j = j0 + own;
+      const bool wanted = j >= lo && j < end, ok = wanted && (unsigned)blk < (unsigned)p.num_blocks;
+      if (wanted && !ok && lane < kTile) set_status(p.status, QLIN_ERR_INVALID_ARG);
+      const int64_t row = ok ? ((int64_t)blk * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
+      there = __ballot_sync(~0u, ok) & (~0u >> (32 - kTile));
+#pragma unroll 1
+      for (int i = 0; i < Geo::kPieces; ++i) {
+        const int r = i * Geo::kRowStep + piece_row;
+        const int64_t off = __shfl_sync(~0u, row, r) * D + piece * 16;
+        const bool fill = !((there >> r) & 1);
+        cp_async16_or_zero(at + r * D + key_chunk<D>(r, piece) * 16, p.kc + off, fill);
+        cp_async16_or_zero(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, p.vc + off, fill);
+      }
+      sv = 0;
+#pragma unroll
+      for (int k = 0; k < (kGroups + 1) / 2; ++k) sc[k] = 0;
+      if (ok && lane < kTile) load_scales(row);
+    }
+    cp_async_commit();
+  };
+  // the scales of the tile issued last, as fp32, into its stage
+  const auto put_scales = [&](int n) {
+    if (n >= mine) return;
+    uint8_t *at = ring + (n % kStages) * Geo::kStageBytes;
+    const float v = half_bits_to_f32((uint16_t)sv);
+    const unsigned top = __reduce_max_sync(~0u, min(__float_as_uint(fabsf(v)), 0x7F7FFFFFu));
+    if (kTile == 32 || lane < kTile) {
+      float *k = reinterpret_cast<float *>(at + Geo::kScaleAt) + lane * kGroups;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) k[i] = half_bits_to_f32((uint16_t)(sc[i / 2] >> (16 * (i & 1))));
+      reinterpret_cast<float *>(at + Geo::kVScaleAt)[lane] = v;
+    }
+    if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(there, top);
+  };
+
+  // the first tiles are on their way while q arrives
+  for (int n = 0; n < kStages - 1; ++n) {
+    issue(n);
+    if (n < kStages - 2) put_scales(n);
   }
 
   // q: row 8*nt + g, as the second operand; its largest magnitude becomes 2^14..2^15
@@ -243,93 +337,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   }
   int vexp = -1000;  // O is sum p v 2^-vexp
 
-  // ---- the ring: tile n covers positions beg + (n * warps + warp) * 16 ...
-  const int tiles = (end - beg + kTile - 1) / kTile;  // beg is a multiple of it
-  const int mine = tiles > warp ? (tiles - warp + kAttnWarps - 1) / kAttnWarps : 0;
-  const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
-  const int own = lane & (kTile - 1);  // the position of a tile whose scales (and page) a lane sees to
-  const bool even = p.block_size % kTile == 0;  // a tile lies in one page
-  const auto first_of = [&](int n) { return beg + (n * kAttnWarps + warp) * kTile; };
-  const auto whole = [&](int n) { return even && n < mine && first_of(n) >= lo && first_of(n) + kTile <= end; };
-  const auto page = [&](int n) {  // page of the lane's position of tile n (-1: none)
-    const int j = first_of(n) + (even ? 0 : own);
-    return n < mine && (whole(n) || (j + (even ? own : 0) >= lo && j + (even ? own : 0) < end))
-               ? __ldg(table + block_of(p, j)) : -1;
-  };
-  const int piece_row = lane / Geo::kChunks, piece = lane % Geo::kChunks;
-  const int64_t row_bytes = (int64_t)p.H * D;
-  const uint32_t step_bytes = (uint32_t)(Geo::kRowStep * row_bytes);  // at most 16 * 4096 * 256
-  const int64_t lane_off = piece_row * row_bytes + (int64_t)h * D + piece * 16;
-  uint32_t sc[(kGroups + 1) / 2];  // the lane's scales of the tile issued last
-  uint32_t sv = 0;
-  unsigned there = 0;  // which positions of that tile are there
-  int next_page = page(0);
-  const auto load_scales = [&](int64_t row) {  // row: (slot, head) of the lane's position
-    sv = __ldg(p.vs + row);
-    if constexpr (kGroups == 1) {
-      sc[0] = __ldg(p.ks + row);
-    } else {
-      load_words<kGroups / 2>(p.ks + row * kGroups, sc);
-    }
-  };
-  const auto issue = [&](int n) {
-    const int blk = next_page, j0 = first_of(n);
-    next_page = page(n + 1);
-    const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
-    if (whole(n) && (unsigned)blk < (unsigned)p.num_blocks) {
-      // one page: rows at one distance
-      const int64_t slot = (int64_t)blk * p.block_size + (j0 - block_of(p, j0) * p.block_size);
-      const int64_t off = slot * row_bytes + lane_off;
-      const uint8_t *k = p.kc + off, *v = p.vc + off;
-#pragma unroll
-      for (int i = 0; i < Geo::kPieces; ++i) {
-        const int r = i * Geo::kRowStep + piece_row;
-        cp_async16(at + r * D + key_chunk<D>(r, piece) * 16, step_from(k, step_bytes, i));
-        cp_async16(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, step_from(v, step_bytes, i));
-      }
-      if (kTile == 32 || lane < kTile) load_scales((slot + own) * p.H + h);
-      there = ~0u >> (32 - kTile);
-    } else if (n < mine) {
-      // positions that are not there (before lo, from end on, without a page): zeros
-      const int j = j0 + own;
-      const bool wanted = j >= lo && j < end, ok = wanted && (unsigned)blk < (unsigned)p.num_blocks;
-      if (wanted && !ok && lane < kTile) set_status(p.status, QLIN_ERR_INVALID_ARG);
-      const int64_t row = ok ? ((int64_t)blk * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
-      there = __ballot_sync(~0u, ok) & (~0u >> (32 - kTile));
-#pragma unroll 1
-      for (int i = 0; i < Geo::kPieces; ++i) {
-        const int r = i * Geo::kRowStep + piece_row;
-        const int64_t off = __shfl_sync(~0u, row, r) * D + piece * 16;
-        const bool fill = !((there >> r) & 1);
-        cp_async16_or_zero(at + r * D + key_chunk<D>(r, piece) * 16, p.kc + off, fill);
-        cp_async16_or_zero(at + Geo::kCodes + r * D + value_chunk<D>(r, piece) * 16, p.vc + off, fill);
-      }
-      sv = 0;
-#pragma unroll
-      for (int k = 0; k < (kGroups + 1) / 2; ++k) sc[k] = 0;
-      if (ok && lane < kTile) load_scales(row);
-    }
-    cp_async_commit();
-  };
-  // the scales of the tile issued last, as fp32, into its stage
-  const auto put_scales = [&](int n) {
-    if (n >= mine) return;
-    uint8_t *at = ring + (n % kStages) * Geo::kStageBytes;
-    const float v = half_bits_to_f32((uint16_t)sv);
-    const unsigned top = __reduce_max_sync(~0u, min(__float_as_uint(fabsf(v)), 0x7F7FFFFFu));
-    if (kTile == 32 || lane < kTile) {
-      float *k = reinterpret_cast<float *>(at + Geo::kScaleAt) + lane * kGroups;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) k[i] = half_bits_to_f32((uint16_t)(sc[i / 2] >> (16 * (i & 1))));
-      reinterpret_cast<float *>(at + Geo::kVScaleAt)[lane] = v;
-    }
-    if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(there, top);
-  };
-
-  for (int n = 0; n < kStages - 1; ++n) {
-    issue(n);
-    if (n < kStages - 2) put_scales(n);
-  }
   for (int n = 0; n < mine; ++n) {
     cp_async_wait<kStages - 2>();
     put_scales(n + kStages - 2);
@@ -589,16 +596,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
 }
 
 // Joins the parts of one row: out = sum_s w_s o_s / sum_s w_s with
-// w_s = 2^(lse_s - max lse).  Many parts: a CTA per row, its eight warps over the
-// parts; few: a warp per row.
-constexpr int kJoinWarps = 8, kFewParts = 16;
-template <int D, int WPR>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams p, int rows) {
-  constexpr int V = D / 32;  // floats of a lane
-  __shared__ float s_o[WPR > 1 ? WPR : 1][D];
-  __shared__ float s_w[kJoinWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = WPR > 1 ? warp : 0;
-  const int64_t row = WPR > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kJoinWarps + warp;
+// w_s = 2^(lse_s - max lse).  Many parts: a CTA per row, its warps over the parts;
+// few: a warp per row.
+constexpr int kFewParts = 16;
+constexpr int kManyWarps = 16, kFewWarps = 8;  // warps of a CTA
+template <int D, bool MANY>
+__global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_join(const SplitParams p, int rows) {
+  constexpr int V = D / 32;                  // floats of a lane
+  constexpr int kOver = MANY ? kManyWarps : 1;  // warps that share a row
+  constexpr int kBatch = MANY ? 8 : 4;       // parts whose loads are in flight at once
+  __shared__ float s_o[kOver][D];
+  __shared__ float s_w[kOver];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = MANY ? warp : 0;
+  const int64_t row = MANY ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kFewWarps + warp;
   const int64_t unit = row / rows;
   const int r = (int)(row % rows);
   const int tile = (int)(unit % p.row_tiles);
@@ -611,24 +621,42 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams
   if (rr >= sq.kept * p.G || sq.kept * p.G > p.few_rows) return;
   const float *lse = p.part_lse + unit * p.splits * rows + r;
   const float *src = p.part_o + (unit * p.splits * rows + r) * D + lane * V;
+  uint32_t x[kBatch][V];
+  float e[kBatch];
+  const auto load = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t s = s0 + i * kOver;
+      e[i] = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[i][v] = 0u;
+      if (s < p.splits) {
+        e[i] = __ldg(lse + s * rows);
+        load_words<V>(src + s * rows * D, x[i]);
+      }
+    }
+  };
+  load(part);
   float top = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, lse[(int64_t)s * rows]);
+  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, __ldg(lse + (int64_t)s * rows));
   top = warp_max(top);
   const float z = top == -INFINITY ? 0.0f : top;
   float o[V], W = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
-#pragma unroll 4
-  for (int s = part; s < p.splits; s += WPR) {
-    const float w = exp2_approx(lse[(int64_t)s * rows] - z);
-    W += w;
-    uint32_t x[V];
-    load_words<V>(src + (int64_t)s * rows * D, x);
+  for (int s0 = part; s0 < p.splits;) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(w, __uint_as_float(x[i]), o[i]);
+    for (int i = 0; i < kBatch; ++i) {
+      const float w = exp2_approx(e[i] - z);  // 0 beyond the last part
+      W += w;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = fmaf(w, __uint_as_float(x[i][v]), o[v]);
+    }
+    s0 += kBatch * kOver;
+    if (s0 < p.splits) load(s0);
   }
   uint16_t *dst = p.out + (int64_t)(sq.first + rr / p.G) * p.ldo + (int64_t)(h * p.G + rr % p.G) * D;
-  if constexpr (WPR > 1) {
+  if constexpr (MANY) {
 #pragma unroll
     for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
     if (lane == 0) s_w[warp] = W;
@@ -637,7 +665,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams
       const int d = 2 * threadIdx.x;
       float a = 0.0f, c = 0.0f, w = 0.0f;
 #pragma unroll
-      for (int k = 0; k < WPR; ++k) {
+      for (int k = 0; k < kOver; ++k) {
         a += s_o[k][d];
         c += s_o[k][d + 1];
         w += s_w[k];
@@ -651,11 +679,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_join(const SplitParams
     if constexpr (V == 1) {
       dst[lane] = f32_to_bf16_bits(o[0] * inv);
     } else {
-      uint32_t x[V / 2];
+      uint32_t w[V / 2];
 #pragma unroll
       for (int i = 0; i < V / 2; ++i)
-        x[i] = (uint32_t)f32_to_bf16_bits(o[2 * i] * inv) | ((uint32_t)f32_to_bf16_bits(o[2 * i + 1] * inv) << 16);
-      store_words<V / 2>(dst + lane * V, x);
+        w[i] = (uint32_t)f32_to_bf16_bits(o[2 * i] * inv) | ((uint32_t)f32_to_bf16_bits(o[2 * i + 1] * inv) << 16);
+      store_words<V / 2>(dst + lane * V, w);
     }
   }
 }
@@ -677,9 +705,9 @@ cudaError_t launch_nt(const SplitParams &p, int64_t units, cudaStream_t st) {
   if (e != cudaSuccess || p.splits == 1) return e;
   const int64_t rows = units * Geo::kRows;
   if (p.splits <= kFewParts)
-    return launch_kernel(k_attn_join<D, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
-                         dim3(32 * kJoinWarps), 0, st, 1, p, (int)Geo::kRows);
-  return launch_kernel(k_attn_join<D, kJoinWarps>, dim3((unsigned)rows), dim3(32 * kJoinWarps), 0, st, 1, p,
+    return launch_kernel(k_attn_join<D, false>, dim3((unsigned)((rows + kFewWarps - 1) / kFewWarps)),
+                         dim3(32 * kFewWarps), 0, st, 1, p, (int)Geo::kRows);
+  return launch_kernel(k_attn_join<D, true>, dim3((unsigned)rows), dim3(32 * kManyWarps), 0, st, 1, p,
                        (int)Geo::kRows);
 }
 template <int D>
