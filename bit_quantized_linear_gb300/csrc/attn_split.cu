@@ -43,6 +43,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAlign = 32;   // parts begin at multiples of this: the most positions a warp handles at once
 
 struct SplitParams : AttnDev {
+  unsigned group_inverse;  // 2^16 / G rounded up: (x * it) >> 16 is x / G for x < 256 (G <= 128)
   float *part_o, *part_lse;
   int64_t chunk;
   int row_tiles, splits;
@@ -171,13 +172,32 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const int R = sq.kept * p.G, r0 = tile * kRows;
   if (r0 >= R || R > p.few_rows) return;
 
+  // token and head of row r0 + i: one division for the tile
+  const int tok0 = r0 / p.G, head0 = r0 - tok0 * p.G;
+  const auto token_of = [&](int i) { return tok0 + (int)(((unsigned)(head0 + i) * p.group_inverse) >> 16); };
+  // q is asked for before the codes, which would keep it waiting
+  uint4 qw[NT][kGroups];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int i = nt * 8 + g, tok = token_of(i);
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      qw[nt][k] = make_uint4(0, 0, 0, 0);
+      if (r0 + i < R) {
+        const uint16_t *row = p.q + (int64_t)(sq.first + tok) * p.ldq +
+                              (int64_t)(h * p.G + r0 + i - tok * p.G) * D + k * 32 + t * 8;
+        qw[nt][k] = __ldg(reinterpret_cast<const uint4 *>(row));
+      }
+    }
+  }
+
   // positions of this CTA: what any of its rows sees, cut into parts
-  const int last = min(r0 + kRows, R) - 1;
+  const int last = min(kRows, R - r0) - 1;
   int lo, hi, beg, end;
   {
     int unused;
-    sees(p, sq, r0 / p.G, lo, unused);
-    sees(p, sq, last / p.G, unused, hi);
+    sees(p, sq, tok0, lo, unused);
+    sees(p, sq, token_of(last), unused, hi);
     const int64_t from = (int64_t)(lo & ~(kAlign - 1)) + (int64_t)split * p.chunk;
     beg = (int)min(from, (int64_t)max(hi, 0));
     end = split == p.splits - 1 ? max(hi, beg) : (int)min(from + p.chunk, (int64_t)max(hi, beg));
@@ -277,18 +297,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   int all_lo = lo, all_hi = hi;  // positions every row sees
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = r0 + nt * 8 + g;
-    uint4 w[kGroups];
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-      w[k] = make_uint4(0, 0, 0, 0);
-      if (r < R) {
-        const uint16_t *row =
-            p.q + (int64_t)(sq.first + r / p.G) * p.ldq + (int64_t)(h * p.G + r % p.G) * D + k * 32 + t * 8;
-        w[k] = *reinterpret_cast<const uint4 *>(row);
-      }
-      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      const uint32_t u[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     const float up = pow2i(14 - e), factor = p.scale_log2 * pow2i(max(e - 14, -126));
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
-      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      const uint32_t u[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         qf[nt][k][j] = half2_of(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
@@ -317,9 +329,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       cf[nt][c] = __shfl_sync(~0u, factor, (2 * t + c) * 4);
-      const int rc = r0 + nt * 8 + 2 * t + c;
+      const int i = nt * 8 + 2 * t + c;
       vlo[nt][c] = lo, vhi[nt][c] = hi;  // columns without a row see everything (their q is 0)
-      if (rc < R) sees(p, sq, rc / p.G, vlo[nt][c], vhi[nt][c]);
+      if (r0 + i < R) sees(p, sq, token_of(i), vlo[nt][c], vhi[nt][c]);
       all_lo = max(all_lo, vlo[nt][c]);
       all_hi = min(all_hi, vhi[nt][c]);
     }
@@ -766,6 +778,7 @@ cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, int 
                               cudaStream_t st) {
   SplitParams p{};
   static_cast<AttnDev &>(p) = attn_dev(a, few_rows, status);
+  p.group_inverse = (65536u + p.G - 1) / p.G;
   p.row_tiles = plan.row_tiles, p.splits = plan.splits, p.chunk = plan.chunk;
   const int64_t units = a.B * a.H * plan.row_tiles;
   p.part_o = (float *)ws;
