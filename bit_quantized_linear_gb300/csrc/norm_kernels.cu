@@ -16,11 +16,14 @@
 //
 // One pass: a row's vectors stay in registers between the sum and the output
 // (and, for per-token scales, between the output's maximum and its codes).  A
-// row is shared by `wpr` warps.  Bound by HBM: x, residual and h_out are 2
-// bytes an element, the output 1 or 2.  The arithmetic is close behind, so it
-// runs on pairs of elements as packed binary32 operations (the same roundings,
-// lane by lane): at 8192 x 2048 with static E4M3 codes that took the kernel from
-// 29.0 us to what the launcher's comment gives.
+// row is the work of `lanes` lanes (short rows: several to a warp) or of `wpr`
+// whole warps.  Bound by HBM: x, residual and h_out are 2 bytes an element, the
+// output 1 or 2.  With codes the arithmetic is close behind, so it runs on pairs
+// of elements as packed binary32 operations (the same roundings, lane by lane),
+// and a CTA walks over rows: the weights are unpacked once, and the next row is on
+// its way while this one is worked on (8192 x 2048 E4M3: 25.6 us without, 22.9
+// with).  BF16 output has arithmetic to spare and gains more from whole rows in
+// flight (32640 x 3584: 146 us walking, 134 not).
 #include "common.cuh"
 #include "kernels.h"
 #include "kv_quant.cuh"
@@ -34,6 +37,7 @@ namespace {
 constexpr int kMaxWarpsPerRow = 16;
 constexpr int kMaxVecs = 8;       // 16-byte vectors of a row a thread holds
 constexpr int kWarpsPerCta = 8;
+constexpr int kCtaWarps = 16;     // warps of an SM the registers are budgeted for
 
 // hi + lo, an unevaluated sum.
 struct TwoFloat {
@@ -101,7 +105,9 @@ __device__ __forceinline__ float rms_reciprocal(TwoFloat S, TwoFloat inv_k, floa
 struct RmsParams {
   const uint16_t *x, *res, *w;
   int64_t ldx, ldr, M;
-  int K8, wpr;  // vectors of a row, warps per row
+  int K8;                     // vectors of a row
+  int lanes, lanes_log2;      // its lanes of a warp (32 for more than one warp)
+  int wpr, wpr_log2;          // its warps
   double eps64, inv_k64;
   float eps;
   TwoFloat inv_k;
@@ -166,154 +172,178 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return bf16x2_of(f32x2_add(f32x2_of(a), f32x2_of(b)));
 }
 
-// y of one vector, pair by pair: fl32(fl32(h * r) * w).
-__device__ __forceinline__ void normed8(const uint4 &h, const uint4 &w, uint64_t r2, uint64_t (&y)[4]) {
-  const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = f32x2_mul(f32x2_mul(f32x2_of(hw[j]), r2), f32x2_of(ww[j]));
-}
+// Eight BF16 values of a row as a thread keeps them: as binary32 pairs where the
+// registers allow (up to four vectors a thread), else packed.
+template <bool WIDE>
+struct Values;
+template <>
+struct Values<true> {
+  uint64_t v[4];
+  __device__ __forceinline__ void set(const uint4 &p) {
+    v[0] = f32x2_of(p.x), v[1] = f32x2_of(p.y), v[2] = f32x2_of(p.z), v[3] = f32x2_of(p.w);
+  }
+  __device__ __forceinline__ uint64_t pair(int j) const { return v[j]; }
+};
+template <>
+struct Values<false> {
+  uint4 p;
+  __device__ __forceinline__ void set(const uint4 &q) { p = q; }
+  __device__ __forceinline__ uint64_t pair(int j) const {
+    return f32x2_of(j == 0 ? p.x : j == 1 ? p.y : j == 2 ? p.z : p.w);
+  }
+};
 
 template <int NV, int OUT, bool DYN>
 __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParams p) {
-  __shared__ TwoFloat s_sum[kMaxWarpsPerRow];
+  constexpr bool kWalk = NV <= 4 && OUT != kNormBf16;
+  using V = Values<kWalk>;
+  __shared__ TwoFloat s_sum[2][kMaxWarpsPerRow];  // by turns: one barrier a row may be all that parts two rows
   __shared__ double s_sum64[kMaxWarpsPerRow];
   __shared__ float s_max[kMaxWarpsPerRow];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = warp / p.wpr, sub = warp % p.wpr, first = group * p.wpr;
-  const int64_t m = (int64_t)blockIdx.x * ((blockDim.x >> 5) / p.wpr) + group;
+  const int group = warp >> p.wpr_log2, sub = warp & (p.wpr - 1), first = group << p.wpr_log2;
+  const int in_row = lane & (p.lanes - 1);
   // the warps of one row meet at a barrier of their own
   const auto row_barrier = [&] {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "r"(p.wpr * 32) : "memory");
   };
-  if (m >= p.M) return;
+  const int at_once = (int)blockDim.x >> (p.wpr_log2 + p.lanes_log2);  // rows of a CTA
+  const int64_t step = (int64_t)gridDim.x * at_once;
+  // a warp's rows leave the loop together: those beyond the last are worked on and not stored
+  const int of_warp = lane >> p.lanes_log2;
+  int64_t m = (int64_t)blockIdx.x * at_once + (group << (5 - p.lanes_log2)) + of_warp;
+  const int index0 = (sub << p.lanes_log2) + in_row, index_step = p.wpr << p.lanes_log2;
+  const auto index = [&](int i) { return index0 + i * index_step; };
 
-  uint4 w[NV], h[NV];
+  V w[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = (i * p.wpr + sub) * 32 + lane;
-    w[i] = v < p.K8 ? __ldg(reinterpret_cast<const uint4 *>(p.w) + v) : make_uint4(0, 0, 0, 0);
-  }
+  for (int i = 0; i < NV; ++i)
+    w[i].set(index(i) < p.K8 ? __ldg(reinterpret_cast<const uint4 *>(p.w) + index(i)) : make_uint4(0, 0, 0, 0));
   pdl_wait();
   pdl_trigger();
-  const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + m * p.ldx);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = (i * p.wpr + sub) * 32 + lane;
-    h[i] = v < p.K8 ? xr[v] : make_uint4(0, 0, 0, 0);
-  }
-  if (p.res) {
-    const uint4 *rr = reinterpret_cast<const uint4 *>(p.res + m * p.ldr);
-    uint4 *ho = reinterpret_cast<uint4 *>(p.h_out) + m * p.K8;
-    uint4 r[NV];
+  uint4 x[NV], r4[NV];
+  const auto load = [&](int64_t row) {
+    const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + row * p.ldx);
+    const uint4 *rr = reinterpret_cast<const uint4 *>(p.res + row * p.ldr);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = (i * p.wpr + sub) * 32 + lane;
-      r[i] = v < p.K8 ? rr[v] : make_uint4(0, 0, 0, 0);
+      const bool ok = row < p.M && index(i) < p.K8;
+      x[i] = ok ? xr[index(i)] : make_uint4(0, 0, 0, 0);
+      if (p.res) r4[i] = ok ? rr[index(i)] : make_uint4(0, 0, 0, 0);
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = (i * p.wpr + sub) * 32 + lane;
-      h[i] = make_uint4(add_bf16x2(h[i].x, r[i].x), add_bf16x2(h[i].y, r[i].y), add_bf16x2(h[i].z, r[i].z),
-                        add_bf16x2(h[i].w, r[i].w));
-      if (v < p.K8) ho[v] = h[i];
-    }
-  }
-
-  // sum of squares
-  TwoFloat2 S2{0, 0};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t hw[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t a = f32x2_of(hw[j]);
-      add_values(S2, f32x2_mul(a, a));
-    }
-  }
-  TwoFloat S{f32x2_lo(S2.hi), f32x2_lo(S2.lo)};
-  add_pair(S, TwoFloat{f32x2_hi(S2.hi), f32x2_hi(S2.lo)});
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
-  if (p.wpr > 1) {
-    if (lane == 0) s_sum[warp] = S;
-    row_barrier();
-    S = lane < p.wpr ? s_sum[first + lane] : TwoFloat{0.0f, 0.0f};
-#pragma unroll
-    for (int o = kMaxWarpsPerRow / 2; o > 0; o >>= 1)
-      add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
-    S.hi = __shfl_sync(~0u, S.hi, 0);  // lanes 16..31 hold no partial sums
-    S.lo = __shfl_sync(~0u, S.lo, 0);
-  }
-  float r;
-  if (S.hi >= 0x1p-80f && S.hi < 0x1p126f) {
-    r = rms_reciprocal(S, p.inv_k, p.eps);
-  } else {
-    // squares beyond binary32 (or an all-zero row): the same sum in FP64
-    double d = 0.0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t hw[4] = {h[i].x, h[i].y, h[i].z, h[i].w};
-#pragma unroll 1
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t u = hw[j >> 1];
-        const double a = (double)__uint_as_float(j & 1 ? u & 0xFFFF0000u : u << 16);
-        d += a * a;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(~0u, d, o);
-    if (p.wpr > 1) {
-      if (lane == 0) s_sum64[warp] = d;
-      row_barrier();
-      d = 0.0;
-      for (int i = 0; i < p.wpr; ++i) d += s_sum64[first + i];
-    }
-    r = (float)(1.0 / sqrt(d * p.inv_k64 + p.eps64));
-  }
-
-  const uint64_t r2 = f32x2_pack(r, r);
-  if constexpr (OUT == kNormBf16) {
-    uint4 *yo = reinterpret_cast<uint4 *>(p.y) + m * p.K8;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = (i * p.wpr + sub) * 32 + lane;
-      uint64_t y[4];
-      normed8(h[i], w[i], r2, y);
-      if (v < p.K8) yo[v] = make_uint4(bf16x2_of(y[0]), bf16x2_of(y[1]), bf16x2_of(y[2]), bf16x2_of(y[3]));
-    }
-  } else {
-    float s;
-    if constexpr (DYN) {
-      float amax = 0.0f;
+  };
+  load(m);
+  for (int turn = 0; m - of_warp < p.M; m += step, turn ^= 1) {
+    const bool stored = m < p.M;
+    V h[NV];
+    if (p.res) {
+      uint4 *ho = reinterpret_cast<uint4 *>(p.h_out) + m * p.K8;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        uint64_t y[4];
-        normed8(h[i], w[i], r2, y);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(f32x2_lo(y[j])), fabsf(f32x2_hi(y[j]))));
+        const uint4 s = make_uint4(add_bf16x2(x[i].x, r4[i].x), add_bf16x2(x[i].y, r4[i].y),
+                                   add_bf16x2(x[i].z, r4[i].z), add_bf16x2(x[i].w, r4[i].w));
+        if (stored && index(i) < p.K8) ho[index(i)] = s;
+        h[i].set(s);
       }
-      amax = warp_max(amax);
-      if (p.wpr > 1) {
-        if (lane == 0) s_max[warp] = amax;
-        row_barrier();
-        amax = warp_max(lane < p.wpr ? s_max[first + lane] : 0.0f);
-      }
-      s = __fdiv_rn(amax, OUT == kNormInt8 ? kQmaxInt8 : kQmaxE4m3);
-      s = s > 0.0f ? s : 1.0f;
-      if (sub == 0 && lane == 0) p.x_scale[m] = s;
     } else {
-      s = *p.in_scale;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) h[i].set(x[i]);
     }
-    const RowQuantizer<OUT, DYN> quantize(s);
-    uint2 *yo = reinterpret_cast<uint2 *>(p.y) + m * p.K8;
+    if (kWalk) load(m + step);
+
+    // sum of squares
+    TwoFloat2 S2{0, 0};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = (i * p.wpr + sub) * 32 + lane;
-      uint64_t y[4];
-      normed8(h[i], w[i], r2, y);
-      if (v < p.K8) yo[v] = make_uint2(quantize.codes4(y[0], y[1]), quantize.codes4(y[2], y[3]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) add_values(S2, f32x2_mul(h[i].pair(j), h[i].pair(j)));
     }
+    TwoFloat S{f32x2_lo(S2.hi), f32x2_lo(S2.lo)};
+    add_pair(S, TwoFloat{f32x2_hi(S2.hi), f32x2_hi(S2.lo)});
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < p.lanes) add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
+    if (p.wpr > 1) {
+      if (lane == 0) s_sum[turn][warp] = S;
+      row_barrier();
+      S = lane < p.wpr ? s_sum[turn][first + lane] : TwoFloat{0.0f, 0.0f};
+#pragma unroll
+      for (int o = kMaxWarpsPerRow / 2; o > 0; o >>= 1)
+        add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
+      S.hi = __shfl_sync(~0u, S.hi, 0);  // lanes 16..31 hold no partial sums
+      S.lo = __shfl_sync(~0u, S.lo, 0);
+    }
+    float r = rms_reciprocal(S, p.inv_k, p.eps);
+    const bool exact = S.hi >= 0x1p-80f && S.hi < 0x1p126f;
+    if (__builtin_expect(__any_sync(~0u, !exact), 0)) {
+      // squares beyond binary32 (or an all-zero row): the same sum in FP64.  (Of one
+      // row's warps all come here or none: their sum is the same.)
+      double d = 0.0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t a = h[i].pair(j);
+          d += (double)f32x2_lo(a) * (double)f32x2_lo(a) + (double)f32x2_hi(a) * (double)f32x2_hi(a);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < p.lanes) d += __shfl_xor_sync(~0u, d, o);
+      if (p.wpr > 1) {
+        if (lane == 0) s_sum64[warp] = d;
+        row_barrier();
+        d = 0.0;
+        for (int i = 0; i < p.wpr; ++i) d += s_sum64[first + i];
+        row_barrier();
+      }
+      if (!exact) r = (float)(1.0 / sqrt(d * p.inv_k64 + p.eps64));
+    }
+
+    const uint64_t r2 = f32x2_pack(r, r);
+    const auto normed = [&](int i, int j) { return f32x2_mul(f32x2_mul(h[i].pair(j), r2), w[i].pair(j)); };
+    if constexpr (OUT == kNormBf16) {
+      uint4 *yo = reinterpret_cast<uint4 *>(p.y) + m * p.K8;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (stored && index(i) < p.K8)
+          yo[index(i)] = make_uint4(bf16x2_of(normed(i, 0)), bf16x2_of(normed(i, 1)), bf16x2_of(normed(i, 2)),
+                                    bf16x2_of(normed(i, 3)));
+    } else {
+      float s;
+      if constexpr (DYN) {
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t y = normed(i, j);
+            amax = fmaxf(amax, fmaxf(fabsf(f32x2_lo(y)), fabsf(f32x2_hi(y))));
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (o < p.lanes) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+        if (p.wpr > 1) {
+          if (lane == 0) s_max[warp] = amax;
+          row_barrier();
+          amax = warp_max(lane < p.wpr ? s_max[first + lane] : 0.0f);
+        }
+        s = __fdiv_rn(amax, OUT == kNormInt8 ? kQmaxInt8 : kQmaxE4m3);
+        s = s > 0.0f ? s : 1.0f;
+        if (stored && sub == 0 && in_row == 0) p.x_scale[m] = s;
+      } else {
+        s = *p.in_scale;
+      }
+      const RowQuantizer<OUT, DYN> quantize(s);
+      uint2 *yo = reinterpret_cast<uint2 *>(p.y) + m * p.K8;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (stored && index(i) < p.K8)
+          yo[index(i)] = make_uint2(quantize.codes4(normed(i, 0), normed(i, 1)),
+                                    quantize.codes4(normed(i, 2), normed(i, 3)));
+    }
+    if (!kWalk) break;  // the grid covers all rows
   }
 }
 
@@ -332,26 +362,35 @@ cudaError_t launch_nv(int nv, const RmsParams &p, dim3 grid, dim3 block, cudaStr
 
 cudaError_t launch_rmsnorm(const NormArgs &a, int sms, cudaStream_t st) {
   const int K8 = (int)(a.K / 8);
-  int wpr = 1;
-  while (wpr < kMaxWarpsPerRow && wpr * 32 * kMaxVecs < K8) wpr *= 2;
-  if (wpr * 32 * kMaxVecs < K8) return cudaErrorInvalidValue;
+  // lanes, then warps of a row, for at most four vectors a thread (BF16, or beyond
+  // 16 warps: eight); few rows: more of both, down to one vector
+  const int most = a.out == kNormBf16 ? kMaxVecs : 4;
+  int lanes = 4, wpr = 1;
   const auto vecs = [&] {
     int nv = 1;
-    while (nv * wpr * 32 < K8) nv *= 2;
+    while (nv * wpr * lanes < K8) nv *= 2;
     return nv;
   };
-  // few rows: more warps on each
-  while (wpr < kMaxWarpsPerRow && vecs() > 1 && a.M * wpr < (int64_t)sms * 16) wpr *= 2;
+  const auto widen = [&] { lanes < 32 ? lanes *= 2 : wpr *= 2; };
+  while (wpr < kMaxWarpsPerRow && vecs() > most) widen();
+  while (wpr < kMaxWarpsPerRow && vecs() > 1 && a.M * wpr * lanes < (int64_t)sms * kCtaWarps * 32) widen();
+  if (vecs() > kMaxVecs) return cudaErrorInvalidValue;
   RmsParams p{};
   p.x = (const uint16_t *)a.x, p.res = (const uint16_t *)a.residual, p.w = (const uint16_t *)a.weight;
-  p.ldx = a.ldx, p.ldr = a.ldr, p.M = a.M, p.K8 = K8, p.wpr = wpr;
+  p.ldx = a.ldx, p.ldr = a.ldr, p.M = a.M, p.K8 = K8;
+  p.lanes = lanes, p.wpr = wpr;
+  while (1 << p.lanes_log2 < lanes) ++p.lanes_log2;
+  while (1 << p.wpr_log2 < wpr) ++p.wpr_log2;
   p.eps = a.eps, p.eps64 = (double)a.eps, p.inv_k64 = 1.0 / (double)a.K;
   p.inv_k.hi = (float)p.inv_k64;
   p.inv_k.lo = (float)(p.inv_k64 - (double)p.inv_k.hi);
   p.in_scale = a.input_scale, p.h_out = (uint16_t *)a.h_out, p.y = a.y, p.x_scale = a.x_scale;
-  const int rows = std::max(1, kWarpsPerCta / wpr);
-  const dim3 grid((unsigned)((a.M + rows - 1) / rows)), block(32 * wpr * rows);
+  const int warps = std::max(wpr, kWarpsPerCta), rows = warps / wpr * (32 / lanes);
+  const dim3 block(32 * warps);
   const int nv = vecs();
+  const bool walk = nv <= 4 && a.out != kNormBf16;  // as in the kernel
+  const int64_t all = (a.M + rows - 1) / rows;
+  const dim3 grid((unsigned)(walk ? std::min<int64_t>(all, (int64_t)sms * (kCtaWarps / warps)) : all));
   switch (a.out) {
     case kNormBf16: return launch_nv<kNormBf16, false>(nv, p, grid, block, st);
     case kNormInt8:
