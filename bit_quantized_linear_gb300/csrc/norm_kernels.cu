@@ -16,8 +16,7 @@
 //
 // One pass: a row's vectors stay in registers between the sum and the output
 // (and, for per-token scales, between the output's maximum and its codes).  A
-// row is the work of `lanes` lanes (short rows: several to a warp) or of `wpr`
-// whole warps.  Bound by HBM: x, residual and h_out are 2 bytes an element, the
+// row is the work of `wpr` warps.  Bound by HBM: x, residual and h_out are 2 bytes an element, the
 // output 1 or 2.  With codes the arithmetic is close behind, so it runs on pairs
 // of elements as packed binary32 operations (the same roundings, lane by lane),
 // and a CTA walks over rows: the weights are unpacked once, and the next row is on
@@ -106,7 +105,6 @@ struct RmsParams {
   const uint16_t *x, *res, *w;
   int64_t ldx, ldr, M;
   int K8;                     // vectors of a row
-  int lanes, lanes_log2;      // its lanes of a warp (32 for more than one warp)
   int wpr, wpr_log2;          // its warps
   double eps64, inv_k64;
   float eps;
@@ -168,8 +166,13 @@ struct RowQuantizer {
   }
 };
 
+// bf16(x + r) of two pairs: one rounding of the exact sum.  (Rounding to binary32
+// first, as the definition has it, gives the same: binary32 only rounds a sum whose
+// smaller term is below 2^-16 of the larger, which is then the nearest BF16 itself.)
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-  return bf16x2_of(f32x2_add(f32x2_of(a), f32x2_of(b)));
+  const __nv_bfloat162 s =
+      __hadd2_rn(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&s);
 }
 
 // Eight BF16 values of a row as a thread keeps them: as binary32 pairs where the
@@ -202,17 +205,14 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
   __shared__ float s_max[kMaxWarpsPerRow];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp >> p.wpr_log2, sub = warp & (p.wpr - 1), first = group << p.wpr_log2;
-  const int in_row = lane & (p.lanes - 1);
   // the warps of one row meet at a barrier of their own
   const auto row_barrier = [&] {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "r"(p.wpr * 32) : "memory");
   };
-  const int at_once = (int)blockDim.x >> (p.wpr_log2 + p.lanes_log2);  // rows of a CTA
+  const int at_once = (int)blockDim.x >> (p.wpr_log2 + 5);  // rows of a CTA
   const int64_t step = (int64_t)gridDim.x * at_once;
-  // a warp's rows leave the loop together: those beyond the last are worked on and not stored
-  const int of_warp = lane >> p.lanes_log2;
-  int64_t m = (int64_t)blockIdx.x * at_once + (group << (5 - p.lanes_log2)) + of_warp;
-  const int index0 = (sub << p.lanes_log2) + in_row, index_step = p.wpr << p.lanes_log2;
+  int64_t m = (int64_t)blockIdx.x * at_once + group;
+  const int index0 = sub * 32 + lane, index_step = p.wpr * 32;
   const auto index = [&](int i) { return index0 + i * index_step; };
 
   V w[NV];
@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
     }
   };
   load(m);
-  for (int turn = 0; m - of_warp < p.M; m += step, turn ^= 1) {
-    const bool stored = m < p.M;
+  for (int turn = 0; m < p.M; m += step, turn ^= 1) {
     V h[NV];
     if (p.res) {
       uint4 *ho = reinterpret_cast<uint4 *>(p.h_out) + m * p.K8;
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
       for (int i = 0; i < NV; ++i) {
         const uint4 s = make_uint4(add_bf16x2(x[i].x, r4[i].x), add_bf16x2(x[i].y, r4[i].y),
                                    add_bf16x2(x[i].z, r4[i].z), add_bf16x2(x[i].w, r4[i].w));
-        if (stored && index(i) < p.K8) ho[index(i)] = s;
+        if (index(i) < p.K8) ho[index(i)] = s;
         h[i].set(s);
       }
     } else {
@@ -262,22 +261,27 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
     add_pair(S, TwoFloat{f32x2_hi(S2.hi), f32x2_hi(S2.lo)});
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-      if (o < p.lanes) add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
+      add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
     if (p.wpr > 1) {
       if (lane == 0) s_sum[turn][warp] = S;
       row_barrier();
-      S = lane < p.wpr ? s_sum[turn][first + lane] : TwoFloat{0.0f, 0.0f};
+      if (p.wpr <= 4) {
+        S = s_sum[turn][first];
+#pragma unroll 1
+        for (int i = 1; i < p.wpr; ++i) add_pair(S, s_sum[turn][first + i]);
+      } else {
+        S = lane < p.wpr ? s_sum[turn][first + lane] : TwoFloat{0.0f, 0.0f};
 #pragma unroll
-      for (int o = kMaxWarpsPerRow / 2; o > 0; o >>= 1)
-        add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
-      S.hi = __shfl_sync(~0u, S.hi, 0);  // lanes 16..31 hold no partial sums
-      S.lo = __shfl_sync(~0u, S.lo, 0);
+        for (int o = kMaxWarpsPerRow / 2; o > 0; o >>= 1)
+          add_pair(S, TwoFloat{__shfl_xor_sync(~0u, S.hi, o), __shfl_xor_sync(~0u, S.lo, o)});
+        S.hi = __shfl_sync(~0u, S.hi, 0);  // lanes 16..31 hold no partial sums
+        S.lo = __shfl_sync(~0u, S.lo, 0);
+      }
     }
     float r = rms_reciprocal(S, p.inv_k, p.eps);
-    const bool exact = S.hi >= 0x1p-80f && S.hi < 0x1p126f;
-    if (__builtin_expect(__any_sync(~0u, !exact), 0)) {
-      // squares beyond binary32 (or an all-zero row): the same sum in FP64.  (Of one
-      // row's warps all come here or none: their sum is the same.)
+    if (__builtin_expect(!(S.hi >= 0x1p-80f && S.hi < 0x1p126f), 0)) {
+      // squares beyond binary32 (or an all-zero row): the same sum in FP64.  (All of a
+      // row's lanes come here or none: their sum is the same.)
       double d = 0.0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
-        if (o < p.lanes) d += __shfl_xor_sync(~0u, d, o);
+        d += __shfl_xor_sync(~0u, d, o);
       if (p.wpr > 1) {
         if (lane == 0) s_sum64[warp] = d;
         row_barrier();
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
         for (int i = 0; i < p.wpr; ++i) d += s_sum64[first + i];
         row_barrier();
       }
-      if (!exact) r = (float)(1.0 / sqrt(d * p.inv_k64 + p.eps64));
+      r = (float)(1.0 / sqrt(d * p.inv_k64 + p.eps64));
     }
 
     const uint64_t r2 = f32x2_pack(r, r);
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
       uint4 *yo = reinterpret_cast<uint4 *>(p.y) + m * p.K8;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (stored && index(i) < p.K8)
+        if (index(i) < p.K8)
           yo[index(i)] = make_uint4(bf16x2_of(normed(i, 0)), bf16x2_of(normed(i, 1)), bf16x2_of(normed(i, 2)),
                                     bf16x2_of(normed(i, 3)));
     } else {
@@ -321,9 +325,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
             amax = fmaxf(amax, fmaxf(fabsf(f32x2_lo(y)), fabsf(f32x2_hi(y))));
           }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          if (o < p.lanes) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+        amax = warp_max(amax);
         if (p.wpr > 1) {
           if (lane == 0) s_max[warp] = amax;
           row_barrier();
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
         }
         s = __fdiv_rn(amax, OUT == kNormInt8 ? kQmaxInt8 : kQmaxE4m3);
         s = s > 0.0f ? s : 1.0f;
-        if (stored && sub == 0 && in_row == 0) p.x_scale[m] = s;
+        if (sub == 0 && lane == 0) p.x_scale[m] = s;
       } else {
         s = *p.in_scale;
       }
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(32 * kMaxWarpsPerRow) k_rmsnorm(const RmsParam
       uint2 *yo = reinterpret_cast<uint2 *>(p.y) + m * p.K8;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (stored && index(i) < p.K8)
+        if (index(i) < p.K8)
           yo[index(i)] = make_uint2(quantize.codes4(normed(i, 0), normed(i, 1)),
                                     quantize.codes4(normed(i, 2), normed(i, 3)));
     }
@@ -362,30 +364,28 @@ cudaError_t launch_nv(int nv, const RmsParams &p, dim3 grid, dim3 block, cudaStr
 
 cudaError_t launch_rmsnorm(const NormArgs &a, int sms, cudaStream_t st) {
   const int K8 = (int)(a.K / 8);
-  // lanes, then warps of a row, for at most four vectors a thread (BF16, or beyond
-  // 16 warps: eight); few rows: more of both, down to one vector
+  // warps of a row for at most four vectors a thread (BF16, or beyond 16 warps:
+  // eight); few rows: more warps, down to one vector
   const int most = a.out == kNormBf16 ? kMaxVecs : 4;
-  int lanes = 4, wpr = 1;
+  int wpr = 1;
   const auto vecs = [&] {
     int nv = 1;
-    while (nv * wpr * lanes < K8) nv *= 2;
+    while (nv * wpr * 32 < K8) nv *= 2;
     return nv;
   };
-  const auto widen = [&] { lanes < 32 ? lanes *= 2 : wpr *= 2; };
-  while (wpr < kMaxWarpsPerRow && vecs() > most) widen();
-  while (wpr < kMaxWarpsPerRow && vecs() > 1 && a.M * wpr * lanes < (int64_t)sms * kCtaWarps * 32) widen();
+  while (wpr < kMaxWarpsPerRow && vecs() > most) wpr *= 2;
+  while (wpr < kMaxWarpsPerRow && vecs() > 1 && a.M * wpr < (int64_t)sms * kCtaWarps) wpr *= 2;
   if (vecs() > kMaxVecs) return cudaErrorInvalidValue;
   RmsParams p{};
   p.x = (const uint16_t *)a.x, p.res = (const uint16_t *)a.residual, p.w = (const uint16_t *)a.weight;
   p.ldx = a.ldx, p.ldr = a.ldr, p.M = a.M, p.K8 = K8;
-  p.lanes = lanes, p.wpr = wpr;
-  while (1 << p.lanes_log2 < lanes) ++p.lanes_log2;
+  p.wpr = wpr;
   while (1 << p.wpr_log2 < wpr) ++p.wpr_log2;
   p.eps = a.eps, p.eps64 = (double)a.eps, p.inv_k64 = 1.0 / (double)a.K;
   p.inv_k.hi = (float)p.inv_k64;
   p.inv_k.lo = (float)(p.inv_k64 - (double)p.inv_k.hi);
   p.in_scale = a.input_scale, p.h_out = (uint16_t *)a.h_out, p.y = a.y, p.x_scale = a.x_scale;
-  const int warps = std::max(wpr, kWarpsPerCta), rows = warps / wpr * (32 / lanes);
+  const int warps = std::max(wpr, kWarpsPerCta), rows = warps / wpr;
   const dim3 block(32 * warps);
   const int nv = vecs();
   const bool walk = nv <= 4 && a.out != kNormBf16;  // as in the kernel
