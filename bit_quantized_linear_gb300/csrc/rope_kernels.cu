@@ -10,7 +10,10 @@
 //
 // With the store, a token's rotated key goes to the mixed cache through the
 // quantizer of qlin_kv_store_mixed without passing through memory as BF16.
-// Bound by HBM: q in and out, k and v in, codes out.
+// Bound by HBM: q in and out, k and v in, codes out.  A warp asks for all of its
+// heads before it waits for its position and the table's row, so a token costs one
+// trip to memory and not three (8192 tokens of 28 + 2 x 4 heads of 128: 40.6 us
+// with three).
 #include "common.cuh"
 #include "kernels.h"
 #include "kv_quant.cuh"
@@ -21,8 +24,8 @@ namespace qlin {
 
 namespace {
 
-constexpr int kWarps = 8;         // warps of a CTA; each takes work units of its own
-constexpr int kHeadsPerItem = 4;  // kv heads of one token a warp quantizes at once
+constexpr int kWarps = 8;         // warps of a CTA; each takes a work unit of its own
+constexpr int kHeadsPerItem = 4;  // (token, kv head) pairs a warp quantizes at once
 
 // ---------------------------------------------------------------- frequencies
 // Radians per position of pair i, scaled for long contexts:
@@ -66,8 +69,10 @@ struct RopeParams {
   uint16_t *q_out, *k_out;
   int64_t T, ldq, ldk, ldqo, ldko, max_pos;
   int Hq, Hk, D, rot, half_layout;
-  int units_q, units;  // work units of a token: q (and k) slices, all
-  int slice;           // heads of a q slice
+  // A unit of rotation is `tokens` tokens' heads, or (few tokens) one token's slice of
+  // `slice` heads, `slices` of them to a token.
+  int tokens, slice, slices;
+  int64_t units;
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -82,140 +87,183 @@ __device__ __forceinline__ float turn_b(float a, float b, float c, float s) {
   return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
-// Heads [h0, h1) of one token.  A lane keeps 16 dimensions of a head (8 pairs,
-// whose cosines and sines it loads once, or 16 dimensions past rot) and walks
-// over the heads; D/16 lanes make a head.
-__device__ __forceinline__ void rotate_heads(const RopeParams &p, int64_t t, const float *row, int h0, int h1,
-                                             int lane) {
+// The table row of a position, or null: a negative position is padding, one
+// beyond the table is reported.
+__device__ __forceinline__ const float *table_row(const RopeParams &p, int64_t pos, unsigned *status) {
+  if (pos >= p.max_pos) set_status(status, QLIN_ERR_INVALID_ARG);
+  return pos >= 0 && pos < p.max_pos ? p.table + pos * p.rot : nullptr;
+}
+
+// Unit u: heads of p.tokens tokens, or a slice of one's.  A lane keeps 16
+// dimensions of a head of one token (8 pairs, whose cosines and sines it loads
+// once, or 16 dimensions past rot) and walks over the heads; D/16 lanes make a
+// head.
+constexpr int kHeadBatch = 8;  // heads of a lane that are in flight at once
+__device__ __forceinline__ void rotate_heads(const RopeParams &p, int64_t u, int lane, unsigned *status) {
   const int per = p.D / 16;              // lanes of a head
-  const int at_once = 32 / per;          // heads a warp handles at once
-  const int item = lane % per, first = lane / per;
-  if (first >= at_once) return;
+  const int item = lane % per, group = lane / per;
+  int at_once = 32 / per;                // heads a warp handles at once
+  if (group >= at_once) return;
+  int64_t t;
+  int first = group, h0 = 0, h1 = p.Hq + p.Hk;
+  if (p.slices == 1) {
+    at_once /= p.tokens;                 // of each token (tokens is 1 or divides it)
+    t = u * p.tokens + group / at_once;
+    first = group % at_once;
+  } else {
+    t = u / p.slices;
+    h0 = (int)(u - t * p.slices) * p.slice;
+    h1 = min(h0 + p.slice, h1);
+  }
+  if (t >= p.T) return;
+  const int64_t pos = __ldg(p.positions + t);
   const bool turns = item * 16 < p.rot;
   const int half = p.rot / 2;
   // the two 8-dimension pieces of the lane
   const int d0 = turns && p.half_layout ? item * 8 : item * 16;
   const int d1 = turns && p.half_layout ? half + item * 8 : item * 16 + 8;
+  const auto place = [&](const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, int h) {
+    return h < p.Hq ? q + t * ldq + (int64_t)h * p.D : k + t * ldk + (int64_t)(h - p.Hq) * p.D;
+  };
   float c[8], s[8];
-  if (turns) {
-    *reinterpret_cast<float4 *>(c) = __ldg(reinterpret_cast<const float4 *>(row + item * 8));
-    *reinterpret_cast<float4 *>(c + 4) = __ldg(reinterpret_cast<const float4 *>(row + item * 8) + 1);
-    *reinterpret_cast<float4 *>(s) = __ldg(reinterpret_cast<const float4 *>(row + half + item * 8));
-    *reinterpret_cast<float4 *>(s + 4) = __ldg(reinterpret_cast<const float4 *>(row + half + item * 8) + 1);
-  }
-#pragma unroll 4
-  for (int h = h0 + first; h < h1; h += at_once) {
-    const bool isq = h < p.Hq;
-    const int64_t head = (int64_t)(isq ? h : h - p.Hq) * p.D;
-    const uint16_t *in = (isq ? p.q + t * p.ldq : p.k + t * p.ldk) + head;
-    uint16_t *out = (isq ? p.q_out + t * p.ldqo : p.k_out + t * p.ldko) + head;
-    uint4 a = *reinterpret_cast<const uint4 *>(in + d0), b = *reinterpret_cast<const uint4 *>(in + d1);
-    if (turns) {
-      uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      if (p.half_layout) {
+  bool ready = false;
+  for (int hb = h0 + first; hb < h1; hb += kHeadBatch * at_once) {
+    uint4 a[kHeadBatch], b[kHeadBatch];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float al = lo_f(x[j]), ah = hi_f(x[j]), bl = lo_f(x[4 + j]), bh = hi_f(x[4 + j]);
-          x[j] = pack_bf16(turn_a(al, bl, c[2 * j], s[2 * j]), turn_a(ah, bh, c[2 * j + 1], s[2 * j + 1]));
-          x[4 + j] = pack_bf16(turn_b(al, bl, c[2 * j], s[2 * j]), turn_b(ah, bh, c[2 * j + 1], s[2 * j + 1]));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float al = lo_f(x[j]), bl = hi_f(x[j]);
-          x[j] = pack_bf16(turn_a(al, bl, c[j], s[j]), turn_b(al, bl, c[j], s[j]));
-        }
+    for (int i = 0; i < kHeadBatch; ++i) {
+      const int h = hb + i * at_once;
+      if (h < h1) {
+        const uint16_t *in = place(p.q, p.ldq, p.k, p.ldk, h);
+        a[i] = *reinterpret_cast<const uint4 *>(in + d0);
+        b[i] = *reinterpret_cast<const uint4 *>(in + d1);
       }
-      a = make_uint4(x[0], x[1], x[2], x[3]);
-      b = make_uint4(x[4], x[5], x[6], x[7]);
     }
-    *reinterpret_cast<uint4 *>(out + d0) = a;
-    *reinterpret_cast<uint4 *>(out + d1) = b;
+    if (!ready) {
+      const float *row = table_row(p, pos, status);
+      if (!row) return;
+      if (turns) {
+        *reinterpret_cast<float4 *>(c) = __ldg(reinterpret_cast<const float4 *>(row + item * 8));
+        *reinterpret_cast<float4 *>(c + 4) = __ldg(reinterpret_cast<const float4 *>(row + item * 8) + 1);
+        *reinterpret_cast<float4 *>(s) = __ldg(reinterpret_cast<const float4 *>(row + half + item * 8));
+        *reinterpret_cast<float4 *>(s + 4) = __ldg(reinterpret_cast<const float4 *>(row + half + item * 8) + 1);
+      }
+      ready = true;
+    }
+#pragma unroll
+    for (int i = 0; i < kHeadBatch; ++i) {
+      const int h = hb + i * at_once;
+      if (h >= h1) break;
+      if (turns) {
+        uint32_t x[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
+        if (p.half_layout) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float al = lo_f(x[j]), ah = hi_f(x[j]), bl = lo_f(x[4 + j]), bh = hi_f(x[4 + j]);
+            x[j] = pack_bf16(turn_a(al, bl, c[2 * j], s[2 * j]), turn_a(ah, bh, c[2 * j + 1], s[2 * j + 1]));
+            x[4 + j] = pack_bf16(turn_b(al, bl, c[2 * j], s[2 * j]), turn_b(ah, bh, c[2 * j + 1], s[2 * j + 1]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float al = lo_f(x[j]), bl = hi_f(x[j]);
+            x[j] = pack_bf16(turn_a(al, bl, c[j], s[j]), turn_b(al, bl, c[j], s[j]));
+          }
+        }
+        a[i] = make_uint4(x[0], x[1], x[2], x[3]);
+        b[i] = make_uint4(x[4], x[5], x[6], x[7]);
+      }
+      uint16_t *out = const_cast<uint16_t *>(place(p.q_out, p.ldqo, p.k_out, p.ldko, h));
+      *reinterpret_cast<uint4 *>(out + d0) = a[i];
+      *reinterpret_cast<uint4 *>(out + d1) = b[i];
+    }
   }
 }
 
-// N (4 or 8) consecutive dimensions from d0 on of a rotated head, as BF16 words
-// (the partner dimensions of the half layout are read from memory again).
+// N (4 or 8) consecutive dimensions from d0 on of a head and, in the half layout,
+// their partner dimensions: as loaded, then rotated.
 template <int N>
-__device__ __forceinline__ void rotated_piece(const uint16_t *head, int d0, const float *row, int rot,
-                                              bool half_layout, uint32_t (&o)[N / 2]) {
-  load_words<N / 2>(head + d0, o);
-  if (d0 >= rot) return;
-  const int half = rot / 2;
-  if (half_layout) {
-    const bool is_a = d0 < half;
-    uint32_t other[N / 2];
-    load_words<N / 2>(head + (is_a ? d0 + half : d0 - half), other);
-    const float *c = row + (is_a ? d0 : d0 - half), *s = c + half;
+struct Piece {
+  uint32_t own[N / 2], other[N / 2];
+  __device__ __forceinline__ void load(const uint16_t *head, int d0, int rot, bool half_layout) {
+    load_words<N / 2>(head + d0, own);
+    if (d0 < rot && half_layout) load_words<N / 2>(head + (d0 < rot / 2 ? d0 + rot / 2 : d0 - rot / 2), other);
+  }
+  __device__ __forceinline__ void rotate(int d0, const float *row, int rot, bool half_layout) {
+    if (d0 >= rot) return;
+    const int half = rot / 2;
+    if (half_layout) {
+      const bool is_a = d0 < half;
+      const float *c = row + (is_a ? d0 : d0 - half), *s = c + half;
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      const float2 cc = __ldg(reinterpret_cast<const float2 *>(c) + j);
-      float2 ss = __ldg(reinterpret_cast<const float2 *>(s) + j);
-      if (is_a) ss = make_float2(-ss.x, -ss.y);
-      o[j] = pack_bf16(turn_b(lo_f(other[j]), lo_f(o[j]), cc.x, ss.x), turn_b(hi_f(other[j]), hi_f(o[j]), cc.y, ss.y));
-    }
-  } else {
-    const float *c = row + d0 / 2, *s = c + half;
+      for (int j = 0; j < N / 2; ++j) {
+        const float2 cc = __ldg(reinterpret_cast<const float2 *>(c) + j);
+        float2 ss = __ldg(reinterpret_cast<const float2 *>(s) + j);
+        if (is_a) ss = make_float2(-ss.x, -ss.y);
+        own[j] = pack_bf16(turn_b(lo_f(other[j]), lo_f(own[j]), cc.x, ss.x),
+                           turn_b(hi_f(other[j]), hi_f(own[j]), cc.y, ss.y));
+      }
+    } else {
+      const float *c = row + d0 / 2, *s = c + half;
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      const float a = lo_f(o[j]), b = hi_f(o[j]), cc = __ldg(c + j), ss = __ldg(s + j);
-      o[j] = pack_bf16(turn_a(a, b, cc, ss), turn_b(a, b, cc, ss));
+      for (int j = 0; j < N / 2; ++j) {
+        const float a = lo_f(own[j]), b = hi_f(own[j]), cc = __ldg(c + j), ss = __ldg(s + j);
+        own[j] = pack_bf16(turn_a(a, b, cc, ss), turn_b(a, b, cc, ss));
+      }
     }
   }
-}
+};
 
-// The table row of token t's position, or null: a negative position is padding,
-// one beyond the table is reported.
-__device__ __forceinline__ const float *table_row(const RopeParams &p, int64_t t, unsigned *status) {
-  const int64_t pos = p.positions[t];
-  if (pos >= p.max_pos) set_status(status, QLIN_ERR_INVALID_ARG);
-  return pos >= 0 && pos < p.max_pos ? p.table + pos * p.rot : nullptr;
-}
-
-__global__ void __launch_bounds__(32 * kWarps) k_rope(const RopeParams p, unsigned *status) {
+__global__ void __launch_bounds__(32 * kWarps, 2) k_rope(const RopeParams p, unsigned *status) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
-  for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < p.T * p.units; u += nwarps) {
-    const int64_t t = u / p.units;
-    const int part = (int)(u % p.units);
-    const float *row = table_row(p, t, status);
-    if (row) rotate_heads(p, t, row, part * p.slice, min((part + 1) * p.slice, p.Hq + p.Hk), lane);
-  }
+  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u < p.units) rotate_heads(p, u, threadIdx.x & 31, status);
 }
 
 // ------------------------------------------------------- rotation and store
 struct StoreParams {
   const uint16_t *v;
-  int64_t ldv, num_slots;
+  int64_t ldv, num_slots, items;
   const int64_t *slots;
   int H;
   uint8_t *kc, *vc;
   uint16_t *ks, *vs;
 };
 
-// Quantizes kv heads [h0, h0 + 4) of token t into its slot: lanes 8j..8j+7 hold
-// head h0 + j, each E = D/8 consecutive dimensions, as the plain store does.
+// Quantizes (token, kv head) pairs 4 * item .. 4 * item + 3 into their slots: lanes
+// 8j..8j+7 hold pair j, each E = D/8 consecutive dimensions, as the plain store
+// does.
 template <int E>
-__device__ __forceinline__ void store_item(const RopeParams &p, const StoreParams &s, int64_t t, int64_t slot,
-                                           const float *row, int h0, int lane) {
+__device__ __forceinline__ void store_item(const RopeParams &p, const StoreParams &s, int64_t item, int lane,
+                                           unsigned *status) {
   constexpr int D = 8 * E;
   constexpr int GL = E >= 32 ? 1 : 32 / E;  // lanes of a 32-dimension key group
   constexpr int N = E < 8 ? E : 8;
-  const int j = lane / 8, sub = lane % 8, h = h0 + j;
+  const int sub = lane % 8;
+  const int64_t pair = item * kHeadsPerItem + lane / 8;
+  const int64_t t = pair >> 32 ? pair / s.H : (int64_t)((uint32_t)pair / (uint32_t)s.H);
+  const int h = (int)(pair - t * s.H);
+  const bool real = t < p.T;
+  const int64_t pos = real ? __ldg(p.positions + t) : -1, slot = real ? __ldg(s.slots + t) : -1;
   uint32_t kw[E / 2], vw[E / 2];
+  Piece<N> piece[E / N];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) kw[i] = vw[i] = 0u;
-  if (h < s.H) {
+  if (real) {
     const uint16_t *kh = p.k + t * p.ldk + (int64_t)h * D;
     load_words<E / 2>(s.v + t * s.ldv + (int64_t)h * D + sub * E, vw);
 #pragma unroll
-    for (int i = 0; i < E / N; ++i) {
-      uint32_t o[N / 2];
-      rotated_piece<N>(kh, sub * E + i * N, row, p.rot, p.half_layout, o);
+    for (int i = 0; i < E / N; ++i) piece[i].load(kh, sub * E + i * N, p.rot, p.half_layout);
+  }
+  if (slot >= s.num_slots) set_status(status, QLIN_ERR_INVALID_ARG);
+  const float *row = table_row(p, pos, status);
+  const bool stored = row && slot >= 0 && slot < s.num_slots;
+  if (stored) {
 #pragma unroll
-      for (int n = 0; n < N / 2; ++n) kw[i * (N / 2) + n] = o[n];
+    for (int i = 0; i < E / N; ++i) {
+      piece[i].rotate(sub * E + i * N, row, p.rot, p.half_layout);
+#pragma unroll
+      for (int n = 0; n < N / 2; ++n) kw[i * (N / 2) + n] = piece[i].own[n];
     }
   }
   float ka = 0.0f, va = 0.0f;
@@ -238,7 +286,7 @@ __device__ __forceinline__ void store_item(const RopeParams &p, const StoreParam
     vq[i] = e4m3_pack4(quotient<true>(lo_f(vw[2 * i]), vsc), quotient<true>(hi_f(vw[2 * i]), vsc),
                        quotient<true>(lo_f(vw[2 * i + 1]), vsc), quotient<true>(hi_f(vw[2 * i + 1]), vsc));
   }
-  if (h < s.H) {
+  if (stored) {
     const int64_t base = slot * s.H + h;
     store_words<E / 4>(s.kc + base * D + sub * E, kq);
     store_words<E / 4>(s.vc + base * D + sub * E, vq);
@@ -247,61 +295,48 @@ __device__ __forceinline__ void store_item(const RopeParams &p, const StoreParam
   }
 }
 
+// Units of rotation (q), then items of the store.
 template <int E>
-__global__ void __launch_bounds__(32 * kWarps) k_rope_kv_store(const RopeParams p, const StoreParams s,
-                                                              unsigned *status) {
+__global__ void __launch_bounds__(32 * kWarps, 2) k_rope_kv_store(const RopeParams p, const StoreParams s,
+                                                                 unsigned *status) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
-  for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < p.T * p.units; u += nwarps) {
-    const int64_t t = u / p.units;
-    const int part = (int)(u % p.units);
-    const float *row = table_row(p, t, status);
-    if (part < p.units_q) {
-      if (row) rotate_heads(p, t, row, part * p.slice, min((part + 1) * p.slice, p.Hq), lane);
-      continue;
-    }
-    const int64_t slot = s.slots[t];
-    if (slot >= s.num_slots) {
-      if (lane == 0) set_status(status, QLIN_ERR_INVALID_ARG);
-    } else if (slot >= 0 && row) {
-      store_item<E>(p, s, t, slot, row, (part - p.units_q) * kHeadsPerItem, lane);
-    }
-  }
+  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u < p.units)
+    rotate_heads(p, u, lane, status);
+  else if (u < p.units + s.items)
+    store_item<E>(p, s, u - p.units, lane, status);
 }
 
-// Heads of a q slice: as few as a warp handles at once while the tokens do not
-// fill the GPU (latency), a token's whole row of heads when they do (the lane
-// then loads its cosines and sines once).
-int slice_heads(int64_t T, int heads, int D, int sms) {
-  const int at_once = std::max(1, 32 / (D / 16));
-  int slices = (heads + at_once - 1) / at_once;
-  while (slices > 1 && T * slices > (int64_t)sms * 32) slices = (slices + 1) / 2;
-  return ((heads + slices - 1) / slices + at_once - 1) / at_once * at_once;
-}
-
+// Tokens that fill the GPU: as many to a unit as give a lane up to kHeadBatch
+// heads.  Fewer: slices of a token, down to the heads a warp handles at once.
 RopeParams rope_params(const RopeArgs &r, int heads, int sms) {
   RopeParams p{};
   p.table = r.table, p.positions = r.positions, p.max_pos = r.max_pos;
   p.q = (const uint16_t *)r.q, p.k = (const uint16_t *)r.k;
   p.q_out = (uint16_t *)r.q_out, p.k_out = (uint16_t *)r.k_out;
   p.T = r.T, p.ldq = r.ldq, p.ldk = r.ldk, p.ldqo = r.ldqo, p.ldko = r.ldko;
-  p.Hq = (int)r.Hq, p.Hk = (int)r.Hk, p.D = (int)r.D, p.rot = (int)r.rot;
+  p.Hq = (int)r.Hq, p.Hk = heads - (int)r.Hq, p.D = (int)r.D, p.rot = (int)r.rot;
   p.half_layout = r.layout == QLIN_ROPE_HALF;
-  p.slice = slice_heads(r.T, heads, p.D, sms);
-  p.units_q = p.units = (heads + p.slice - 1) / p.slice;
+  const int at_once = std::max(1, 32 / (p.D / 16));
+  const int64_t full = (int64_t)sms * 32;  // units that fill the GPU
+  p.tokens = 1;
+  while (at_once % (2 * p.tokens) == 0 && heads * 2 * p.tokens <= kHeadBatch * at_once && r.T >= full * 2 * p.tokens)
+    p.tokens *= 2;
+  p.slices = p.tokens > 1 ? 1 : (heads + at_once - 1) / at_once;
+  while (p.slices > 1 && r.T * p.slices > full) p.slices = (p.slices + 1) / 2;
+  p.slice = ((heads + p.slices - 1) / p.slices + at_once - 1) / at_once * at_once;
+  p.slices = (heads + p.slice - 1) / p.slice;
+  p.units = p.slices > 1 ? r.T * p.slices : (r.T + p.tokens - 1) / p.tokens;
   return p;
 }
 
-dim3 unit_grid(int64_t units, int sms) {
-  const int64_t need = (units + kWarps - 1) / kWarps;
-  return dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(need, (int64_t)sms * 64)));
-}
+dim3 unit_grid(int64_t units) { return dim3((unsigned)((units + kWarps - 1) / kWarps)); }
 
 template <int E>
-cudaError_t launch_store_e(const RopeParams &p, const StoreParams &s, unsigned *status, int sms, cudaStream_t st) {
-  return launch_kernel(k_rope_kv_store<E>, unit_grid(p.T * p.units, sms), dim3(32 * kWarps), 0, st, 1, p, s, status);
+cudaError_t launch_store_e(const RopeParams &p, const StoreParams &s, unsigned *status, cudaStream_t st) {
+  return launch_kernel(k_rope_kv_store<E>, unit_grid(p.units + s.items), dim3(32 * kWarps), 0, st, 1, p, s, status);
 }
 
 }  // namespace
@@ -317,21 +352,21 @@ cudaError_t launch_rope_table(int64_t max_pos, int64_t rot, double theta, int sc
 
 cudaError_t launch_rope(const RopeArgs &r, unsigned *status, int sms, cudaStream_t st) {
   const RopeParams p = rope_params(r, (int)(r.Hq + r.Hk), sms);
-  return launch_kernel(k_rope, unit_grid(p.T * p.units, sms), dim3(32 * kWarps), 0, st, 1, p, status);
+  return launch_kernel(k_rope, unit_grid(p.units), dim3(32 * kWarps), 0, st, 1, p, status);
 }
 
 cudaError_t launch_rope_kv_store(const RopeArgs &r, const KvArgs &kv, unsigned *status, int sms, cudaStream_t st) {
-  RopeParams p = rope_params(r, (int)r.Hq, sms);
-  p.units = p.units_q + (int)((r.Hk + kHeadsPerItem - 1) / kHeadsPerItem);
+  const RopeParams p = rope_params(r, (int)r.Hq, sms);
   StoreParams s{};
+  s.items = (r.T * r.Hk + kHeadsPerItem - 1) / kHeadsPerItem;
   s.v = (const uint16_t *)kv.v, s.ldv = kv.ldv, s.num_slots = kv.num_slots, s.slots = kv.slots, s.H = (int)r.Hk;
   s.kc = (uint8_t *)kv.k_cache, s.ks = (uint16_t *)kv.k_scale;
   s.vc = (uint8_t *)kv.v_cache, s.vs = (uint16_t *)kv.v_scale;
   switch (r.D) {
-    case 32: return launch_store_e<4>(p, s, status, sms, st);
-    case 64: return launch_store_e<8>(p, s, status, sms, st);
-    case 128: return launch_store_e<16>(p, s, status, sms, st);
-    case 256: return launch_store_e<32>(p, s, status, sms, st);
+    case 32: return launch_store_e<4>(p, s, status, st);
+    case 64: return launch_store_e<8>(p, s, status, st);
+    case 128: return launch_store_e<16>(p, s, status, st);
+    case 256: return launch_store_e<32>(p, s, status, st);
   }
   return cudaErrorInvalidValue;
 }
