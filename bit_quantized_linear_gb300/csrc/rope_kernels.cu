@@ -98,7 +98,7 @@ __device__ __forceinline__ const float *table_row(const RopeParams &p, int64_t p
 // dimensions of a head of one token (8 pairs, whose cosines and sines it loads
 // once, or 16 dimensions past rot) and walks over the heads; D/16 lanes make a
 // head.
-constexpr int kHeadBatch = 8;  // heads of a lane that are in flight at once
+constexpr int kHeadBatch = 4;  // heads of a lane that are in flight at once
 __device__ __forceinline__ void rotate_heads(const RopeParams &p, int64_t u, int lane, unsigned *status) {
   const int per = p.D / 16;              // lanes of a head
   const int item = lane % per, group = lane / per;
@@ -188,32 +188,45 @@ struct Piece {
     load_words<N / 2>(head + d0, own);
     if (d0 < rot && half_layout) load_words<N / 2>(head + (d0 < rot / 2 ? d0 + rot / 2 : d0 - rot / 2), other);
   }
-  __device__ __forceinline__ void rotate(int d0, const float *row, int rot, bool half_layout) {
+  // Its cosines and sines (both layouts: N, or N/2, consecutive ones).
+  float c[N], s[N];
+  __device__ __forceinline__ void load_angles(int d0, const float *row, int rot, bool half_layout) {
     if (d0 >= rot) return;
     const int half = rot / 2;
+    const float *from = row + (half_layout ? (d0 < half ? d0 : d0 - half) : d0 / 2);
     if (half_layout) {
-      const bool is_a = d0 < half;
-      const float *c = row + (is_a ? d0 : d0 - half), *s = c + half;
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        const float2 cc = __ldg(reinterpret_cast<const float2 *>(c) + j);
-        float2 ss = __ldg(reinterpret_cast<const float2 *>(s) + j);
-        if (is_a) ss = make_float2(-ss.x, -ss.y);
-        own[j] = pack_bf16(turn_b(lo_f(other[j]), lo_f(own[j]), cc.x, ss.x),
-                           turn_b(hi_f(other[j]), hi_f(own[j]), cc.y, ss.y));
+      for (int j = 0; j < N; j += 4) {
+        *reinterpret_cast<float4 *>(c + j) = __ldg(reinterpret_cast<const float4 *>(from + j));
+        *reinterpret_cast<float4 *>(s + j) = __ldg(reinterpret_cast<const float4 *>(from + half + j));
       }
     } else {
-      const float *c = row + d0 / 2, *s = c + half;
+#pragma unroll
+      for (int j = 0; j < N / 2; j += 2) {
+        *reinterpret_cast<float2 *>(c + j) = __ldg(reinterpret_cast<const float2 *>(from + j));
+        *reinterpret_cast<float2 *>(s + j) = __ldg(reinterpret_cast<const float2 *>(from + half + j));
+      }
+    }
+  }
+  __device__ __forceinline__ void rotate(int d0, int rot, bool half_layout) {
+    if (d0 >= rot) return;
+    if (half_layout) {
+      const float sign = d0 < rot / 2 ? -1.0f : 1.0f;  // a' = a c - b s, b' = b c + a s
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j)
+        own[j] = pack_bf16(turn_b(lo_f(other[j]), lo_f(own[j]), c[2 * j], sign * s[2 * j]),
+                           turn_b(hi_f(other[j]), hi_f(own[j]), c[2 * j + 1], sign * s[2 * j + 1]));
+    } else {
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) {
-        const float a = lo_f(own[j]), b = hi_f(own[j]), cc = __ldg(c + j), ss = __ldg(s + j);
-        own[j] = pack_bf16(turn_a(a, b, cc, ss), turn_b(a, b, cc, ss));
+        const float a = lo_f(own[j]), b = hi_f(own[j]);
+        own[j] = pack_bf16(turn_a(a, b, c[j], s[j]), turn_b(a, b, c[j], s[j]));
       }
     }
   }
 };
 
-__global__ void __launch_bounds__(32 * kWarps, 2) k_rope(const RopeParams p, unsigned *status) {
+__global__ void __launch_bounds__(32 * kWarps, 3) k_rope(const RopeParams p, unsigned *status) {
   pdl_wait();
   pdl_trigger();
   const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -223,90 +236,101 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_rope(const RopeParams p, uns
 // ------------------------------------------------------- rotation and store
 struct StoreParams {
   const uint16_t *v;
-  int64_t ldv, num_slots, items;
+  int64_t ldv, num_slots;
+  unsigned ctas;  // of the store
   const int64_t *slots;
   int H;
   uint8_t *kc, *vc;
   uint16_t *ks, *vs;
 };
 
-// Quantizes (token, kv head) pairs 4 * item .. 4 * item + 3 into their slots: lanes
-// 8j..8j+7 hold pair j, each E = D/8 consecutive dimensions, as the plain store
-// does.
+// A (token, kv head) pair as eight lanes hold it: E = D/8 consecutive dimensions
+// each, as the plain store does.
 template <int E>
-__device__ __forceinline__ void store_item(const RopeParams &p, const StoreParams &s, int64_t item, int lane,
-                                           unsigned *status) {
-  constexpr int D = 8 * E;
-  constexpr int GL = E >= 32 ? 1 : 32 / E;  // lanes of a 32-dimension key group
-  constexpr int N = E < 8 ? E : 8;
-  const int sub = lane % 8;
-  const int64_t pair = item * kHeadsPerItem + lane / 8;
-  const int64_t t = pair >> 32 ? pair / s.H : (int64_t)((uint32_t)pair / (uint32_t)s.H);
-  const int h = (int)(pair - t * s.H);
-  const bool real = t < p.T;
-  const int64_t pos = real ? __ldg(p.positions + t) : -1, slot = real ? __ldg(s.slots + t) : -1;
-  uint32_t kw[E / 2], vw[E / 2];
-  Piece<N> piece[E / N];
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i) kw[i] = vw[i] = 0u;
-  if (real) {
+struct StorePair {
+  static constexpr int D = 8 * E, N = E < 8 ? E : 8;
+  int64_t pos, slot;
+  int h;
+  Piece<N> k[E / N];
+  uint32_t v[E / 2];
+
+  __device__ __forceinline__ void load(const RopeParams &p, const StoreParams &s, int64_t pair, int sub) {
+    const int64_t t = pair >> 32 ? pair / s.H : (int64_t)((uint32_t)pair / (uint32_t)s.H);
+    h = (int)(pair - t * s.H);
+    pos = slot = -1;
+    if (t >= p.T) return;
+    pos = __ldg(p.positions + t);
+    slot = __ldg(s.slots + t);
     const uint16_t *kh = p.k + t * p.ldk + (int64_t)h * D;
-    load_words<E / 2>(s.v + t * s.ldv + (int64_t)h * D + sub * E, vw);
 #pragma unroll
-    for (int i = 0; i < E / N; ++i) piece[i].load(kh, sub * E + i * N, p.rot, p.half_layout);
+    for (int i = 0; i < E / N; ++i) k[i].load(kh, sub * E + i * N, p.rot, p.half_layout);
+    load_words<E / 2>(s.v + t * s.ldv + (int64_t)h * D + sub * E, v);
   }
-  if (slot >= s.num_slots) set_status(status, QLIN_ERR_INVALID_ARG);
-  const float *row = table_row(p, pos, status);
-  const bool stored = row && slot >= 0 && slot < s.num_slots;
-  if (stored) {
+
+  // (the lanes of a pair that is not stored take part in the shuffles)
+  __device__ __forceinline__ void store(const RopeParams &p, const StoreParams &s, int sub, unsigned *status) {
+    constexpr int GL = E >= 32 ? 1 : 32 / E;  // lanes of a 32-dimension key group
+    if (slot >= s.num_slots) set_status(status, QLIN_ERR_INVALID_ARG);
+    const float *row = table_row(p, pos, status);
+    const bool stored = row && slot >= 0 && slot < s.num_slots;
+    uint32_t kw[E / 2];
+    if (stored) {
+#pragma unroll
+      for (int i = 0; i < E / N; ++i) k[i].load_angles(sub * E + i * N, row, p.rot, p.half_layout);
+    }
 #pragma unroll
     for (int i = 0; i < E / N; ++i) {
-      piece[i].rotate(sub * E + i * N, row, p.rot, p.half_layout);
+      if (stored) k[i].rotate(sub * E + i * N, p.rot, p.half_layout);
 #pragma unroll
-      for (int n = 0; n < N / 2; ++n) kw[i * (N / 2) + n] = piece[i].own[n];
+      for (int n = 0; n < N / 2; ++n) kw[i * (N / 2) + n] = k[i].own[n];
     }
-  }
-  float ka = 0.0f, va = 0.0f;
+    float ka = 0.0f, va = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    ka = fmaxf(ka, fmaxf(fabsf(lo_f(kw[i])), fabsf(hi_f(kw[i]))));
-    va = fmaxf(va, fmaxf(fabsf(lo_f(vw[i])), fabsf(hi_f(vw[i]))));
-  }
-  ka = group_max<GL>(ka);
-  va = group_max<8>(va);
-  const uint16_t ks16 = scale16(ka, kQmaxInt8), vs16 = scale16(va, kQmaxE4m3);
-  const Scale ksc = make_scale(half_bits_to_f32(ks16)), vsc = make_scale(half_bits_to_f32(vs16));
-  uint32_t kq[E / 4], vq[E / 4];
+    for (int i = 0; i < E / 2; ++i) {
+      ka = fmaxf(ka, fmaxf(fabsf(lo_f(kw[i])), fabsf(hi_f(kw[i]))));
+      va = fmaxf(va, fmaxf(fabsf(lo_f(v[i])), fabsf(hi_f(v[i]))));
+    }
+    ka = group_max<GL>(ka);
+    va = group_max<8>(va);
+    if (!stored) return;
+    const uint16_t ks16 = scale16(ka, kQmaxInt8), vs16 = scale16(va, kQmaxE4m3);
+    const Scale ksc = make_scale(half_bits_to_f32(ks16)), vsc = make_scale(half_bits_to_f32(vs16));
+    uint32_t kq[E / 4], vq[E / 4];
 #pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
-    kq[i] = pack4_low(int8_code_word(quotient<true>(lo_f(kw[2 * i]), ksc)),
-                      int8_code_word(quotient<true>(hi_f(kw[2 * i]), ksc)),
-                      int8_code_word(quotient<true>(lo_f(kw[2 * i + 1]), ksc)),
-                      int8_code_word(quotient<true>(hi_f(kw[2 * i + 1]), ksc)));
-    vq[i] = e4m3_pack4(quotient<true>(lo_f(vw[2 * i]), vsc), quotient<true>(hi_f(vw[2 * i]), vsc),
-                       quotient<true>(lo_f(vw[2 * i + 1]), vsc), quotient<true>(hi_f(vw[2 * i + 1]), vsc));
-  }
-  if (stored) {
+    for (int i = 0; i < E / 4; ++i) {
+      kq[i] = pack4_low(int8_code_word(quotient<true>(lo_f(kw[2 * i]), ksc)),
+                        int8_code_word(quotient<true>(hi_f(kw[2 * i]), ksc)),
+                        int8_code_word(quotient<true>(lo_f(kw[2 * i + 1]), ksc)),
+                        int8_code_word(quotient<true>(hi_f(kw[2 * i + 1]), ksc)));
+      vq[i] = e4m3_pack4(quotient<true>(lo_f(v[2 * i]), vsc), quotient<true>(hi_f(v[2 * i]), vsc),
+                         quotient<true>(lo_f(v[2 * i + 1]), vsc), quotient<true>(hi_f(v[2 * i + 1]), vsc));
+    }
     const int64_t base = slot * s.H + h;
     store_words<E / 4>(s.kc + base * D + sub * E, kq);
     store_words<E / 4>(s.vc + base * D + sub * E, vq);
     if (sub % GL == 0) s.ks[base * (D / 32) + sub / GL] = ks16;
     if (sub == 0) s.vs[base] = vs16;
   }
-}
+};
 
-// Units of rotation (q), then items of the store.
+// CTAs of rotation (q) and of the store take turns, in proportion, so that both
+// kinds are in flight all the time.
 template <int E>
-__global__ void __launch_bounds__(32 * kWarps, 2) k_rope_kv_store(const RopeParams p, const StoreParams s,
+__global__ void __launch_bounds__(32 * kWarps, 3) k_rope_kv_store(const RopeParams p, const StoreParams s,
                                                                  unsigned *status) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u < p.units)
-    rotate_heads(p, u, lane, status);
-  else if (u < p.units + s.items)
-    store_item<E>(p, s, u - p.units, lane, status);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned before = (unsigned)((uint64_t)blockIdx.x * s.ctas / gridDim.x);
+  const unsigned after = (unsigned)(((uint64_t)blockIdx.x + 1) * s.ctas / gridDim.x);
+  if (after == before) {
+    const int64_t u = (int64_t)(blockIdx.x - before) * kWarps + warp;
+    if (u < p.units) rotate_heads(p, u, lane, status);
+    return;
+  }
+  StorePair<E> pair;
+  pair.load(p, s, ((int64_t)before * kWarps + warp) * kHeadsPerItem + lane / 8, lane % 8);
+  pair.store(p, s, lane % 8, status);
 }
 
 // Tokens that fill the GPU: as many to a unit as give a lane up to kHeadBatch
@@ -332,11 +356,13 @@ RopeParams rope_params(const RopeArgs &r, int heads, int sms) {
   return p;
 }
 
-dim3 unit_grid(int64_t units) { return dim3((unsigned)((units + kWarps - 1) / kWarps)); }
+unsigned unit_ctas(int64_t units) { return (unsigned)((units + kWarps - 1) / kWarps); }
 
 template <int E>
-cudaError_t launch_store_e(const RopeParams &p, const StoreParams &s, unsigned *status, cudaStream_t st) {
-  return launch_kernel(k_rope_kv_store<E>, unit_grid(p.units + s.items), dim3(32 * kWarps), 0, st, 1, p, s, status);
+cudaError_t launch_store_e(const RopeParams &p, StoreParams s, unsigned *status, cudaStream_t st) {
+  s.ctas = unit_ctas((p.T * s.H + kHeadsPerItem - 1) / kHeadsPerItem);
+  return launch_kernel(k_rope_kv_store<E>, dim3(unit_ctas(p.units) + s.ctas), dim3(32 * kWarps), 0, st, 1, p, s,
+                       status);
 }
 
 }  // namespace
@@ -352,13 +378,12 @@ cudaError_t launch_rope_table(int64_t max_pos, int64_t rot, double theta, int sc
 
 cudaError_t launch_rope(const RopeArgs &r, unsigned *status, int sms, cudaStream_t st) {
   const RopeParams p = rope_params(r, (int)(r.Hq + r.Hk), sms);
-  return launch_kernel(k_rope, unit_grid(p.units), dim3(32 * kWarps), 0, st, 1, p, status);
+  return launch_kernel(k_rope, dim3(unit_ctas(p.units)), dim3(32 * kWarps), 0, st, 1, p, status);
 }
 
 cudaError_t launch_rope_kv_store(const RopeArgs &r, const KvArgs &kv, unsigned *status, int sms, cudaStream_t st) {
   const RopeParams p = rope_params(r, (int)r.Hq, sms);
   StoreParams s{};
-  s.items = (r.T * r.Hk + kHeadsPerItem - 1) / kHeadsPerItem;
   s.v = (const uint16_t *)kv.v, s.ldv = kv.ldv, s.num_slots = kv.num_slots, s.slots = kv.slots, s.H = (int)r.Hk;
   s.kc = (uint8_t *)kv.k_cache, s.ks = (uint16_t *)kv.k_scale;
   s.vc = (uint8_t *)kv.v_cache, s.vs = (uint16_t *)kv.v_scale;
