@@ -98,7 +98,7 @@ __device__ __forceinline__ const float *table_row(const RopeParams &p, int64_t p
 // dimensions of a head of one token (8 pairs, whose cosines and sines it loads
 // once, or 16 dimensions past rot) and walks over the heads; D/16 lanes make a
 // head.
-constexpr int kHeadBatch = 4;  // heads of a lane that are in flight at once
+constexpr int kHeadBatch = 2;  // heads of a lane that are in flight at once (more cost more warps than they hide)
 __device__ __forceinline__ void rotate_heads(const RopeParams &p, int64_t u, int lane, unsigned *status) {
   const int per = p.D / 16;              // lanes of a head
   const int item = lane % per, group = lane / per;
@@ -226,7 +226,7 @@ struct Piece {
   }
 };
 
-__global__ void __launch_bounds__(32 * kWarps, 3) k_rope(const RopeParams p, unsigned *status) {
+__global__ void __launch_bounds__(32 * kWarps, 4) k_rope(const RopeParams p, unsigned *status) {
   pdl_wait();
   pdl_trigger();
   const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -316,7 +316,7 @@ struct StorePair {
 // CTAs of rotation (q) and of the store take turns, in proportion, so that both
 // kinds are in flight all the time.
 template <int E>
-__global__ void __launch_bounds__(32 * kWarps, 3) k_rope_kv_store(const RopeParams p, const StoreParams s,
+__global__ void __launch_bounds__(32 * kWarps, E >= 32 ? 2 : 4) k_rope_kv_store(const RopeParams p, const StoreParams s,
                                                                  unsigned *status) {
   pdl_wait();
   pdl_trigger();
