@@ -99,4 +99,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half(uint16_t c) {
   return r;
 }
 
+// Partial results of rows whose positions several CTAs share: [unit][part][row of
+// the unit's tile] O (D fp32) and the base-2 logarithm of its sum (-inf: nothing
+// seen), unit = (b * H + h) * row_tiles + tile.
+struct AttnParts {
+  float *o, *lse;
+  int row_tiles, rows, splits;
+};
+// Joins them into `out`.  many: of the sequences with more than p.few_rows rows, else of the others.
+cudaError_t launch_attn_join(const AttnDev &p, const AttnParts &parts, int64_t D, bool many, cudaStream_t st);
+
 }  // namespace qlin

@@ -11,7 +11,9 @@
 //
 // k_attn_prefill: a CTA takes 256 rows of one (sequence, kv head), packed
 // token-major over the heads of the group, as two row tiles A and B of 128, and
-// walks over the position tiles, each one contiguous bulk copy.  Roles:
+// walks over the position tiles, each one contiguous bulk copy.  Where that would
+// leave multiprocessors idle, several CTAs share the positions and a join follows.
+// Roles:
 //   * warps 0-3 and 4-7: softmax of tile A and of tile B, a thread per row.  S
 //     comes from tensor memory, P goes back there (over S) as float16.
 //   * warp 8: copies; warp 9: issues S = Q K^T (both from shared memory) and
@@ -25,7 +27,9 @@
 // them whatever the cache's scales; 2^ek joins the score's factor and ev the
 // exponent, so that neither costs the softmax an instruction per score.  O is
 // rescaled only where a row's maximum grew by more than 2^6 since its reference;
-// P stays below 2^14.
+// P stays below 2^14.  Positions whose value scale is 0 do not raise that
+// reference (they would push P of the others out of float16): they count in the
+// sum of the row alone, which for that has a reference of its own.
 #include <algorithm>
 
 #include "attn.cuh"
@@ -47,6 +51,7 @@ constexpr int kThreads = 320;
 constexpr int kMetaSlots = 4;
 constexpr float kPBias = 8.0f;  // P is 2^8 p: float16's subnormals lie below 2^-22 p
 constexpr float kGrowth = 6.0f;
+constexpr float kLead = 32.0f;  // a score without a value may pass the sum's reference by 2^this
 constexpr int kValueUp = 5;     // a value's scale becomes 2^5..2^6 (times at most 448: below float16's 65504)
 constexpr int kValueSpan = 8;   // scales of a unit within 2^8 share an exponent: E4M3's 2^-9 stays normal
 
@@ -105,8 +110,10 @@ __device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float((
 __device__ __forceinline__ uint32_t swizzled(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
 struct PrefillParams : AttnDev {
-  int row_tiles, tiles;      // row tiles and position tiles of a sequence
+  int row_tiles, tiles;      // row tiles (of A and B together) and position tiles of a sequence
   int head0, heads;          // kv heads of this pass
+  AttnParts parts;           // splits > 1: parts of chunk position tiles, a CTA each (all heads in one pass)
+  int chunk;
   uint8_t *images;           // [B, heads, tiles] key and value tile
   TileMeta *meta;            // [B, heads, tiles]
 };
@@ -224,7 +231,11 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
     return;
   }
 
-  const bool wide = e - min(exponent(__reduce_min_sync(~0u, low)), e) > kValueSpan;
+  bool nothing = false;  // a position there with a scale of 0
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) nothing |= ((valid[i] >> lane) & 1) && (scale[i] & 0x7FFFu) == 0;
+  const bool wide =
+      __any_sync(~0u, nothing) || e - min(exponent(__reduce_min_sync(~0u, low)), e) > kValueSpan;
   // Values that are not finite: zeros in the tile, and a mark.
   unsigned poison[kWords];
 #pragma unroll
@@ -256,12 +267,9 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
     const float s = half_at(scale[i], 0);
-    int es = e;
-    if (wide) {
-      const unsigned a = __float_as_uint(fabsf(s));
-      es = a ? exponent(a) : e;
-    }
-    tm.pos_ev[block * C::kUnit + i * 32 + lane] = (float)(es - kValueUp);
+    const unsigned a = __float_as_uint(fabsf(s));
+    const int es = wide && a ? exponent(a) : e;
+    tm.pos_ev[block * C::kUnit + i * 32 + lane] = a ? (float)(es - kValueUp) : -INFINITY;
     const uint32_t w = __half_as_ushort(__float2half_rn(s * pow2i(kValueUp - es)));
     sw[i] = w | (__shfl_down_sync(~0u, w, 1) << 16);
   }
@@ -308,13 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // the last row tiles see the most positions: they go first
-  const int heads = p.B * p.heads;
-  const int tile = p.row_tiles - 1 - (int)(blockIdx.x / heads);
-  const int b = (int)(blockIdx.x % heads) / p.heads, h = p.head0 + (int)(blockIdx.x % heads) % p.heads;
+  const int heads = p.B * p.heads, split = (int)(blockIdx.x % p.parts.splits);
+  const unsigned unit = blockIdx.x / p.parts.splits;
+  const int tile = p.row_tiles - 1 - (int)(unit / heads);
+  const int b = (int)(unit % heads) / p.heads, h = p.head0 + (int)(unit % heads) % p.heads;
   pdl_wait();
   pdl_trigger();
   const Sequence sq = sequence(p, b);
-  if (sq.broken && h == 0 && tile == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
+  if (sq.broken && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
   const int R = sq.kept * p.G, r0 = tile * 2 * kRowTile;
   if (r0 >= R || R <= p.few_rows) return;
 
@@ -323,13 +332,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   const int last = min(r0 + 2 * kRowTile, R) - 1;
   sees(p, sq, r0 / p.G, beg, all_hi);
   sees(p, sq, last / p.G, all_lo, end);
-  const int lo = beg, tile0 = beg / kPos;
+  const int lo = beg;
+  int tile0 = beg / kPos, n = end > lo ? (end + kPos - 1) / kPos - tile0 : 0;
+  if (p.parts.splits > 1) {  // this CTA's part; the last one takes what is left
+    const int skip = min(split * p.chunk, n);
+    tile0 += skip;
+    n -= skip;
+    if (split < p.parts.splits - 1) n = min(n, p.chunk);
+  }
   beg = tile0 * kPos;
-  const int n = end > lo ? (end - beg + kPos - 1) / kPos : 0;
+  // of row r: where the parts' results go
+  const auto part_row = [&](int r) {
+    const int64_t unit_at = ((int64_t)b * p.H + h) * p.row_tiles + tile;
+    return (unit_at * p.parts.splits + split) * p.parts.rows + (r - r0);
+  };
 
   if (n == 0) {  // rows that see nothing
     for (int i = threadIdx.x; i < (last - r0 + 1) * (D / 8); i += kThreads) {
       const int r = r0 + i / (D / 8);
+      if (p.parts.splits > 1) {
+        float4 *o = reinterpret_cast<float4 *>(p.parts.o + part_row(r) * D) + i % (D / 8) * 2;
+        o[0] = o[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i % (D / 8) == 0) p.parts.lse[part_row(r)] = -INFINITY;
+        continue;
+      }
       uint16_t *dst = p.out + (int64_t)(sq.first + r / p.G) * p.ldo + (int64_t)(h * p.G + r % p.G) * D;
       reinterpret_cast<uint4 *>(dst)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
     }
@@ -396,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     const uint32_t s_at = at + C::kS + half * kPos, o_at = at + C::kO + half * D;
     int row_lo = lo, row_hi = end;
     if (r < R) sees(p, sq, r / p.G, row_lo, row_hi);
-    float m = -INFINITY, l = 0.0f;
+    // O is sum p v under the reference m, l is sum p under m_l >= m; to_l = 2^(m - m_l)
+    float m = -INFINITY, m_l = -INFINITY, l = 0.0f, to_l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
@@ -443,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
 #pragma unroll
         for (int c = 0; c < 4; ++c) mask(c, s[c]);
       }
-      float now = m;
+      float now = m, nothing = -INFINITY;  // nothing: the largest score of a position without a value
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         float mx = -INFINITY;
@@ -456,15 +483,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
           mx = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaf(__uint_as_float(s[c][i]), f[c], tm.pos_ev[c * 32 + i]));
+          for (int i = 0; i < 32; ++i) {
+            const float x = __uint_as_float(s[c][i]) * f[c], e = tm.pos_ev[c * 32 + i];
+            mx = fmaxf(mx, x + e);
+            if (e == -INFINITY) nothing = fmaxf(nothing, x);
+          }
         }
         now = fmaxf(now, mx);
       }
-      if (__any_sync(~0u, now > m + kGrowth)) {
+      if (__any_sync(~0u, now > m + kGrowth || nothing > m_l + kLead)) {
         // a new reference: what was summed under the old one is scaled down
-        const float a = now > m + kGrowth ? exp2_approx(m - now) : 1.0f;
-        if (now > m + kGrowth) m = now;
-        l *= a;
+        const bool grew = now > m + kGrowth;
+        const float a = grew ? exp2_approx(m - now) : 1.0f;
+        if (grew) m = now;
+        const float most = fmaxf(fmaxf(m, m_l), nothing > m_l + kLead ? nothing : m_l);
+        if (most > m_l) {
+          l *= exp2_approx(m_l - most);
+          m_l = most;
+        }
+        to_l = m == -INFINITY ? 0.0f : exp2_approx(m - m_l);
         if (j > 0) {
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) {
@@ -495,16 +532,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
               o[i] = half2_of(a, e);
             }
             sum2[0] = f32x2_add(sum2[0], sum2[1]);
-            sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * pow2i(-ev);
+            sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * (pow2i(-ev) * to_l);
           } else {
             // an exponent for each position; l counts P without it
             sum = 0.0f;
+            const float z_l = kPBias - (m_l == -INFINITY ? 0.0f : m_l);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float e0 = tm.pos_ev[k * 32 + 2 * i], e1 = tm.pos_ev[k * 32 + 2 * i + 1];
               const float a = exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, e0 + z));
               const float e = exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, e1 + z));
-              sum += a * pow2i(-(int)e0) + e * pow2i(-(int)e1);
+              sum += exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, z_l)) +
+                     exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, z_l));
               o[i] = half2_of(a, e);
             }
           }
@@ -530,18 +569,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     if (__all_sync(~0u, ok)) ok = mbar_wait(&sh.o_full[half], 0, abort_flag);
     if (__all_sync(~0u, ok)) {
       tc_fence_after();
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      // 2^(m - m_l) goes on in two halves: it can be below binary32's range where its product with O is not
+      const float half_to = m == -INFINITY ? 0.0f : exp2_approx(0.5f * (m - m_l));
+      const float inv = l == 0.0f ? 0.0f : half_to / l;
+      const auto out = [&](uint32_t x) { return (__uint_as_float(x) * half_to) * inv; };
       uint16_t *dst = p.out + (int64_t)(sq.first + r / p.G) * p.ldo + (int64_t)(h * p.G + r % p.G) * D;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(o_at + c * 32, o);
         tmem_ld_wait();
+        if (p.parts.splits > 1) {
+          if (r < R) {
+            float4 *to = reinterpret_cast<float4 *>(p.parts.o + part_row(r) * D + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              to[i] = make_float4(out(o[4 * i]), out(o[4 * i + 1]), out(o[4 * i + 2]), out(o[4 * i + 3]));
+            if (c == 0) p.parts.lse[part_row(r)] = l == 0.0f ? -INFINITY : m_l - kPBias + log2f(l);
+          }
+          continue;
+        }
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          w[i] = (uint32_t)f32_to_bf16_bits(__uint_as_float(o[2 * i]) * inv) |
-                 ((uint32_t)f32_to_bf16_bits(__uint_as_float(o[2 * i + 1]) * inv) << 16);
+          w[i] = (uint32_t)f32_to_bf16_bits(out(o[2 * i])) | ((uint32_t)f32_to_bf16_bits(out(o[2 * i + 1])) << 16);
         if (r < R) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -671,10 +722,11 @@ cudaError_t launch_d(PrefillParams p, int64_t group, cudaStream_t st) {
     const int64_t pairs = (int64_t)p.B * p.heads;
     e = launch_kernel(k_attn_unpack<D>, dim3((unsigned)(pairs * p.tiles)), dim3(64 * C::kUnits), 0, st, 1, p);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(k_attn_prefill<D>, dim3((unsigned)(pairs * p.row_tiles)), dim3(kThreads), C::kSmem, st, 1, p);
+    e = launch_kernel(k_attn_prefill<D>, dim3((unsigned)(pairs * p.row_tiles * p.parts.splits)), dim3(kThreads),
+                      C::kSmem, st, 1, p);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  return p.parts.splits > 1 ? launch_attn_join(p, p.parts, D, true, st) : cudaSuccess;
 }
 
 }  // namespace
@@ -683,12 +735,32 @@ bool attn_prefill_has(int64_t D) { return D == 64 || D == 128; }
 
 // kv heads are unpacked together until their images reach 2 GB (a quarter of
 // the positions of a full GPU of 8-bit cache), then in groups one after the other.
-AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t D, int64_t max_kv) {
+// Where the row tiles leave multiprocessors idle, positions are split so that the
+// waves of CTAs, times the position tiles of a part (and about two tiles' time to
+// begin and end one), are fewest; the join counts three.
+AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t max_q, int64_t max_kv,
+                                  int64_t window, int sms) {
   AttnPrefillPlan plan{};
   const int64_t tiles = std::max<int64_t>(1, (max_kv + kPos - 1) / kPos);
   const int64_t head = B * tiles * (4 * kPos * D + (int64_t)sizeof(TileMeta));
   plan.heads = std::max<int64_t>(1, std::min(H, ((int64_t)2 << 30) / head));
-  plan.ws_bytes = round_up((size_t)(head * plan.heads), 256);
+  plan.image_bytes = round_up((size_t)(head * plan.heads), 256);
+  constexpr int64_t rows = 2 * kRowTile;
+  plan.row_tiles = (max_q * G + rows - 1) / rows;
+  int64_t range = max_kv;
+  if (window > 0 && window < max_kv) range = std::min(range, window + rows / G + 1 + kPos);
+  const int64_t range_tiles = std::max<int64_t>(1, (range + kPos - 1) / kPos);
+  const int64_t ctas = B * H * plan.row_tiles;
+  plan.splits = 1;
+  int64_t least = (ctas + sms - 1) / sms * (range_tiles + 2);
+  for (int64_t s = 2; plan.heads == H && ctas < sms && s <= std::min<int64_t>(range_tiles / 2, 64); ++s) {
+    const int64_t cost = (ctas * s + sms - 1) / sms * ((range_tiles + s - 1) / s + 2) + 3;
+    if (cost < least) least = cost, plan.splits = s;
+  }
+  plan.chunk = (range_tiles + plan.splits - 1) / plan.splits;
+  plan.splits = (range_tiles + plan.chunk - 1) / plan.chunk;
+  plan.ws_bytes = plan.image_bytes;
+  if (plan.splits > 1) plan.ws_bytes += round_up((size_t)(ctas * plan.splits * rows * (D + 1) * 4), 256);
   return plan;
 }
 
@@ -696,10 +768,14 @@ cudaError_t launch_attn_prefill(const AttnArgs &a, const AttnPrefillPlan &plan, 
                                 unsigned *status, cudaStream_t st) {
   PrefillParams p{};
   static_cast<AttnDev &>(p) = attn_dev(a, few_rows, status);
-  p.row_tiles = (int)((a.max_q * (a.Hq / a.H) + 2 * kRowTile - 1) / (2 * kRowTile));
+  p.row_tiles = (int)plan.row_tiles;
   p.tiles = (int)std::max<int64_t>(1, (a.max_kv + kPos - 1) / kPos);
   p.images = (uint8_t *)ws;
   p.heads = (int)plan.heads;
+  p.chunk = (int)plan.chunk;
+  p.parts.row_tiles = p.row_tiles, p.parts.rows = 2 * kRowTile, p.parts.splits = (int)plan.splits;
+  p.parts.o = reinterpret_cast<float *>((char *)ws + plan.image_bytes);
+  p.parts.lse = p.parts.o + a.B * a.H * plan.row_tiles * plan.splits * p.parts.rows * a.D;
   if (a.D == 64) return launch_d<64>(p, plan.heads, st);
   if (a.D == 128) return launch_d<128>(p, plan.heads, st);
   return cudaErrorInvalidValue;

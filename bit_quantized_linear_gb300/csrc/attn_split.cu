@@ -44,9 +44,8 @@ constexpr int kAlign = 32;   // parts begin at multiples of this: the most posit
 
 struct SplitParams : AttnDev {
   unsigned group_inverse;  // 2^16 / G rounded up: (x * it) >> 16 is x / G for x < 256 (G <= 128)
-  float *part_o, *part_lse;
+  AttnParts parts;
   int64_t chunk;
-  int row_tiles, splits;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -153,10 +152,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const uint32_t ring_at = tc::smem_u32(ring);
 
   const int64_t cta = blockIdx.x;
-  const int split = (int)(cta % p.splits);
-  const int64_t unit = cta / p.splits;
-  const int tile = (int)(unit % p.row_tiles);
-  const int h = (int)(unit / p.row_tiles % p.H), b = (int)(unit / p.row_tiles / p.H);
+  const int split = (int)(cta % p.parts.splits);
+  const int64_t unit = cta / p.parts.splits;
+  const int tile = (int)(unit % p.parts.row_tiles);
+  const int h = (int)(unit / p.parts.row_tiles % p.H), b = (int)(unit / p.parts.row_tiles / p.H);
   const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
   const int own = lane & (kTile - 1);  // the position of a tile whose scales (and page) a lane sees to
   const bool even = p.block_size % kTile == 0;  // a tile lies in one page
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     sees(p, sq, token_of(last), unused, hi);
     const int64_t from = (int64_t)(lo & ~(kAlign - 1)) + (int64_t)split * p.chunk;
     beg = (int)min(from, (int64_t)max(hi, 0));
-    end = split == p.splits - 1 ? max(hi, beg) : (int)min(from + p.chunk, (int64_t)max(hi, beg));
+    end = split == p.parts.splits - 1 ? max(hi, beg) : (int)min(from + p.chunk, (int64_t)max(hi, beg));
   }
 
   // ---- the ring: tile n covers positions beg + (n * warps + warp) * 16 ...
@@ -593,7 +592,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    if (p.splits == 1) {
+    if (p.parts.splits == 1) {
       const int rr = r0 + r;
       uint16_t *dst = p.out + (int64_t)(sq.first + rr / p.G) * p.ldo + (int64_t)(h * p.G + rr % p.G) * D + d;
       *reinterpret_cast<uint2 *>(dst) =
@@ -601,8 +600,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
                      (uint32_t)f32_to_bf16_bits(o.z) | ((uint32_t)f32_to_bf16_bits(o.w) << 16));
     } else {
       const int64_t at = cta * kRows + r;
-      *reinterpret_cast<float4 *>(p.part_o + at * D + d) = o;
-      if (d == 0) p.part_lse[at] = L == 0.0f ? -INFINITY : top + log2f(L);
+      *reinterpret_cast<float4 *>(p.parts.o + at * D + d) = o;
+      if (d == 0) p.parts.lse[at] = L == 0.0f ? -INFINITY : top + log2f(L);
     }
   }
 }
@@ -613,7 +612,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
 constexpr int kFewParts = 16;
 constexpr int kManyWarps = 16, kFewWarps = 8;  // warps of a CTA
 template <int D, bool MANY>
-__global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_join(const SplitParams p, int rows) {
+__global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_join(const AttnDev p, const AttnParts parts, bool many) {
+  const int rows = parts.rows;
   constexpr int V = D / 32;                  // floats of a lane
   constexpr int kOver = MANY ? kManyWarps : 1;  // warps that share a row
   constexpr int kBatch = MANY ? 8 : 4;       // parts whose loads are in flight at once
@@ -623,16 +623,16 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_j
   const int64_t row = MANY ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kFewWarps + warp;
   const int64_t unit = row / rows;
   const int r = (int)(row % rows);
-  const int tile = (int)(unit % p.row_tiles);
-  const int h = (int)(unit / p.row_tiles % p.H), b = (int)(unit / p.row_tiles / p.H);
+  const int tile = (int)(unit % parts.row_tiles);
+  const int h = (int)(unit / parts.row_tiles % p.H), b = (int)(unit / parts.row_tiles / p.H);
   pdl_wait();
   pdl_trigger();
   if (b >= p.B) return;
   const Sequence sq = sequence(p, b);
   const int rr = tile * rows + r;
-  if (rr >= sq.kept * p.G || sq.kept * p.G > p.few_rows) return;
-  const float *lse = p.part_lse + unit * p.splits * rows + r;
-  const float *src = p.part_o + (unit * p.splits * rows + r) * D + lane * V;
+  if (rr >= sq.kept * p.G || (sq.kept * p.G > p.few_rows) != many) return;
+  const float *lse = parts.lse + unit * parts.splits * rows + r;
+  const float *src = parts.o + (unit * parts.splits * rows + r) * D + lane * V;
   uint32_t x[kBatch][V];
   float e[kBatch];
   const auto load = [&](int s0) {
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_j
       e[i] = -INFINITY;
 #pragma unroll
       for (int v = 0; v < V; ++v) x[i][v] = 0u;
-      if (s < p.splits) {
+      if (s < parts.splits) {
         e[i] = __ldg(lse + s * rows);
         load_words<V>(src + s * rows * D, x[i]);
       }
@@ -650,13 +650,13 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_j
   };
   load(part);
   float top = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, __ldg(lse + (int64_t)s * rows));
+  for (int s = lane; s < parts.splits; s += 32) top = fmaxf(top, __ldg(lse + (int64_t)s * rows));
   top = warp_max(top);
   const float z = top == -INFINITY ? 0.0f : top;
   float o[V], W = 0.0f;
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
-  for (int s0 = part; s0 < p.splits;) {
+  for (int s0 = part; s0 < parts.splits;) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const float w = exp2_approx(e[i] - z);  // 0 beyond the last part
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_j
       for (int v = 0; v < V; ++v) o[v] = fmaf(w, __uint_as_float(x[i][v]), o[v]);
     }
     s0 += kBatch * kOver;
-    if (s0 < p.splits) load(s0);
+    if (s0 < parts.splits) load(s0);
   }
   uint16_t *dst = p.out + (int64_t)(sq.first + rr / p.G) * p.ldo + (int64_t)(h * p.G + rr % p.G) * D;
   if constexpr (MANY) {
@@ -712,15 +712,18 @@ cudaError_t launch_nt(const SplitParams &p, int64_t units, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  e = launch_kernel(k_attn_split<D, NT>, dim3((unsigned)(units * p.splits)), dim3(32 * kAttnWarps), Geo::kSmem, st, 1,
+  e = launch_kernel(k_attn_split<D, NT>, dim3((unsigned)(units * p.parts.splits)), dim3(32 * kAttnWarps), Geo::kSmem, st, 1,
                     p);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  const int64_t rows = units * Geo::kRows;
-  if (p.splits <= kFewParts)
+  if (e != cudaSuccess || p.parts.splits == 1) return e;
+  return launch_attn_join(p, p.parts, D, false, st);
+}
+template <int D>
+cudaError_t launch_join_d(const AttnDev &p, const AttnParts &parts, bool many, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.B * p.H * parts.row_tiles * parts.rows;
+  if (parts.splits <= kFewParts)
     return launch_kernel(k_attn_join<D, false>, dim3((unsigned)((rows + kFewWarps - 1) / kFewWarps)),
-                         dim3(32 * kFewWarps), 0, st, 1, p, (int)Geo::kRows);
-  return launch_kernel(k_attn_join<D, true>, dim3((unsigned)rows), dim3(32 * kManyWarps), 0, st, 1, p,
-                       (int)Geo::kRows);
+                         dim3(32 * kFewWarps), 0, st, 1, p, parts, many);
+  return launch_kernel(k_attn_join<D, true>, dim3((unsigned)rows), dim3(32 * kManyWarps), 0, st, 1, p, parts, many);
 }
 template <int D>
 cudaError_t launch_d(const SplitParams &p, int rows, int64_t units, cudaStream_t st) {
@@ -728,6 +731,16 @@ cudaError_t launch_d(const SplitParams &p, int rows, int64_t units, cudaStream_t
 }
 
 }  // namespace
+
+cudaError_t launch_attn_join(const AttnDev &p, const AttnParts &parts, int64_t D, bool many, cudaStream_t st) {
+  switch (D) {
+    case 32: return launch_join_d<32>(p, parts, many, st);
+    case 64: return launch_join_d<64>(p, parts, many, st);
+    case 128: return launch_join_d<128>(p, parts, many, st);
+    case 256: return launch_join_d<256>(p, parts, many, st);
+  }
+  return cudaErrorInvalidValue;
+}
 
 AttnDev attn_dev(const AttnArgs &a, int few_rows, unsigned *status) {
   AttnDev p{};
@@ -779,10 +792,10 @@ cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, int 
   SplitParams p{};
   static_cast<AttnDev &>(p) = attn_dev(a, few_rows, status);
   p.group_inverse = (65536u + p.G - 1) / p.G;
-  p.row_tiles = plan.row_tiles, p.splits = plan.splits, p.chunk = plan.chunk;
+  p.parts.row_tiles = plan.row_tiles, p.parts.rows = plan.rows, p.parts.splits = plan.splits, p.chunk = plan.chunk;
   const int64_t units = a.B * a.H * plan.row_tiles;
-  p.part_o = (float *)ws;
-  p.part_lse = p.part_o ? p.part_o + units * plan.splits * plan.rows * a.D : nullptr;
+  p.parts.o = (float *)ws;
+  p.parts.lse = p.parts.o ? p.parts.o + units * plan.splits * plan.rows * a.D : nullptr;
   switch (a.D) {
     case 32: return launch_d<32>(p, plan.rows, units, st);
     case 64: return launch_d<64>(p, plan.rows, units, st);

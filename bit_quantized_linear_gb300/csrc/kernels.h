@@ -286,10 +286,14 @@ cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, int 
                               cudaStream_t st);
 bool attn_prefill_has(int64_t D);
 struct AttnPrefillPlan {
-  int64_t heads;  // kv heads whose keys and values are in the workspace at once
-  size_t ws_bytes;
+  int64_t heads;      // kv heads whose keys and values are in the workspace at once
+  int64_t row_tiles;  // of 256 rows, for a sequence
+  int64_t splits;     // parts of the positions, each a CTA
+  int64_t chunk;      // position tiles of a part
+  size_t image_bytes, ws_bytes;
 };
-AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t D, int64_t max_kv);
+AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t max_q, int64_t max_kv,
+                                  int64_t window, int sms);
 cudaError_t launch_attn_prefill(const AttnArgs &a, const AttnPrefillPlan &plan, int few_rows, void *ws,
                                 unsigned *status, cudaStream_t st);
 

@@ -1,6 +1,7 @@
 // C-ABI shims of the decoder-layer operators around the linears: RMSNorm,
 // the W8A8 linear on given codes, rotary positions and attention over the mixed
 // KV cache.  Argument checks on the host, then launches on the caller's stream.
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -54,11 +55,23 @@ qlin_status check_attn_sizes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_
   return QLIN_OK;
 }
 
-// Which kernel takes which sequences: where some may have more than kFewRows rows
-// for a kv head, those go to the tcgen05 kernel and the others of the batch to
-// the split kernel; each kernel leaves the other's sequences.  A lone sequence
-// goes to one kernel by its bound.
+// Which kernel takes which sequences.  The split kernel reads all positions once
+// for every 16 rows, 4e-5 us for each (16 rows, kv head, position) when it fills the
+// GPU; the tcgen05 kernels take 20 us (and with a batch 30, the other kernel being
+// launched as well) whatever they do.  So where a sequence may have more rows than
+// come to that much (of a batch, half of the bound on average), they take those
+// sequences of the batch that have more than kFewRows rows, and the split kernel
+// the others; each leaves the other's sequences.  A lone sequence goes to one kernel
+// by its bound.  Measured, 28 heads over 4, one sequence: 8192 positions, 84 rows
+// 27.7 us split and 25.6 us tcgen05, 336 rows 55 and 36; 1024 positions, 336 rows
+// 14.8 and 23.3, 1344 rows 39 and 27.  Four sequences: 8192 positions, 84 rows 34.7
+// and 54, 336 rows 79 and 65.
 constexpr int64_t kFewRows = 64;
+int64_t attn_most_split_rows(int64_t B, int64_t H, int64_t max_kv, int64_t window) {
+  const int64_t range = window > 0 ? std::min(window, max_kv) : max_kv;
+  const int64_t rows = (B > 1 ? 20000000 : 6000000) / std::max<int64_t>(1, B * H * range);
+  return std::min<int64_t>(std::max<int64_t>(rows, kFewRows), 512);
+}
 struct AttnRoute {
   bool few, many;  // the split kernel, the tcgen05 kernel
   int few_rows;
@@ -69,10 +82,10 @@ struct AttnRoute {
 AttnRoute attn_route(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv, int64_t window) {
   AttnRoute r{};
   const int64_t rows = max_q * (Hq / H);
-  r.many = attn_prefill_has(D) && rows > kFewRows;
+  r.many = attn_prefill_has(D) && rows > attn_most_split_rows(B, H, max_kv, window);
   r.few = !r.many || B > 1;
   r.few_rows = r.many ? (r.few ? (int)kFewRows : 0) : (int)rows;
-  if (r.many) r.prefill = attn_prefill_plan(B, H, D, max_kv);
+  if (r.many) r.prefill = attn_prefill_plan(B, H, Hq / H, D, max_q, max_kv, window, sm_count());
   if (r.few) r.split = attn_split_plan(B, Hq, H, D, r.few_rows, max_kv, window, sm_count());
   return r;
 }
@@ -188,8 +201,12 @@ const char *qlin_attn_mixed_kernel_name(int64_t B, int64_t Hq, int64_t H, int64_
   if (check_attn_sizes(B, Hq, H, D, max_q, max_kv, window)) return "invalid";
   if (B == 0 || max_q == 0) return "none";
   const AttnRoute r = attn_route(B, Hq, H, D, max_q, max_kv, window);
-  if (!r.few) return "k_attn_unpack+k_attn_prefill";
-  if (r.many) return r.split.splits > 1 ? "k_attn_unpack+k_attn_prefill+k_attn_split+k_attn_join" : "k_attn_unpack+k_attn_prefill+k_attn_split";
+  static const char *many[2][3] = {
+      {"k_attn_unpack+k_attn_prefill", "k_attn_unpack+k_attn_prefill+k_attn_split",
+       "k_attn_unpack+k_attn_prefill+k_attn_split+k_attn_join"},
+      {"k_attn_unpack+k_attn_prefill+k_attn_join", "k_attn_unpack+k_attn_prefill+k_attn_join+k_attn_split",
+       "k_attn_unpack+k_attn_prefill+k_attn_join+k_attn_split+k_attn_join"}};
+  if (r.many) return many[r.prefill.splits > 1][!r.few ? 0 : r.split.splits > 1 ? 2 : 1];
   return r.split.splits > 1 ? "k_attn_split+k_attn_join" : "k_attn_split";
 }
 
