@@ -5,9 +5,9 @@
 // the workspace, as the very images of shared memory that the products read: per
 // 128 positions a K-major key tile and a V^T tile (positions along the row), both
 // in the 128-byte swizzle, and what the softmax needs beside them.  (Converting
-// in the product kernel, by warps of its own, cost 2.3 times the time at 8192 x
-// 16384: every row tile converts the same codes again, and the two kinds of code
-// drive one another out of the instruction cache.)
+// in the product kernel, by warps of its own, took 1.75 ms against 1.36 ms at
+// 8192 new tokens over 16384 positions, 28 heads over 4 of 128: every row tile
+// converts the same codes again.)
 //
 // k_attn_prefill: a CTA takes 256 rows of one (sequence, kv head), packed
 // token-major over the heads of the group, as two row tiles A and B of 128, and
@@ -31,6 +31,7 @@
 // reference (they would push P of the others out of float16): they count in the
 // sum of the row alone, which for that has a reference of its own.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.cuh"
 #include "common.cuh"
@@ -425,146 +426,164 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     // O is sum p v under the reference m, l is sum p under m_l >= m; to_l = 2^(m - m_l)
     float m = -INFINITY, m_l = -INFINITY, l = 0.0f, to_l = 0.0f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
-           mbar_wait(&sh.s_full[half], j & 1, abort_flag);
-      if (!__all_sync(~0u, ok)) break;
-      tc_fence_after();
-      const TileMeta &tm = sh.meta[j % kMetaSlots];
-      const int j0 = beg + j * kPos;
-      const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
-                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
-                        (tm.poison[0] | tm.poison[1] | tm.poison[2] | tm.poison[3]) == 0;
-      // Scores this row does not see become -inf, those of a NaN value NaN (32 columns
-      // from c * 32 on).
-      const auto mask = [&](int c, uint32_t (&s)[32]) {
-        const int from = row_lo - (j0 + c * 32), to = row_hi - (j0 + c * 32);
-        unsigned seen = tm.valid[c];
-        seen &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
-        seen &= to <= 0 ? 0u : to >= 32 ? ~0u : ~(~0u << to);
+    int j = 0;
+    // The tiles from j on; without ANY, up to the first with a unit that is wide (m_l
+    // is m until then).  Such tiles are rare, and their code in the loop of the others
+    // costs each of them: 1342 us against 1169 at 8192 x 16384, 28 heads over 4 of 128.
+    const auto tiles = [&](auto any) {
+      constexpr bool ANY = decltype(any)::value;
+      for (; j < n; ++j) {
+        ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
+             mbar_wait(&sh.s_full[half], j & 1, abort_flag);
+        if (!__all_sync(~0u, ok)) break;
+        tc_fence_after();
+        const TileMeta &tm = sh.meta[j % kMetaSlots];
+        if (!ANY && (tm.wide[0] | tm.wide[1] | tm.wide[2] | tm.wide[3])) break;
+        const int j0 = beg + j * kPos;
+        const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
+                          (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
+                          (tm.poison[0] | tm.poison[1] | tm.poison[2] | tm.poison[3]) == 0;
+        // Scores this row does not see become -inf, those of a NaN value NaN (32 columns
+        // from c * 32 on).
+        const auto mask = [&](int c, uint32_t (&s)[32]) {
+          const int from = row_lo - (j0 + c * 32), to = row_hi - (j0 + c * 32);
+          unsigned seen = tm.valid[c];
+          seen &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+          seen &= to <= 0 ? 0u : to >= 32 ? ~0u : ~(~0u << to);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1 ? s[i] : 0xFF800000u;
-        const unsigned bad = tm.poison[c] & seen;
-        if (bad) {
+          for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1 ? s[i] : 0xFF800000u;
+          const unsigned bad = tm.poison[c] & seen;
+          if (bad) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = (bad >> i) & 1 ? 0x7FFFFFFFu : s[i];
-        }
-      };
-      // a score's factor (never 0, so that -inf stays -inf)
-      const auto factor = [&](int ek) { return fmaxf(row_factor * pow2i(ek), 0x1p-100f); };
-
-      // S into registers and the row's largest exponent
-      uint32_t s[4][32];
-      float f[4];
-      int ev[4];
-      unsigned wide[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld32(s_at + c * 32, s[c]);
-        f[c] = factor(tm.ek[c]);
-        ev[c] = tm.ev[c];
-        wide[c] = tm.wide[c];
-      }
-      tmem_ld_wait();
-      if (__builtin_expect(!full, 0)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mask(c, s[c]);
-      }
-      float now = m, nothing = -INFINITY;  // nothing: the largest score of a position without a value
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float mx = -INFINITY;
-        if (__builtin_expect(wide[c] == 0, 1)) {
-          float t[4];  // four chains
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[c][i]);
-#pragma unroll
-          for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[c][i]));
-          mx = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = __uint_as_float(s[c][i]) * f[c], e = tm.pos_ev[c * 32 + i];
-            mx = fmaxf(mx, x + e);
-            if (e == -INFINITY) nothing = fmaxf(nothing, x);
+            for (int i = 0; i < 32; ++i) s[i] = (bad >> i) & 1 ? 0x7FFFFFFFu : s[i];
           }
-        }
-        now = fmaxf(now, mx);
-      }
-      if (__any_sync(~0u, now > m + kGrowth || nothing > m_l + kLead)) {
-        // a new reference: what was summed under the old one is scaled down
-        const bool grew = now > m + kGrowth;
-        const float a = grew ? exp2_approx(m - now) : 1.0f;
-        if (grew) m = now;
-        const float most = fmaxf(fmaxf(m, m_l), nothing > m_l + kLead ? nothing : m_l);
-        if (most > m_l) {
-          l *= exp2_approx(m_l - most);
-          m_l = most;
-        }
-        to_l = m == -INFINITY ? 0.0f : exp2_approx(m - m_l);
-        if (j > 0) {
-#pragma unroll 1
-          for (int k = 0; k < D / 16; ++k) {
-            uint32_t o[16];
-            tmem_ld16(o_at + k * 16, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-            tmem_st16(o_at + k * 16, o);
-          }
-        }
-      }
-      // P = 2^(s + ev - m + bias), over S
-      {
-        const float z = kPBias - (m == -INFINITY ? 0.0f : m);
-        const auto probabilities = [&](int k, const uint32_t (&s)[32], float f, int ev, unsigned wide) {
-          uint32_t o[16];
-          float sum;
-          if (__builtin_expect(wide == 0, 1)) {
-            const float g = (float)ev + z;
-            const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
-            uint64_t sum2[2] = {0, 0};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
-              const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
-              sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
-              o[i] = half2_of(a, e);
-            }
-            sum2[0] = f32x2_add(sum2[0], sum2[1]);
-            sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * (pow2i(-ev) * to_l);
-          } else {
-            // an exponent for each position; l counts P without it
-            sum = 0.0f;
-            const float z_l = kPBias - (m_l == -INFINITY ? 0.0f : m_l);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float e0 = tm.pos_ev[k * 32 + 2 * i], e1 = tm.pos_ev[k * 32 + 2 * i + 1];
-              const float a = exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, e0 + z));
-              const float e = exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, e1 + z));
-              sum += exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, z_l)) +
-                     exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, z_l));
-              o[i] = half2_of(a, e);
-            }
-          }
-          l += sum;
-          tmem_st16(s_at + k * 16, o);
         };
+        // a score's factor (never 0, so that -inf stays -inf)
+        const auto factor = [&](int ek) { return fmaxf(row_factor * pow2i(ek), 0x1p-100f); };
+
+        // S into registers and the row's largest exponent
+        uint32_t s[4][32];
+        float f[4];
+        int ev[4];
+        unsigned wide[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          probabilities(c, s[c], f[c], ev[c], wide[c]);
-          if (c == 1) {  // the first half of P: its products start
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_half[half]);
+          tmem_ld32(s_at + c * 32, s[c]);
+          f[c] = factor(tm.ek[c]);
+          ev[c] = tm.ev[c];
+          wide[c] = ANY ? tm.wide[c] : 0;
+        }
+        tmem_ld_wait();
+        if (__builtin_expect(!full, 0)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mask(c, s[c]);
+        }
+        float now = m, nothing = -INFINITY;  // nothing: the largest score of a position without a value
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float mx = -INFINITY;
+          if (!ANY || wide[c] == 0) {
+            float t[4];  // four chains
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[c][i]);
+#pragma unroll
+            for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[c][i]));
+            mx = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = __uint_as_float(s[c][i]) * f[c], e = tm.pos_ev[c * 32 + i];
+              mx = fmaxf(mx, x + e);
+              if (e == -INFINITY) nothing = fmaxf(nothing, x);
+            }
+          }
+          now = fmaxf(now, mx);
+        }
+        if (__any_sync(~0u, now > m + kGrowth || (ANY && nothing > m_l + kLead))) {
+          // a new reference: what was summed under the old one is scaled down
+          const bool grew = now > m + kGrowth;
+          const float a = grew ? exp2_approx(m - now) : 1.0f;
+          if (grew) m = now;
+          if constexpr (ANY) {
+            const float most = fmaxf(fmaxf(m, m_l), nothing > m_l + kLead ? nothing : m_l);
+            if (most > m_l) {
+              l *= exp2_approx(m_l - most);
+              m_l = most;
+            }
+            to_l = m == -INFINITY ? 0.0f : exp2_approx(m - m_l);
+          } else {
+            l *= a;
+          }
+          if (j > 0) {
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t o[16];
+              tmem_ld16(o_at + k * 16, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st16(o_at + k * 16, o);
+            }
           }
         }
+        // P = 2^(s + ev - m + bias), over S
+        {
+          const float z = kPBias - (m == -INFINITY ? 0.0f : m);
+          const auto probabilities = [&](int k, const uint32_t (&s)[32], float f, int ev, unsigned wide) {
+            uint32_t o[16];
+            float sum;
+            if (!ANY || wide == 0) {
+              const float g = (float)ev + z;
+              const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
+              uint64_t sum2[2] = {0, 0};
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
+                const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
+                sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
+                o[i] = half2_of(a, e);
+              }
+              sum2[0] = f32x2_add(sum2[0], sum2[1]);
+              sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * (ANY ? pow2i(-ev) * to_l : pow2i(-ev));
+            } else {
+              // an exponent for each position; l counts P without it
+              sum = 0.0f;
+              const float z_l = kPBias - (m_l == -INFINITY ? 0.0f : m_l);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float e0 = tm.pos_ev[k * 32 + 2 * i], e1 = tm.pos_ev[k * 32 + 2 * i + 1];
+                const float a = exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, e0 + z));
+                const float e = exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, e1 + z));
+                sum += exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, z_l)) +
+                       exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, z_l));
+                o[i] = half2_of(a, e);
+              }
+            }
+            l += sum;
+            tmem_st16(s_at + k * 16, o);
+          };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            probabilities(c, s[c], f[c], ev[c], wide[c]);
+            if (c == 1) {  // the first half of P: its products start
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.p_half[half]);
+            }
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[half]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[half]);
+    };
+    tiles(std::false_type{});
+    m_l = m;
+    if (j < n && __all_sync(~0u, ok)) {
+      to_l = m == -INFINITY ? 0.0f : 1.0f;
+      tiles(std::true_type{});
     }
     if (__all_sync(~0u, ok)) ok = mbar_wait(&sh.o_full[half], 0, abort_flag);
     if (__all_sync(~0u, ok)) {

@@ -59,30 +59,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
-// mbar_wait for waits that are expected to be long: the thread sleeps in the
-// hardware for up to `ns` at a time instead of polling, which leaves the issue
-// slots to the other warps.
-__device__ __forceinline__ bool mbar_try_wait_ns(uint32_t addr, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(addr), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_asleep(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-  const uint32_t addr = smem_u32(bar);
-  if (mbar_try_wait(addr, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!mbar_try_wait_ns(addr, parity, 20000)) {
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  }
-  return true;
-}
-
 // Waits (bounded, whatever the abort flag says) for copies or MMA commits this
 // CTA issued to land before it leaves: no async write may reach shared memory
 // the next CTA on the SM already owns.  A copy in flight lands within
