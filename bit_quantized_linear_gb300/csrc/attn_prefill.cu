@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
   for (int i = 0; i < kWords; ++i) {
     const int j = tile * kPos + block * C::kUnit + i * 32 + lane, blk = block_of(p, j);
     const bool wanted = j >= lo && j < hi;
-    const int page = wanted ? __ldg(table + blk) : -1;
+    const int page = wanted ? ld_input(table + blk) : -1;
     const bool ok = page >= 0 && page < p.num_blocks;
     if (wanted && !ok) set_status(p.status, QLIN_ERR_INVALID_ARG);
     valid[i] = __ballot_sync(~0u, ok);
@@ -175,19 +175,20 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
       const int64_t other = __shfl_sync(~0u, row[1], t & 31);
       if (t >= 32) at = other, there = valid[1];
     }
-    code[i] = (there >> (t & 31)) & 1 ? __ldg(reinterpret_cast<const uint4 *>(codes + at * D)) : make_uint4(0, 0, 0, 0);
+    code[i] = (there >> (t & 31)) & 1 ? ld_input(reinterpret_cast<const uint4 *>(codes + at * D))
+                                      : make_uint4(0, 0, 0, 0);
   }
   uint32_t scale[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
     if (!((valid[i] >> lane) & 1)) continue;
     if (value) {
-      scale[i] = __ldg(p.vs + row[i]);
+      scale[i] = ld_input(p.vs + row[i]);
     } else if constexpr (kWords == 1) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p.ks + row[0] * (D / 32)));
+      const uint2 w = ld_input(reinterpret_cast<const uint2 *>(p.ks + row[0] * (D / 32)));
       scale[0] = w.x, scale[1] = w.y;
     } else {
-      scale[i] = __ldg(reinterpret_cast<const uint32_t *>(p.ks + row[i] * (D / 32)));
+      scale[i] = ld_input(reinterpret_cast<const uint32_t *>(p.ks + row[i] * (D / 32)));
     }
   }
   // exponent e of a scale, 2^e <= |s| < 2^(e+1); those that are not finite count as the largest

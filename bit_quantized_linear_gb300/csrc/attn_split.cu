@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const int64_t guess = (int64_t)split * p.chunk + warp * kTile + (even ? 0 : own);
   int guessed = -1;
   if (p.window == 0 && guess < p.max_kv && block_of(p, (int)guess) < p.max_blocks)
-    guessed = __ldg(table + block_of(p, (int)guess));
+    guessed = ld_input(table + block_of(p, (int)guess));
   const Sequence sq = sequence(p, b);
   if (sq.broken && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
   const int R = sq.kept * p.G, r0 = tile * kRows;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
       if (r0 + i < R) {
         const uint16_t *row = p.q + (int64_t)(sq.first + tok) * p.ldq +
                               (int64_t)(h * p.G + r0 + i - tok * p.G) * D + k * 32 + t * 8;
-        qw[nt][k] = __ldg(reinterpret_cast<const uint4 *>(row));
+        qw[nt][k] = ld_input(reinterpret_cast<const uint4 *>(row));
       }
     }
   }
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const auto page = [&](int n) {  // page of the lane's position of tile n (-1: none)
     const int j = first_of(n) + (even ? 0 : own);
     return n < mine && (whole(n) || (j + (even ? own : 0) >= lo && j + (even ? own : 0) < end))
-               ? __ldg(table + block_of(p, j)) : -1;
+               ? ld_input(table + block_of(p, j)) : -1;
   };
   const int piece_row = lane / Geo::kChunks, piece = lane % Geo::kChunks;
   const int64_t row_bytes = (int64_t)p.H * D;
@@ -221,9 +221,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   unsigned there = 0;  // which positions of that tile are there
   int next_page = p.window == 0 && mine > 0 ? guessed : page(0);
   const auto load_scales = [&](int64_t row) {  // row: (slot, head) of the lane's position
-    sv = __ldg(p.vs + row);
+    sv = ld_input(p.vs + row);
     if constexpr (kGroups == 1) {
-      sc[0] = __ldg(p.ks + row);
+      sc[0] = ld_input(p.ks + row);
     } else {
       load_words<kGroups / 2>(p.ks + row * kGroups, sc);
     }
@@ -643,14 +643,14 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_j
 #pragma unroll
       for (int v = 0; v < V; ++v) x[i][v] = 0u;
       if (s < parts.splits) {
-        e[i] = __ldg(lse + s * rows);
+        e[i] = ld_input(lse + s * rows);
         load_words<V>(src + s * rows * D, x[i]);
       }
     }
   };
   load(part);
   float top = -INFINITY;
-  for (int s = lane; s < parts.splits; s += 32) top = fmaxf(top, __ldg(lse + (int64_t)s * rows));
+  for (int s = lane; s < parts.splits; s += 32) top = fmaxf(top, ld_input(lse + (int64_t)s * rows));
   top = warp_max(top);
   const float z = top == -INFINITY ? 0.0f : top;
   float o[V], W = 0.0f;

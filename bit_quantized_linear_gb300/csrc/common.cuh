@@ -4,6 +4,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "qlin.h"
 
@@ -204,6 +205,40 @@ __device__ __forceinline__ float warp_max(float v) {
 // lets the next kernel start its own prologue early.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A load of memory that an earlier kernel of the stream may write: after pdl_wait().
+// Not __ldg: the non-coherent load is defined only for memory that nobody writes
+// while the kernel lives, and this kernel lives before its predecessor's end, so
+// the compiler may move it above the wait.  (With __ldg a W8A16 linear after a merged
+// gate_up in a graph read its input before it was written.)  Volatile, it stays below.
+template <typename T>
+__device__ __forceinline__ T ld_input(const T *p) {
+  static_assert(sizeof(T) <= 2 || sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16, "size of a load");
+  T out;
+  if constexpr (sizeof(T) == 16) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    memcpy(&out, &v, 16);
+  } else if constexpr (sizeof(T) == 8) {
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    memcpy(&out, &v, 8);
+  } else if constexpr (sizeof(T) == 4) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    memcpy(&out, &v, 4);
+  } else if constexpr (sizeof(T) == 2) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    memcpy(&out, &v, 2);
+  } else {
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    const uint8_t b = (uint8_t)v;
+    memcpy(&out, &b, 1);
+  }
+  return out;
+}
 
 // Sets the device status word (first error wins).
 __device__ __forceinline__ void set_status(unsigned *status, unsigned code) {

@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(Fp8CfgT<XQ, PAIR>::THREADS, 1)
       }
     } else {  // ---- conversion: warps 12..15, 128 threads
       const int qt = threadIdx.x - 384;
-      const StaticE4m3 xs = make_static_e4m3(__ldg(p.x_scale));
+      const StaticE4m3 xs = make_static_e4m3(ld_input(p.x_scale));
       for (int c = 0; c < chunks; ++c) {
         const int b = c % NB;
         // the warp takes one path whatever each lane's bounded wait saw
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(Fp8CfgT<XQ, PAIR>::THREADS, 1)
   } else if (warp >= 4) {  // ------------------------- epilogue
     const int q4 = warp & 3, half = (warp - 4) >> 2;  // half h owns channels [128h, 128h + 128)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-    const float sx = p.xs_per_token ? 1.0f : __ldg(p.x_scale);
+    const float sx = p.xs_per_token ? 1.0f : ld_input(p.x_scale);
     // Output path: each 32 x 32 block of BF16 results (row = lane) is written into
     // one of this warp's two staging blocks with the 64-byte swizzle (16-byte chunk
     // q of row r at chunk q ^ ((r >> 1) & 3): the lanes' row writes hit distinct
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(Fp8CfgT<XQ, PAIR>::THREADS, 1)
         continue;
       }
       // per-token activation scale multiplies the row (lane = token)
-      const float sxm = p.xs_per_token ? (m < p.M ? __ldg(p.x_scale + m) : 0.0f) : 1.0f;
+      const float sxm = p.xs_per_token ? (m < p.M ? ld_input(p.x_scale + m) : 0.0f) : 1.0f;
       if (p.glu) {
         // columns [0,128) hold gate channels n0/2 + c, columns [128,256) the matching up
         // channels; half h takes gate columns [64h, 64h + 64) and their up partners
@@ -1056,7 +1056,7 @@ __global__ void __launch_bounds__(640, 1)
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
     bool ok = true;
     Scale xsc{1.0f, 1.0f, true};
-    if constexpr (kXQ) xsc = make_scale(__ldg(p.x_scale));
+    if constexpr (kXQ) xsc = make_scale(ld_input(p.x_scale));
     for (int i = quad; i < total; i += C::QUADS) {
       const int r = i % C::R, sa = i % C::NA;
       if (!mbar_wait(&raw_full[r], (i / C::R) & 1, abort_flag)) {
@@ -1130,7 +1130,7 @@ __global__ void __launch_bounds__(640, 1)
       scl_b[nl] = MODE != kSwapI8Raw && in && p.bias ? bf16_bits_to_f32(__ldg(p.bias + ch)) : 0.0f;
       for (int t = nl; t < BNT; t += 128)
         scl_x[t] = MODE == kSwapI8Scaled || MODE == kSwapI8Fused
-                       ? (p.xs_per_token ? (mu + t < p.M ? __ldg(p.x_scale + mu + t) : 0.0f) : __ldg(p.x_scale))
+                       ? (p.xs_per_token ? (mu + t < p.M ? ld_input(p.x_scale + mu + t) : 0.0f) : ld_input(p.x_scale))
                        : 1.0f;
     }
     int cidx = 0, xround = 0;
@@ -1209,7 +1209,7 @@ __global__ void __launch_bounds__(640, 1)
         constexpr bool kScaled = MODE != kSwapI8Raw;
         sw = kScaled && S == 1 && valid ? __ldg(p.w_scale + wrow) : 0.0f;
         b = kScaled && S == 1 && valid && p.bias ? bf16_bits_to_f32(__ldg(p.bias + wrow)) : 0.0f;
-        sx = kScaled && kI8 && S == 1 ? __ldg(p.x_scale) : 1.0f;
+        sx = kScaled && kI8 && S == 1 ? ld_input(p.x_scale) : 1.0f;
       };
       float sw_u = 0.0f, b_u = 0.0f, sx_u = 1.0f;
       if constexpr (kEarly) row_factors(sw_u, b_u, sx_u);
@@ -1387,7 +1387,7 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
                   for (int e = 0; e < 16; ++e) {
                     const int m = m0 + c + e;
-                    const float sx = p.xs_per_token ? (m < p.M ? __ldg(p.x_scale + m) : 0.0f) : sx0;
+                    const float sx = p.xs_per_token ? (m < p.M ? ld_input(p.x_scale + m) : 0.0f) : sx0;
                     v[e] = fmaf((float)s16[e], sx * sw, b);
                   }
                   ok = emit16(m0, c, ochan, v);

@@ -48,7 +48,7 @@ __device__ __forceinline__ void store_fetch(StoreItem<E> &it, int64_t t, int h, 
                                             const uint16_t *__restrict__ v, int64_t ldv,
                                             const int64_t *__restrict__ slots, int sub) {
   constexpr int D = 8 * E;
-  it.slot = __ldg(slots + t);
+  it.slot = ld_input(slots + t);
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) it.k[i] = it.v[i] = 0u;
   if (active) {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(32 * kTokensPerBlock, L >= 8 ? 4 : 6) k_kv_loa
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kTokensPerBlock + (threadIdx.x >> 5);
   if (t >= T) return;
-  const int64_t slot = __ldg(slots + t);
+  const int64_t slot = ld_input(slots + t);
   const bool ok = slot >= 0 && slot < num_slots;
   if (slot >= num_slots && lane == 0) set_status(status, QLIN_ERR_INVALID_ARG);
   for (int h0 = 0; h0 < H; h0 += HF) {
@@ -211,10 +211,10 @@ __global__ void __launch_bounds__(32 * kTokensPerBlock, L >= 8 ? 4 : 6) k_kv_loa
       ksh[j] = vsh[j] = 0;
       if (ok && h0 + j < H) {
         const int64_t base = slot * H + h0 + j;
-        kw[j] = __ldg(reinterpret_cast<const C *>(kc + base * D) + lane);
-        vw[j] = __ldg(reinterpret_cast<const C *>(vc + base * D) + lane);
-        ksh[j] = __ldg(ks + base * (D / 32) + lane / GL);
-        vsh[j] = __ldg(vs + base);
+        kw[j] = ld_input(reinterpret_cast<const C *>(kc + base * D) + lane);
+        vw[j] = ld_input(reinterpret_cast<const C *>(vc + base * D) + lane);
+        ksh[j] = ld_input(ks + base * (D / 32) + lane / GL);
+        vsh[j] = ld_input(vs + base);
       }
     }
     // code * scale is exact in fp32 (at most 8 x 11 significant bits), so the

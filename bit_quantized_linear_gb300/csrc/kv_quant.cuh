@@ -12,14 +12,14 @@ namespace qlin {
 template <int N>
 __device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    w[0] = ld_input(reinterpret_cast<const uint32_t *>(p));
   } else if constexpr (N == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint2 v = ld_input(reinterpret_cast<const uint2 *>(p));
     w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+      const uint4 v = ld_input(reinterpret_cast<const uint4 *>(p) + i);
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) k_absmax_bf16(const uint4 *__restrict__ x
   float amax = 0.0f;
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8;
        i += (int64_t)gridDim.x * blockDim.x) {
-    uint4 v = __ldg(x + i);
+    uint4 v = ld_input(x + i);
     uint32_t wds[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -88,7 +88,7 @@ __global__ void k_scale_finalize(const unsigned *__restrict__ amax_bits, float *
                                  float qmax) {
   pdl_wait();
   pdl_trigger();
-  const float a = __uint_as_float(*amax_bits);
+  const float a = __uint_as_float(ld_input(amax_bits));
   *scale = a > 0.0f ? __fdiv_rn(a, qmax) : 1.0f;
 }
 
@@ -103,14 +103,14 @@ __global__ void __launch_bounds__(256) k_quantize_act(const uint4 *__restrict__ 
                                                       uint4 *__restrict__ q, int64_t n16) {
   pdl_wait();
   pdl_trigger();
-  const float sv = __ldg(s_ptr);
+  const float sv = ld_input(s_ptr);
   const Scale s = make_scale(sv);
   if constexpr (QT == QLIN_E4M3) {
     if (s.fast) {
       const StaticE4m3 se = make_static_e4m3(sv);
       for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n16;
            i += (int64_t)gridDim.x * blockDim.x) {
-        const uint4 a = __ldg(x + 2 * i), b = __ldg(x + 2 * i + 1);
+        const uint4 a = ld_input(x + 2 * i), b = ld_input(x + 2 * i + 1);
         q[i] = make_uint4(e4m3_static4_fast(a.x, a.y, se), e4m3_static4_fast(a.z, a.w, se),
                           e4m3_static4_fast(b.x, b.y, se), e4m3_static4_fast(b.z, b.w, se));
       }
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) k_quantize_act(const uint4 *__restrict__ 
   }
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n16;
        i += (int64_t)gridDim.x * blockDim.x) {
-    uint4 a = __ldg(x + 2 * i), b = __ldg(x + 2 * i + 1);
+    uint4 a = ld_input(x + 2 * i), b = ld_input(x + 2 * i + 1);
     uint32_t in[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t out[4];
 #pragma unroll
@@ -143,9 +143,9 @@ __global__ void __launch_bounds__(256) k_quantize_act_i8bf16(const uint4 *__rest
                                                             uint4 *__restrict__ q, int64_t n8) {
   pdl_wait();
   pdl_trigger();
-  const Scale s = make_scale(__ldg(s_ptr));
+  const Scale s = make_scale(ld_input(s_ptr));
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n8; i += (int64_t)gridDim.x * blockDim.x) {
-    const uint4 a = __ldg(x + i);
+    const uint4 a = ld_input(x + i);
     uint32_t in[4] = {a.x, a.y, a.z, a.w}, out[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256) k_i8_to_bf16(const uint4 *__restrict__ q,
   pdl_wait();
   pdl_trigger();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n16; i += (int64_t)gridDim.x * blockDim.x) {
-    const uint4 a = __ldg(q + i);
+    const uint4 a = ld_input(q + i);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
     uint32_t o[8];
 #pragma unroll
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256) k_quantize_act_dyn(const uint16_t *__rest
   const int64_t K8 = K / 8;
   float amax = 0.0f;
   for (int64_t i = threadIdx.x; i < K8; i += blockDim.x) {
-    const uint4 v = __ldg(row + i);
+    const uint4 v = ld_input(row + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256) k_quantize_act_dyn(const uint16_t *__rest
   if (threadIdx.x == 0) s_out[m] = sc;
   const Scale scl = make_scale(sc);
   for (int64_t i = threadIdx.x; i < K8; i += blockDim.x) {
-    const uint4 v = __ldg(row + i);
+    const uint4 v = ld_input(row + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if constexpr (OUT_BF16) {
       uint32_t o[4];

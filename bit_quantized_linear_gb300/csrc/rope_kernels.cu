@@ -116,7 +116,7 @@ __device__ __forceinline__ void rotate_heads(const RopeParams &p, int64_t u, int
     h1 = min(h0 + p.slice, h1);
   }
   if (t >= p.T) return;
-  const int64_t pos = __ldg(p.positions + t);
+  const int64_t pos = ld_input(p.positions + t);
   const bool turns = item * 16 < p.rot;
   const int half = p.rot / 2;
   // the two 8-dimension pieces of the lane
@@ -142,10 +142,10 @@ __device__ __forceinline__ void rotate_heads(const RopeParams &p, int64_t u, int
       const float *row = table_row(p, pos, status);
       if (!row) return;
       if (turns) {
-        *reinterpret_cast<float4 *>(c) = __ldg(reinterpret_cast<const float4 *>(row + item * 8));
-        *reinterpret_cast<float4 *>(c + 4) = __ldg(reinterpret_cast<const float4 *>(row + item * 8) + 1);
-        *reinterpret_cast<float4 *>(s) = __ldg(reinterpret_cast<const float4 *>(row + half + item * 8));
-        *reinterpret_cast<float4 *>(s + 4) = __ldg(reinterpret_cast<const float4 *>(row + half + item * 8) + 1);
+        *reinterpret_cast<float4 *>(c) = ld_input(reinterpret_cast<const float4 *>(row + item * 8));
+        *reinterpret_cast<float4 *>(c + 4) = ld_input(reinterpret_cast<const float4 *>(row + item * 8) + 1);
+        *reinterpret_cast<float4 *>(s) = ld_input(reinterpret_cast<const float4 *>(row + half + item * 8));
+        *reinterpret_cast<float4 *>(s + 4) = ld_input(reinterpret_cast<const float4 *>(row + half + item * 8) + 1);
       }
       ready = true;
     }
@@ -197,14 +197,14 @@ struct Piece {
     if (half_layout) {
 #pragma unroll
       for (int j = 0; j < N; j += 4) {
-        *reinterpret_cast<float4 *>(c + j) = __ldg(reinterpret_cast<const float4 *>(from + j));
-        *reinterpret_cast<float4 *>(s + j) = __ldg(reinterpret_cast<const float4 *>(from + half + j));
+        *reinterpret_cast<float4 *>(c + j) = ld_input(reinterpret_cast<const float4 *>(from + j));
+        *reinterpret_cast<float4 *>(s + j) = ld_input(reinterpret_cast<const float4 *>(from + half + j));
       }
     } else {
 #pragma unroll
       for (int j = 0; j < N / 2; j += 2) {
-        *reinterpret_cast<float2 *>(c + j) = __ldg(reinterpret_cast<const float2 *>(from + j));
-        *reinterpret_cast<float2 *>(s + j) = __ldg(reinterpret_cast<const float2 *>(from + half + j));
+        *reinterpret_cast<float2 *>(c + j) = ld_input(reinterpret_cast<const float2 *>(from + j));
+        *reinterpret_cast<float2 *>(s + j) = ld_input(reinterpret_cast<const float2 *>(from + half + j));
       }
     }
   }
@@ -259,8 +259,8 @@ struct StorePair {
     h = (int)(pair - t * s.H);
     pos = slot = -1;
     if (t >= p.T) return;
-    pos = __ldg(p.positions + t);
-    slot = __ldg(s.slots + t);
+    pos = ld_input(p.positions + t);
+    slot = ld_input(s.slots + t);
     const uint16_t *kh = p.k + t * p.ldk + (int64_t)h * D;
 #pragma unroll
     for (int i = 0; i < E / N; ++i) k[i].load(kh, sub * E + i * N, p.rot, p.half_layout);

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_w8a16_split(const uint16_t *_
 #pragma unroll
   for (int i = 0; i < kSplitMaxPer; ++i) {  // all of this thread's loads in flight at once
     const int u = u0 + (int)threadIdx.x + i * kSplitThreads;
-    v[i] = u < u1 ? __ldg(row + u) : make_uint4(0, 0, 0, 0);
+    v[i] = u < u1 ? ld_input(row + u) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < kSplitMaxPer; ++i) a = fmaxf(a, absmax8(v[i]));
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(W8F8Cfg<TMAX>::THREADS, 1)
     bool ok = true;
     pdl_wait();  // the split's scales are complete from here on
     const int m0 = tj * tt, e = threadIdx.x - 64;
-    if (e < tt) xsc[e] = m0 + e < p.M ? __ldg(p.x_scale + m0 + e) : 0.0f;
+    if (e < tt) xsc[e] = m0 + e < p.M ? ld_input(p.x_scale + m0 + e) : 0.0f;
     bar_sync_named(1, 128);  // the four epilogue warps
     ok = ok && mbar_wait(acc_full, 0, abort_flag);
     tc_fence_after();
