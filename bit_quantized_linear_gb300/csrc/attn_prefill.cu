@@ -103,6 +103,11 @@ __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// Values of a tcgen05.ld: not used before this point (which follows its wait).
+__device__ __forceinline__ void tie(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ float f32x2_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
@@ -462,44 +467,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
         // a score's factor (never 0, so that -inf stays -inf)
         const auto factor = [&](int ek) { return fmaxf(row_factor * pow2i(ek), 0x1p-100f); };
 
-        // S into registers and the row's largest exponent
+        // The row's largest exponent.  P of the first half of the scores goes over them, so
+        // they stay in registers; those of the second half (columns that P leaves alone)
+        // are read again: 128 registers of scores spill (1173 us against 1162).
         uint32_t s[4][32];
         float f[4];
         int ev[4];
         unsigned wide[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          tmem_ld32(s_at + c * 32, s[c]);
           f[c] = factor(tm.ek[c]);
           ev[c] = tm.ev[c];
           wide[c] = ANY ? tm.wide[c] : 0;
         }
-        tmem_ld_wait();
-        if (__builtin_expect(!full, 0)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mask(c, s[c]);
-        }
         float now = m, nothing = -INFINITY;  // nothing: the largest score of a position without a value
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        const auto maximum = [&](int c, const uint32_t (&s)[32]) {
           float mx = -INFINITY;
           if (!ANY || wide[c] == 0) {
             float t[4];  // four chains
 #pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[c][i]);
+            for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[i]);
 #pragma unroll
-            for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[c][i]));
+            for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[i]));
             mx = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float x = __uint_as_float(s[c][i]) * f[c], e = tm.pos_ev[c * 32 + i];
+              const float x = __uint_as_float(s[i]) * f[c], e = tm.pos_ev[c * 32 + i];
               mx = fmaxf(mx, x + e);
               if (e == -INFINITY) nothing = fmaxf(nothing, x);
             }
           }
           now = fmaxf(now, mx);
-        }
+        };
+        const auto arrived = [&](int c) {
+          tmem_ld_wait();
+          tie(s[c]);
+          if (__builtin_expect(!full, 0)) mask(c, s[c]);
+        };
+        tmem_ld32(s_at + 2 * 32, s[2]);
+        arrived(2);
+        tmem_ld32(s_at + 3 * 32, s[3]);
+        maximum(2, s[2]);
+        arrived(3);
+        tmem_ld32(s_at, s[0]);
+        maximum(3, s[3]);
+        arrived(0);
+        tmem_ld32(s_at + 32, s[1]);
+        maximum(0, s[0]);
+        arrived(1);
+        maximum(1, s[1]);
         if (__any_sync(~0u, now > m + kGrowth || (ANY && nothing > m_l + kLead))) {
           // a new reference: what was summed under the old one is scaled down
           const bool grew = now > m + kGrowth;
@@ -563,16 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
             l += sum;
             tmem_st16(s_at + k * 16, o);
           };
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            probabilities(c, s[c], f[c], ev[c], wide[c]);
-            if (c == 1) {  // the first half of P: its products start
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.p_half[half]);
-            }
-          }
+          tmem_ld32(s_at + 2 * 32, s[2]);
+          probabilities(0, s[0], f[0], ev[0], wide[0]);
+          probabilities(1, s[1], f[1], ev[1], wide[1]);
+          arrived(2);
+          tmem_ld32(s_at + 3 * 32, s[3]);
+          tmem_st_wait();  // the first half of P: its products start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_half[half]);
+          probabilities(2, s[2], f[2], ev[2], wide[2]);
+          arrived(3);
+          probabilities(3, s[3], f[3], ev[3], wide[3]);
         }
         tmem_st_wait();
         tc_fence_before();

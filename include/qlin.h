@@ -462,7 +462,7 @@ qlin_status qlin_rope_kv_store_mixed(qlin_rope_layout layout, int64_t T, int64_t
  *   ws: qlin_attn_mixed_workspace_bytes(B, Hq, H, D, max_q, max_kv, window)
  *   bytes: partial results where the positions are split over CTAs, and for many
  *   rows the positions as float16 (4 D + 5 bytes for each position of max_kv, kv
- *   head and sequence; at most about 2 GB, the kv heads go in groups beyond that).
+ *   head and sequence; beyond about 2 GB the kv heads go in groups, of one at least).
  *   max_q and max_kv bound the launch: tight ones cost less memory and time.
  * Requirements: B >= 0, D 32, 64, 128 or 256, Hq a multiple of H, Hq / H <= 128,
  * block_size >= 1, num_slots a multiple of block_size, window >= 0, scale finite,

@@ -284,3 +284,34 @@ def test_strides_capture_and_repetition(capi):
             side.synchronize()
             assert torch.equal(out, first)
     assert (out[:, n:] == 7).all() and capi.qlin_get_device_status() == capi.QLIN_OK
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_offsets_beyond_32_bits(capi, D):
+    """Pages whose codes lie beyond 2^32 bytes of the cache."""
+    H, block = 4, 256
+    blocks = 2 ** 32 // (H * D * block) + 8
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 10 GB")
+    a = ref.Attn([200, 90], [700, 500], H, 7, D, block, seed=D + 5, extra_blocks=0)
+    _many(capi, a)
+    big = [torch.empty((blocks * block,) + tuple(t.shape[1:]), dtype=t.dtype, device="cuda") for t in a.cache()]
+    far = torch.randperm(8, generator=torch.Generator().manual_seed(2)) + blocks - 8
+    far[::2] -= blocks // 2  # some below, some beyond
+    for t, x in zip(big, a.cache()):
+        for i in range(a.blocks):
+            t[far[i] * block: (far[i] + 1) * block] = x[i * block: (i + 1) * block].cuda()
+    table = torch.where(a.table >= 0, far[a.table.clamp(min=0).long()].int(), a.table)
+    out = capi.attn_mixed(a.q.cuda(), a.q_start.cuda(), a.kv_len.cuda(), table.cuda(), block, big, 200, 700)
+    assert capi.qlin_get_device_status() == capi.QLIN_OK
+    _check(out.float().cpu().double(), a)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_same_bits_twice(capi, D):
+    """Split positions and their join included: no order of sums depends on the run."""
+    a = ref.Attn([100, 40], [6000, 800], 2, 7, D, 64, seed=D)
+    _many(capi, a)
+    first = _run(capi, a)
+    for _ in range(3):
+        assert torch.equal(_run(capi, a), first)
