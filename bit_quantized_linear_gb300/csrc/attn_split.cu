@@ -282,294 +282,299 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(there, top);
   };
 
-  // the first tiles are on their way while q arrives
-  for (int n = 0; n < kStages - 1; ++n) {
-    issue(n);
-    if (n < kStages - 2) put_scales(n);
-  }
-
-  // q: row 8*nt + g, as the second operand; its largest magnitude becomes 2^14..2^15
-  uint32_t qf[NT][kGroups][4];
-  float qoff[NT][kGroups][2];    // -1152 times the sums of columns 2t and 2t + 1 over a key group
-  float cf[NT][2];               // score factors of columns 2t and 2t + 1
-  int vlo[NT][2], vhi[NT][2];    // positions those columns see
-  int all_lo = lo, all_hi = hi;  // positions every row sees
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      const uint32_t u[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+  // warps without a tile (few positions) go to the join, which leaves them out: 149 x 8 kv
+  // heads over 2 positions 15.2 us, 17.1 with all warps prepared, written and joined
+  if (mine > 0) {
+    // the first tiles are on their way while q arrives
+    for (int n = 0; n < kStages - 1; ++n) {
+      issue(n);
+      if (n < kStages - 2) put_scales(n);
     }
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-    const int e = q_exponent(top);
-    const float up = pow2i(14 - e), factor = p.scale_log2 * pow2i(max(e - 14, -126));
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-      const uint32_t u[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        qf[nt][k][j] = half2_of(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = __half22float2(bits_half2(qf[nt][k][j]));
-        sum += x.x + x.y;
-      }
-      sum += __shfl_xor_sync(~0u, sum, 1);
-      sum += __shfl_xor_sync(~0u, sum, 2);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) qoff[nt][k][c] = -1152.0f * __shfl_sync(~0u, sum, (2 * t + c) * 4);
-    }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      cf[nt][c] = __shfl_sync(~0u, factor, (2 * t + c) * 4);
-      const int i = nt * 8 + 2 * t + c;
-      vlo[nt][c] = lo, vhi[nt][c] = hi;  // columns without a row see everything (their q is 0)
-      if (r0 + i < R) sees(p, sq, token_of(i), vlo[nt][c], vhi[nt][c]);
-      all_lo = max(all_lo, vlo[nt][c]);
-      all_hi = min(all_hi, vhi[nt][c]);
-    }
-  }
-  all_lo = __reduce_max_sync(~0u, all_lo);
-  all_hi = __reduce_min_sync(~0u, all_hi);
 
-  float m[NT][2], l[NT][2], O[NT][kDims / 2][4];
+    // q: row 8*nt + g, as the second operand; its largest magnitude becomes 2^14..2^15
+    uint32_t qf[NT][kGroups][4];
+    float qoff[NT][kGroups][2];    // -1152 times the sums of columns 2t and 2t + 1 over a key group
+    float cf[NT][2];               // score factors of columns 2t and 2t + 1
+    int vlo[NT][2], vhi[NT][2];    // positions those columns see
+    int all_lo = lo, all_hi = hi;  // positions every row sees
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kDims / 2; ++i) O[nt][i][0] = O[nt][i][1] = O[nt][i][2] = O[nt][i][3] = 0.0f;
-  }
-  int vexp = -1000;  // O is sum p v 2^-vexp
-
-  for (int n = 0; n < mine; ++n) {
-    cp_async_wait<kStages - 2>();
-    put_scales(n + kStages - 2);
-    __syncwarp();
-    issue(n + kStages - 1);
-    const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
-    uint8_t *stage = ring + (n % kStages) * Geo::kStageBytes;
-    const uint2 info = *reinterpret_cast<const uint2 *>(stage + Geo::kInfoAt);
-    const int j0 = first_of(n);
-    const bool full = info.x == (~0u >> (32 - kTile)) && j0 >= all_lo && j0 + kTile <= all_hi;
-    float vs[kHalves][2];  // of positions g and g + 8 of each half
-
-    // scores of those positions and columns 2t, 2t + 1
-    float S[kHalves][NT][4];
-#pragma unroll
-    for (int f = 0; f < kHalves; ++f) {
-      const int r0 = 16 * f + g, r1 = r0 + 8;
-      vs[f][0] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r0];
-      vs[f][1] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r1];
-      float ks[2][kGroups];
-      load_shared<kGroups>(ks[0], reinterpret_cast<const float *>(stage + Geo::kScaleAt) + r0 * kGroups);
-      load_shared<kGroups>(ks[1], reinterpret_cast<const float *>(stage + Geo::kScaleAt) + r1 * kGroups);
+    for (int nt = 0; nt < NT; ++nt) {
+      float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
-        uint32_t w0[2], w1[2];
-        const uint32_t a0 = at + r0 * D + key_chunk<D>(r0, 2 * k) * 16 + t * 8;
-        const uint32_t a1 = at + r1 * D + key_chunk<D>(r1, 2 * k) * 16 + t * 8;
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(a0));
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(a1));
-        float acc[NT][4];
+        const uint32_t u[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t a[4];
-          int8x4_to_offset_half(w0[j], a[0], a[2]);
-          int8x4_to_offset_half(w1[j], a[1], a[3]);
+        for (int j = 0; j < 4; ++j)
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      const int e = q_exponent(top);
+      const float up = pow2i(14 - e), factor = p.scale_log2 * pow2i(max(e - 14, -126));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (j == 0) mma_f16_from(acc[nt], a, qf[nt][k][0], qf[nt][k][1], qoff[nt][k][0], qoff[nt][k][1]);
-            else mma_f16(acc[nt], a, qf[nt][k][2], qf[nt][k][3]);
-          }
+      for (int k = 0; k < kGroups; ++k) {
+        const uint32_t u[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          qf[nt][k][j] = half2_of(__uint_as_float(u[j] << 16) * up, __uint_as_float(u[j] & 0xFFFF0000u) * up);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = __half22float2(bits_half2(qf[nt][k][j]));
+          sum += x.x + x.y;
         }
-        const float k0 = ks[0][k], k1 = ks[1][k];
+        sum += __shfl_xor_sync(~0u, sum, 1);
+        sum += __shfl_xor_sync(~0u, sum, 2);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          S[f][nt][0] = k ? fmaf(acc[nt][0], k0, S[f][nt][0]) : acc[nt][0] * k0;
-          S[f][nt][1] = k ? fmaf(acc[nt][1], k0, S[f][nt][1]) : acc[nt][1] * k0;
-          S[f][nt][2] = k ? fmaf(acc[nt][2], k1, S[f][nt][2]) : acc[nt][2] * k1;
-          S[f][nt][3] = k ? fmaf(acc[nt][3], k1, S[f][nt][3]) : acc[nt][3] * k1;
-        }
+        for (int c = 0; c < 2; ++c) qoff[nt][k][c] = -1152.0f * __shfl_sync(~0u, sum, (2 * t + c) * 4);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        S[f][nt][0] *= cf[nt][0], S[f][nt][2] *= cf[nt][0];
-        S[f][nt][1] *= cf[nt][1], S[f][nt][3] *= cf[nt][1];
+      for (int c = 0; c < 2; ++c) {
+        cf[nt][c] = __shfl_sync(~0u, factor, (2 * t + c) * 4);
+        const int i = nt * 8 + 2 * t + c;
+        vlo[nt][c] = lo, vhi[nt][c] = hi;  // columns without a row see everything (their q is 0)
+        if (r0 + i < R) sees(p, sq, token_of(i), vlo[nt][c], vhi[nt][c]);
+        all_lo = max(all_lo, vlo[nt][c]);
+        all_hi = min(all_hi, vhi[nt][c]);
       }
     }
-    if (!full) {
-      // A NaN value code times P = 0 would reach rows that do not see it: such
-      // codes become 0 and their position's scale NaN.  (Two lanes to a row.)
+    all_lo = __reduce_max_sync(~0u, all_lo);
+    all_hi = __reduce_min_sync(~0u, all_hi);
+
+    float m[NT][2], l[NT][2], O[NT][kDims / 2][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kDims / 2; ++i) O[nt][i][0] = O[nt][i][1] = O[nt][i][2] = O[nt][i][3] = 0.0f;
+    }
+    int vexp = -1000;  // O is sum p v 2^-vexp
+
+    for (int n = 0; n < mine; ++n) {
+      cp_async_wait<kStages - 2>();
+      put_scales(n + kStages - 2);
+      __syncwarp();
+      issue(n + kStages - 1);
+      const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
+      uint8_t *stage = ring + (n % kStages) * Geo::kStageBytes;
+      const uint2 info = *reinterpret_cast<const uint2 *>(stage + Geo::kInfoAt);
+      const int j0 = first_of(n);
+      const bool full = info.x == (~0u >> (32 - kTile)) && j0 >= all_lo && j0 + kTile <= all_hi;
+      float vs[kHalves][2];  // of positions g and g + 8 of each half
+
+      // scores of those positions and columns 2t, 2t + 1
+      float S[kHalves][NT][4];
 #pragma unroll
       for (int f = 0; f < kHalves; ++f) {
         const int r0 = 16 * f + g, r1 = r0 + 8;
-        const bool ok0 = (info.x >> r0) & 1, ok1 = (info.x >> r1) & 1;
-        const int p0 = j0 + r0, p1 = p0 + 8;
+        vs[f][0] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r0];
+        vs[f][1] = reinterpret_cast<const float *>(stage + Geo::kVScaleAt)[r1];
+        float ks[2][kGroups];
+        load_shared<kGroups>(ks[0], reinterpret_cast<const float *>(stage + Geo::kScaleAt) + r0 * kGroups);
+        load_shared<kGroups>(ks[1], reinterpret_cast<const float *>(stage + Geo::kScaleAt) + r1 * kGroups);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          uint32_t w0[2], w1[2];
+          const uint32_t a0 = at + r0 * D + key_chunk<D>(r0, 2 * k) * 16 + t * 8;
+          const uint32_t a1 = at + r1 * D + key_chunk<D>(r1, 2 * k) * 16 + t * 8;
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(a0));
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(a1));
+          float acc[NT][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t a[4];
+            int8x4_to_offset_half(w0[j], a[0], a[2]);
+            int8x4_to_offset_half(w1[j], a[1], a[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (j == 0) mma_f16_from(acc[nt], a, qf[nt][k][0], qf[nt][k][1], qoff[nt][k][0], qoff[nt][k][1]);
+              else mma_f16(acc[nt], a, qf[nt][k][2], qf[nt][k][3]);
+            }
+          }
+          const float k0 = ks[0][k], k1 = ks[1][k];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            S[f][nt][0] = k ? fmaf(acc[nt][0], k0, S[f][nt][0]) : acc[nt][0] * k0;
+            S[f][nt][1] = k ? fmaf(acc[nt][1], k0, S[f][nt][1]) : acc[nt][1] * k0;
+            S[f][nt][2] = k ? fmaf(acc[nt][2], k1, S[f][nt][2]) : acc[nt][2] * k1;
+            S[f][nt][3] = k ? fmaf(acc[nt][3], k1, S[f][nt][3]) : acc[nt][3] * k1;
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          S[f][nt][0] *= cf[nt][0], S[f][nt][2] *= cf[nt][0];
+          S[f][nt][1] *= cf[nt][1], S[f][nt][3] *= cf[nt][1];
+        }
+      }
+      if (!full) {
+        // A NaN value code times P = 0 would reach rows that do not see it: such
+        // codes become 0 and their position's scale NaN.  (Two lanes to a row.)
+#pragma unroll
+        for (int f = 0; f < kHalves; ++f) {
+          const int r0 = 16 * f + g, r1 = r0 + 8;
+          const bool ok0 = (info.x >> r0) & 1, ok1 = (info.x >> r1) & 1;
+          const int p0 = j0 + r0, p1 = p0 + 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (!ok0 || p0 < vlo[nt][c] || p0 >= vhi[nt][c]) S[f][nt][c] = -INFINITY;
+              if (!ok1 || p1 < vlo[nt][c] || p1 >= vhi[nt][c]) S[f][nt][2 + c] = -INFINITY;
+            }
+          unsigned bad = 0;
+          uint32_t *w = reinterpret_cast<uint32_t *>(stage + Geo::kCodes + (16 * f + (lane >> 1)) * D + (lane & 1) * (D / 2));
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t nan = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (nan) w[i] &= ~nan;
+            bad |= nan;
+          }
+          const unsigned rows = __ballot_sync(~0u, bad != 0);
+          if ((rows >> (2 * g)) & 3) vs[f][0] = NAN;
+          if ((rows >> (2 * g + 16)) & 3) vs[f][1] = NAN;
+        }
+        __syncwarp();
+      }
+
+      // value scales relative to 2^vexp; the exponent grows when P would pass 2^15
+      int e = (int)(info.y >> 23) - 127;
+      e = min(max(e, -24), 16);
+      if (e - vexp > 13) {
+        const float down = exp2_approx((float)(vexp - (e - 7)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (!ok0 || p0 < vlo[nt][c] || p0 >= vhi[nt][c]) S[f][nt][c] = -INFINITY;
-            if (!ok1 || p1 < vlo[nt][c] || p1 >= vhi[nt][c]) S[f][nt][2 + c] = -INFINITY;
-          }
-        unsigned bad = 0;
-        uint32_t *w = reinterpret_cast<uint32_t *>(stage + Geo::kCodes + (16 * f + (lane >> 1)) * D + (lane & 1) * (D / 2));
+          for (int i = 0; i < kDims / 2; ++i)
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t nan = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          if (nan) w[i] &= ~nan;
-          bad |= nan;
-        }
-        const unsigned rows = __ballot_sync(~0u, bad != 0);
-        if ((rows >> (2 * g)) & 3) vs[f][0] = NAN;
-        if ((rows >> (2 * g + 16)) & 3) vs[f][1] = NAN;
+            for (int c = 0; c < 4; ++c) O[nt][i][c] *= down;
+        vexp = e - 7;
       }
-      __syncwarp();
-    }
-
-    // value scales relative to 2^vexp; the exponent grows when P would pass 2^15
-    int e = (int)(info.y >> 23) - 127;
-    e = min(max(e, -24), 16);
-    if (e - vexp > 13) {
-      const float down = exp2_approx((float)(vexp - (e - 7)));
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < kDims / 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) O[nt][i][c] *= down;
-      vexp = e - 7;
-    }
-#pragma unroll
-    for (int f = 0; f < kHalves; ++f) {
-      vs[f][0] *= pow2i(-vexp);
-      vs[f][1] *= pow2i(-vexp);
-    }
-
-    // online softmax per column
-    uint32_t pf[kHalves][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float mx[2] = {fmaxf(S[0][nt][0], S[0][nt][2]), fmaxf(S[0][nt][1], S[0][nt][3])};
-      if constexpr (kHalves == 2) {
-        mx[0] = fmaxf(mx[0], fmaxf(S[kHalves - 1][nt][0], S[kHalves - 1][nt][2]));
-        mx[1] = fmaxf(mx[1], fmaxf(S[kHalves - 1][nt][1], S[kHalves - 1][nt][3]));
-      }
-#pragma unroll
-      for (int o = 4; o < 32; o *= 2) {
-        mx[0] = fmaxf(mx[0], __shfl_xor_sync(~0u, mx[0], o));
-        mx[1] = fmaxf(mx[1], __shfl_xor_sync(~0u, mx[1], o));
-      }
-      const bool grew = mx[0] > m[nt][0] || mx[1] > m[nt][1];
-      if (__any_sync(~0u, grew)) {
-        float a[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float now = fmaxf(m[nt][c], mx[c]);
-          a[c] = exp2_approx(m[nt][c] - (now == -INFINITY ? 0.0f : now));
-          m[nt][c] = now;
-          l[nt][c] *= a[c];
-        }
-#pragma unroll
-        for (int i = 0; i < kDims / 2; ++i) {
-          O[nt][i][0] *= a[0], O[nt][i][2] *= a[0];
-          O[nt][i][1] *= a[1], O[nt][i][3] *= a[1];
-        }
-      }
-      const float z0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], z1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
 #pragma unroll
       for (int f = 0; f < kHalves; ++f) {
-        const float(&s)[4] = S[f][nt];
-        const float p00 = exp2_approx(s[0] - z0), p01 = exp2_approx(s[1] - z1);
-        const float p10 = exp2_approx(s[2] - z0), p11 = exp2_approx(s[3] - z1);
-        l[nt][0] += p00 + p10;
-        l[nt][1] += p01 + p11;
-        float w00 = p00 * vs[f][0], w01 = p01 * vs[f][0], w10 = p10 * vs[f][1], w11 = p11 * vs[f][1];
-        if (!full) {  // an unseen position adds nothing, whatever its scale
-          if (s[0] == -INFINITY) w00 = 0.0f;
-          if (s[1] == -INFINITY) w01 = 0.0f;
-          if (s[2] == -INFINITY) w10 = 0.0f;
-          if (s[3] == -INFINITY) w11 = 0.0f;
-        }
-        pf[f][nt][0] = transpose8x8(half2_of(w00, w01));
-        pf[f][nt][1] = transpose8x8(half2_of(w10, w11));
+        vs[f][0] *= pow2i(-vexp);
+        vs[f][1] *= pow2i(-vexp);
       }
-    }
 
-    // O^T += V^T P^T: positions 2t, 2t+1 (and +8) of each half, dimensions g*D/8 ...
-    constexpr int kW = kDims / 4;  // words of a lane's piece of a value row
+      // online softmax per column
+      uint32_t pf[kHalves][NT][2];
 #pragma unroll
-    for (int f = 0; f < kHalves; ++f) {
-      uint32_t v[4][kW];
+      for (int nt = 0; nt < NT; ++nt) {
+        float mx[2] = {fmaxf(S[0][nt][0], S[0][nt][2]), fmaxf(S[0][nt][1], S[0][nt][3])};
+        if constexpr (kHalves == 2) {
+          mx[0] = fmaxf(mx[0], fmaxf(S[kHalves - 1][nt][0], S[kHalves - 1][nt][2]));
+          mx[1] = fmaxf(mx[1], fmaxf(S[kHalves - 1][nt][1], S[kHalves - 1][nt][3]));
+        }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 16 * f + 2 * t + (i & 1) + 8 * (i >> 1);
-        const uint8_t *row = stage + Geo::kCodes + r * D;
-        if constexpr (kDims >= 16) {
+        for (int o = 4; o < 32; o *= 2) {
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(~0u, mx[0], o));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(~0u, mx[1], o));
+        }
+        const bool grew = mx[0] > m[nt][0] || mx[1] > m[nt][1];
+        if (__any_sync(~0u, grew)) {
+          float a[2];
 #pragma unroll
-          for (int c = 0; c < kDims / 16; ++c) {
-            const uint4 x =
-                *reinterpret_cast<const uint4 *>(row + value_chunk<D>(r, g * (kDims / 16) + c) * 16);
-            v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
+          for (int c = 0; c < 2; ++c) {
+            const float now = fmaxf(m[nt][c], mx[c]);
+            a[c] = exp2_approx(m[nt][c] - (now == -INFINITY ? 0.0f : now));
+            m[nt][c] = now;
+            l[nt][c] *= a[c];
           }
-        } else if constexpr (kDims == 8) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(row + value_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
-          v[i][0] = x.x, v[i][1] = x.y;
-        } else {
-          v[i][0] = *reinterpret_cast<const uint32_t *>(row + g * 4);
+#pragma unroll
+          for (int i = 0; i < kDims / 2; ++i) {
+            O[nt][i][0] *= a[0], O[nt][i][2] *= a[0];
+            O[nt][i][1] *= a[1], O[nt][i][3] *= a[1];
+          }
+        }
+        const float z0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], z1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+#pragma unroll
+        for (int f = 0; f < kHalves; ++f) {
+          const float(&s)[4] = S[f][nt];
+          const float p00 = exp2_approx(s[0] - z0), p01 = exp2_approx(s[1] - z1);
+          const float p10 = exp2_approx(s[2] - z0), p11 = exp2_approx(s[3] - z1);
+          l[nt][0] += p00 + p10;
+          l[nt][1] += p01 + p11;
+          float w00 = p00 * vs[f][0], w01 = p01 * vs[f][0], w10 = p10 * vs[f][1], w11 = p11 * vs[f][1];
+          if (!full) {  // an unseen position adds nothing, whatever its scale
+            if (s[0] == -INFINITY) w00 = 0.0f;
+            if (s[1] == -INFINITY) w01 = 0.0f;
+            if (s[2] == -INFINITY) w10 = 0.0f;
+            if (s[3] == -INFINITY) w11 = 0.0f;
+          }
+          pf[f][nt][0] = transpose8x8(half2_of(w00, w01));
+          pf[f][nt][1] = transpose8x8(half2_of(w10, w11));
         }
       }
-#pragma unroll
-      for (int i = 0; i < kW; ++i) {
-        // (position 2t, 2t+1) byte pairs of dimensions 4i, 4i+1 | 4i+2, 4i+3
-        const uint32_t x0 = __byte_perm(v[0][i], v[1][i], 0x5140), x1 = __byte_perm(v[0][i], v[1][i], 0x7362);
-        const uint32_t y0 = __byte_perm(v[2][i], v[3][i], 0x5140), y1 = __byte_perm(v[2][i], v[3][i], 0x7362);
-        const uint32_t a0[4] = {e4m3x2_to_half((uint16_t)x0), e4m3x2_to_half((uint16_t)(x0 >> 16)),
-                                e4m3x2_to_half((uint16_t)y0), e4m3x2_to_half((uint16_t)(y0 >> 16))};
-        const uint32_t a1[4] = {e4m3x2_to_half((uint16_t)x1), e4m3x2_to_half((uint16_t)(x1 >> 16)),
-                                e4m3x2_to_half((uint16_t)y1), e4m3x2_to_half((uint16_t)(y1 >> 16))};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16(O[nt][2 * i], a0, pf[f][nt][0], pf[f][nt][1]);
-          mma_f16(O[nt][2 * i + 1], a1, pf[f][nt][0], pf[f][nt][1]);
-        }
-      }
-    }
-  }
-  cp_async_wait<0>();
 
-  // ---- join the warps
+      // O^T += V^T P^T: positions 2t, 2t+1 (and +8) of each half, dimensions g*D/8 ...
+      constexpr int kW = kDims / 4;  // words of a lane's piece of a value row
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+      for (int f = 0; f < kHalves; ++f) {
+        uint32_t v[4][kW];
 #pragma unroll
-    for (int o = 4; o < 32; o *= 2) {
-      l[nt][0] += __shfl_xor_sync(~0u, l[nt][0], o);
-      l[nt][1] += __shfl_xor_sync(~0u, l[nt][1], o);
-    }
-  __syncwarp();
-  float *res = reinterpret_cast<float *>(ring);
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * f + 2 * t + (i & 1) + 8 * (i >> 1);
+          const uint8_t *row = stage + Geo::kCodes + r * D;
+          if constexpr (kDims >= 16) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+            for (int c = 0; c < kDims / 16; ++c) {
+              const uint4 x =
+                  *reinterpret_cast<const uint4 *>(row + value_chunk<D>(r, g * (kDims / 16) + c) * 16);
+              v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
+            }
+          } else if constexpr (kDims == 8) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(row + value_chunk<D>(r, g >> 1) * 16 + (g & 1) * 8);
+            v[i][0] = x.x, v[i][1] = x.y;
+          } else {
+            v[i][0] = *reinterpret_cast<const uint32_t *>(row + g * 4);
+          }
+        }
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int r = nt * 8 + 2 * t + c;
+        for (int i = 0; i < kW; ++i) {
+          // (position 2t, 2t+1) byte pairs of dimensions 4i, 4i+1 | 4i+2, 4i+3
+          const uint32_t x0 = __byte_perm(v[0][i], v[1][i], 0x5140), x1 = __byte_perm(v[0][i], v[1][i], 0x7362);
+          const uint32_t y0 = __byte_perm(v[2][i], v[3][i], 0x5140), y1 = __byte_perm(v[2][i], v[3][i], 0x7362);
+          const uint32_t a0[4] = {e4m3x2_to_half((uint16_t)x0), e4m3x2_to_half((uint16_t)(x0 >> 16)),
+                                  e4m3x2_to_half((uint16_t)y0), e4m3x2_to_half((uint16_t)(y0 >> 16))};
+          const uint32_t a1[4] = {e4m3x2_to_half((uint16_t)x1), e4m3x2_to_half((uint16_t)(x1 >> 16)),
+                                  e4m3x2_to_half((uint16_t)y1), e4m3x2_to_half((uint16_t)(y1 >> 16))};
 #pragma unroll
-      for (int i = 0; i < kDims / 2; ++i)
-        *reinterpret_cast<float2 *>(res + r * D + g * kDims + 2 * i) = make_float2(O[nt][i][c], O[nt][i][2 + c]);
-      if (g == 0) {
-        res[kRows * D + r] = m[nt][c];
-        res[kRows * D + kRows + r] = l[nt][c];
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(O[nt][2 * i], a0, pf[f][nt][0], pf[f][nt][1]);
+            mma_f16(O[nt][2 * i + 1], a1, pf[f][nt][0], pf[f][nt][1]);
+          }
+        }
       }
     }
-  if (lane == 0) res[kRows * D + 2 * kRows] = mine ? pow2i(vexp) : 0.0f;
+    cp_async_wait<0>();
+
+    // ---- join the warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int o = 4; o < 32; o *= 2) {
+        l[nt][0] += __shfl_xor_sync(~0u, l[nt][0], o);
+        l[nt][1] += __shfl_xor_sync(~0u, l[nt][1], o);
+      }
+    __syncwarp();
+    float *res = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+#pragma unroll
+        for (int i = 0; i < kDims / 2; ++i)
+          *reinterpret_cast<float2 *>(res + r * D + g * kDims + 2 * i) = make_float2(O[nt][i][c], O[nt][i][2 + c]);
+        if (g == 0) {
+          res[kRows * D + r] = m[nt][c];
+          res[kRows * D + kRows + r] = l[nt][c];
+        }
+      }
+    if (lane == 0) res[kRows * D + 2 * kRows] = pow2i(vexp);
+  }
   __syncthreads();
+  const int active = min(tiles, kAttnWarps);
   for (int i = threadIdx.x; i < kRows * D / 4; i += 32 * kAttnWarps) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
     if (r0 + r >= R) break;
@@ -577,12 +582,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     constexpr int kStep = Geo::kWarpBytes / 4;
     float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kAttnWarps; ++k) top = fmaxf(top, w[k * kStep + kRows * D + r]);
+    for (int k = 0; k < kAttnWarps; ++k)
+      if (k < active) top = fmaxf(top, w[k * kStep + kRows * D + r]);
     const float z = top == -INFINITY ? 0.0f : top;
     float L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kAttnWarps; ++k) {
+      if (k >= active) break;
       const float *x = w + k * kStep;
       const float f = exp2_approx(x[kRows * D + r] - z);
       L = fmaf(f, x[kRows * D + kRows + r], L);
@@ -612,7 +619,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
 constexpr int kFewParts = 16;
 constexpr int kManyWarps = 16, kFewWarps = 8;  // warps of a CTA
 template <int D, bool MANY>
-__global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps)) k_attn_join(const AttnDev p, const AttnParts parts, bool many) {
+__global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps))
+    k_attn_join(const AttnDev p, const AttnParts parts, bool many) {
   const int rows = parts.rows;
   constexpr int V = D / 32;                  // floats of a lane
   constexpr int kOver = MANY ? kManyWarps : 1;  // warps that share a row
@@ -712,8 +720,8 @@ cudaError_t launch_nt(const SplitParams &p, int64_t units, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  e = launch_kernel(k_attn_split<D, NT>, dim3((unsigned)(units * p.parts.splits)), dim3(32 * kAttnWarps), Geo::kSmem, st, 1,
-                    p);
+  e = launch_kernel(k_attn_split<D, NT>, dim3((unsigned)(units * p.parts.splits)), dim3(32 * kAttnWarps), Geo::kSmem,
+                    st, 1, p);
   if (e != cudaSuccess || p.parts.splits == 1) return e;
   return launch_attn_join(p, p.parts, D, false, st);
 }
