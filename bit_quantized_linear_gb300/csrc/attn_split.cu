@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
       if (wanted && !ok && lane < kTile) set_status(p.status, QLIN_ERR_INVALID_ARG);
       const int64_t row = ok ? ((int64_t)blk * p.block_size + (j - block_of(p, j) * p.block_size)) * p.H + h : 0;
       there = __ballot_sync(~0u, ok) & (~0u >> (32 - kTile));
-#pragma unroll 1
+#pragma unroll 4
       for (int i = 0; i < Geo::kPieces; ++i) {
         const int r = i * Geo::kRowStep + piece_row;
         const int64_t off = __shfl_sync(~0u, row, r) * D + piece * 16;
