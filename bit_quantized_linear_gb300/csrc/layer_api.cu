@@ -55,21 +55,22 @@ qlin_status check_attn_sizes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_
   return QLIN_OK;
 }
 
-// Which kernel takes which sequences.  The split kernel reads all positions once
-// for every 16 rows, 4e-5 us for each (16 rows, kv head, position) when it fills the
-// GPU; the tcgen05 kernels take 20 us (and with a batch 30, the other kernel being
-// launched as well) whatever they do.  So where a sequence may have more rows than
-// come to that much (of a batch, half of the bound on average), they take those
-// sequences of the batch that have more than kFewRows rows, and the split kernel
-// the others; each leaves the other's sequences.  A lone sequence goes to one kernel
-// by its bound.  Measured, 28 heads over 4, one sequence: 8192 positions, 84 rows
-// 27.7 us split and 25.6 us tcgen05, 336 rows 55 and 36; 1024 positions, 336 rows
-// 14.8 and 23.3, 1344 rows 39 and 27.  Four sequences: 8192 positions, 84 rows 34.7
-// and 54, 336 rows 79 and 65.
+// Which kernel takes which sequences.  With u = sequences x kv heads x positions a row
+// sees at most, the split kernel reads all of u once for every 16 rows: 8 us and, of a
+// ragged batch, 4.3e-5 us (head size 64: 2.9e-5) for each (16 rows, unit of u).  The tcgen05
+// kernels unpack u once: 22 us and 3e-4 us a unit, whatever the rows.  The limit is where
+// the two meet; a lone sequence has no second kernel to launch, and no raggedness.
+// Beyond it they take those sequences of the batch that have more than kFewRows rows,
+// and the split kernel the others; each leaves the other's sequences.  Measured (split and
+// tcgen05, us), one sequence of 28 heads over 4 of 128: 84 rows over 8192 positions 28.2
+// and 25.5, 168 over 8192 43.3 and 30.6, 420 over 2048 32.9 and 23.6.  Batches: 4 x 84 rows
+// over 8192 33.7 and 61.0, 2 x 280 over 4096 46.8 and 33.7, 8 x 196 over 2492 50.2 and 51.4;
+// 8 heads of 128, 4 x 200 over 2048 40.7 and 33.9; of 64, 5 x 333 over 1024 32.8 and 38.5.
 constexpr int64_t kFewRows = 64;
-int64_t attn_most_split_rows(int64_t B, int64_t H, int64_t max_kv, int64_t window) {
+int64_t attn_most_split_rows(int64_t B, int64_t H, int64_t D, int64_t max_kv, int64_t window) {
   const int64_t range = window > 0 ? std::min(window, max_kv) : max_kv;
-  const int64_t rows = (B > 1 ? 20000000 : 6000000) / std::max<int64_t>(1, B * H * range);
+  const int64_t u = std::max<int64_t>(1, B * H * range);
+  const int64_t rows = B == 1 ? 2000000 / u : D == 64 ? 165 + 7700000 / u : 112 + 5200000 / u;
   return std::min<int64_t>(std::max<int64_t>(rows, kFewRows), 512);
 }
 struct AttnRoute {
@@ -82,7 +83,7 @@ struct AttnRoute {
 AttnRoute attn_route(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q, int64_t max_kv, int64_t window) {
   AttnRoute r{};
   const int64_t rows = max_q * (Hq / H);
-  r.many = attn_prefill_has(D) && rows > attn_most_split_rows(B, H, max_kv, window);
+  r.many = attn_prefill_has(D) && rows > attn_most_split_rows(B, H, D, max_kv, window);
   r.few = !r.many || B > 1;
   r.few_rows = r.many ? (r.few ? (int)kFewRows : 0) : (int)rows;
   if (r.many) r.prefill = attn_prefill_plan(B, H, Hq / H, D, max_q, max_kv, window, sm_count());
