@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   const int tile = p.row_tiles - 1 - (int)(unit / heads);
   const int b = (int)(unit % heads) / p.heads, h = p.head0 + (int)(unit % heads) % p.heads;
   pdl_wait();
-  pdl_trigger();
   const Sequence sq = sequence(p, b);
   if (sq.broken && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
   const int R = sq.kept * p.G, r0 = tile * 2 * kRowTile;
@@ -421,6 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // Dependents start only now: a linear's CTA, once resident, takes tensor memory and keeps it
+  // until this kernel has ended, which a CTA still waiting for its columns would never do.
+  pdl_trigger();
 
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------- softmax
