@@ -28,7 +28,7 @@ qlin_status device_ready();
 
 // The current device's cached facts; QLIN_OK or the status to return.
 qlin_status current_device(DeviceInfo **out);
-// Its SM count for choices made without a launch (152, a GB300's, before the first call).
+// Its SM count for choices made before or without a launch (152, a GB300's, without a device).
 int sm_count();
 
 // Small checks shared by the entry points.

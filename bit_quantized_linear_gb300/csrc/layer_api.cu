@@ -86,8 +86,9 @@ AttnRoute attn_route(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t max_q,
   r.many = attn_prefill_has(D) && rows > attn_most_split_rows(B, H, D, max_kv, window);
   r.few = !r.many || B > 1;
   r.few_rows = r.many ? (r.few ? (int)kFewRows : 0) : (int)rows;
-  if (r.many) r.prefill = attn_prefill_plan(B, H, Hq / H, D, max_q, max_kv, window, sm_count());
-  if (r.few) r.split = attn_split_plan(B, Hq, H, D, r.few_rows, max_kv, window, sm_count());
+  const int sms = sm_count();
+  if (r.many) r.prefill = attn_prefill_plan(B, H, Hq / H, D, max_q, max_kv, window, sms);
+  if (r.few) r.split = attn_split_plan(B, Hq, H, D, r.few_rows, max_kv, window, sms);
   return r;
 }
 
@@ -231,14 +232,15 @@ qlin_status qlin_attn_mixed(int64_t B, int64_t T, int64_t Hq, int64_t H, int64_t
                        !al16(k_cache) || !al16(k_scale) || !al16(v_cache) || !al16(v_scale)))
       return QLIN_ERR_INVALID_ARG;
   }
-  const size_t need = work ? qlin_attn_mixed_workspace_bytes(B, Hq, H, D, max_q, max_kv, window) : 0;
+  // one plan, for the check of the workspace and for the launches
+  const AttnRoute r = work ? attn_route(B, Hq, H, D, max_q, max_kv, window) : AttnRoute{};
+  const size_t need = r.ws_bytes();
   if (need && (!ws || !al16(ws) || ws_bytes < need)) return QLIN_ERR_WORKSPACE;
   DeviceInfo *dev;
   if (qlin_status s = current_device(&dev)) return s;
   if (!work) return QLIN_OK;
   AttnArgs a{B,         T,          Hq,        H,       D,       q,       ldq,     q_start, max_q, kv_len, max_kv, block_table,
              max_blocks, block_size, num_slots, k_cache, k_scale, v_cache, v_scale, scale,   causal, window, out,   ldo};
-  const AttnRoute r = attn_route(B, Hq, H, D, max_q, max_kv, window);
   if (r.many && launch_attn_prefill(a, r.prefill, r.few_rows, ws, dev->status, (cudaStream_t)stream) != cudaSuccess)
     return QLIN_ERR_CUDA;
   if (!r.few) return QLIN_OK;

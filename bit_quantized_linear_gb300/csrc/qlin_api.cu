@@ -18,15 +18,17 @@ void note_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_
 static DeviceInfo g_dev[kMaxDevices];
 static std::mutex g_dev_mu;
 
-// SM count of the current device for host-side tile choices that name a
-// kernel without launching it: the cached value, else 152 (GB300).
+// SM count of the current device for choices made before (or without) a launch:
+// the cached value, else the device's own, so that sizes asked for before the first
+// call fit the calls; 152 (a GB300's) where there is no device.
 int sm_count() {
-  int d = -1;
-  if (cudaGetDevice(&d) == cudaSuccess && d >= 0 && d < kMaxDevices) {
+  int d = -1, sms = 0;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0) return 152;
+  if (d < kMaxDevices) {
     std::lock_guard<std::mutex> lk(g_dev_mu);
     if (g_dev[d].device == d && g_dev[d].sms > 0) return g_dev[d].sms;
   }
-  return 152;
+  return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d) == cudaSuccess && sms > 0 ? sms : 152;
 }
 
 // Caches the SM count, compute capability and status-word address of the
