@@ -241,31 +241,74 @@ def qlin_kv_load_mixed(slots, k_cache, k_scale, v_cache, v_scale, k_out, v_out, 
                                    _p(k_out), _p(v_out), _stream(stream)), "qlin_kv_load_mixed")
 
 
-def _row_stride(t, least: int) -> int:
-    """Row stride (elements) of a 2-D tensor whose rows are contiguous, of `least` elements or more (a
-    single row's is whatever its tensor says, so at least that)."""
-    row, one = t.stride()
-    if one != 1:
-        raise ValueError("rows must be contiguous")
-    return row if row >= least or t.shape[0] > 1 else least
+# The C entry points see addresses: what a tensor's type, size or strides would make them misread, the functions
+# below refuse.  (An index array of another type, or a slice of a wider table, is read as other numbers.)
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _dense(t, dtype, size: int, what: str):
+    """t: contiguous, of `size` elements of dtype."""
+    if t.dtype is not dtype or t.numel() != size or not t.is_contiguous():
+        raise ValueError(f"{what}: {size} contiguous elements of {dtype}, not {t.dtype} {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
+
+
+def _bytes(t, size: int, what: str):
+    """t: contiguous, of `size` bytes (codes and scales, whatever type they are held as)."""
+    if t.nbytes != size or not t.is_contiguous():
+        raise ValueError(f"{what}: {size} contiguous bytes, not {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _rows(t, rows: int, least: int, what: str) -> int:
+    """Row stride (elements) of BF16 rows of `least` elements or more."""
+    if t.dtype is _BF16 and t.dim() == 2:
+        (m, n), (row, one) = t.shape, t.stride()
+        if m == rows and n >= least and one == 1:
+            return row if row >= least or m > 1 else least  # a single row's is whatever its tensor says
+    raise ValueError(f"{what}: {rows} BF16 rows of at least {least} contiguous elements, not {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()}")
+
+
+def _mixed_cache(k_cache, k_scale, v_cache, v_scale):
+    """Slots, heads and head size of the four arrays of kv_cache_alloc()."""
+    S, H, D = k_cache.shape
+    n = S * H
+    _bytes(k_cache, n * D, "k_cache")
+    _bytes(k_scale, n * (D // 32) * 2, "k_scale")
+    _bytes(v_cache, n * D, "v_cache")
+    _bytes(v_scale, n * 2, "v_scale")
+    return S, H, D
+
+
+def _norm_inputs(x, residual, weight, h_out):
+    M, K = x.shape
+    _dense(weight, _BF16, K, "weight")
+    if h_out is not None:
+        _dense(h_out, _BF16, M * K, "h_out")
+    return _rows(x, M, K, "x"), 0 if residual is None else _rows(residual, M, K, "residual")
 
 
 def qlin_rmsnorm(x, residual, weight, eps: float, h_out, y_out, stream=None):
     """x, residual (or None) BF16 [M, K] rows; h_out (with a residual) and y_out BF16 [M, K]."""
     M, K = x.shape
-    _check(_lib.qlin_rmsnorm(M, K, _p(x), _row_stride(x, K), _p(residual),
-                             0 if residual is None else _row_stride(residual, K), _p(weight), eps, _p(h_out),
-                             _p(y_out), _stream(stream)), "qlin_rmsnorm")
+    ldx, ldr = _norm_inputs(x, residual, weight, h_out)
+    _dense(y_out, _BF16, M * K, "y_out")
+    _check(_lib.qlin_rmsnorm(M, K, _p(x), ldx, _p(residual), ldr, _p(weight), eps, _p(h_out), _p(y_out),
+                             _stream(stream)), "qlin_rmsnorm")
 
 
 def qlin_rmsnorm_quant(qtype, x, residual, weight, eps: float, input_scale, h_out, qx, x_scale, stream=None):
     """As qlin_rmsnorm with 1-byte codes qx [M, K]: under input_scale [1] (x_scale None), or per-token
     scales written to x_scale [M] (input_scale None)."""
     M, K = x.shape
-    _check(_lib.qlin_rmsnorm_quant(_qt(qtype), M, K, _p(x), _row_stride(x, K), _p(residual),
-                                   0 if residual is None else _row_stride(residual, K), _p(weight), eps,
-                                   _p(input_scale), _p(h_out), _p(qx), _p(x_scale), _stream(stream)),
-           "qlin_rmsnorm_quant")
+    ldx, ldr = _norm_inputs(x, residual, weight, h_out)
+    _bytes(qx, M * K, "qx")
+    if input_scale is not None:
+        _dense(input_scale, _F32, 1, "input_scale")
+    if x_scale is not None:
+        _dense(x_scale, _F32, M, "x_scale")
+    _check(_lib.qlin_rmsnorm_quant(_qt(qtype), M, K, _p(x), ldx, _p(residual), ldr, _p(weight), eps, _p(input_scale),
+                                   _p(h_out), _p(qx), _p(x_scale), _stream(stream)), "qlin_rmsnorm_quant")
 
 
 def qlin_w8a8_linear_codes(qtype, qx, x_scale, qw, w_scale, bias, y, ws=None, stream=None):
@@ -273,8 +316,16 @@ def qlin_w8a8_linear_codes(qtype, qx, x_scale, qw, w_scale, bias, y, ws=None, st
     row's one scale is both)."""
     M, K = qx.shape
     N = qw.shape[0]
+    scales = x_scale.numel()
+    _dense(x_scale, _F32, scales if scales == 1 else M, "x_scale (one value, or one a row)")
+    _bytes(qx, M * K, "qx")
+    _bytes(qw, N * K, "qw")
+    _dense(w_scale, _F32, N, "w_scale")
+    _dense(y, _BF16, M * N, "y")
+    if bias is not None:
+        _dense(bias, _BF16, N, "bias")
     wp, wb = _ws(ws)
-    _check(_lib.qlin_w8a8_linear_codes(_qt(qtype), M, K, N, _p(qx), _p(x_scale), int(x_scale.numel() > 1), _p(qw),
+    _check(_lib.qlin_w8a8_linear_codes(_qt(qtype), M, K, N, _p(qx), _p(x_scale), int(scales > 1), _p(qw),
                                        _p(w_scale), _p(bias), _p(y), wp, wb, _stream(stream)),
            "qlin_w8a8_linear_codes")
 
@@ -283,47 +334,62 @@ def qlin_rope_table(table, theta: float, scaling="plain", factor: float = 1.0, o
                     beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float = 1.0, stream=None):
     """Fills table, fp32 [max_pos, rot]."""
     max_pos, rot = table.shape
+    _dense(table, _F32, max_pos * rot, "table")
     _check(_lib.qlin_rope_table(max_pos, rot, theta, ROPE_SCALINGS[scaling], factor, original_context, beta_fast,
                                 beta_slow, amplitude, _p(table), _stream(stream)), "qlin_rope_table")
 
 
+def _turns(table, rot: int, positions):
+    """Tokens and rows of the table."""
+    max_pos, turned = table.shape
+    if turned != rot:
+        raise ValueError(f"the table turns {turned} dimensions, not {rot}")
+    _dense(table, _F32, max_pos * rot, "table")
+    T = positions.shape[0]
+    _dense(positions, _I64, T, "positions")
+    return T, max_pos
+
+
 def qlin_rope(layout, Hq: int, Hk: int, D: int, rot: int, table, positions, q, k, q_out, k_out, stream=None):
     """q [T, >= Hq*D] and k [T, >= Hk*D] BF16 rows (k and k_out None when Hk is 0); table of qlin_rope_table."""
-    if table.shape[1] != rot:
-        raise ValueError(f"the table turns {table.shape[1]} dimensions, not {rot}")
-    T = positions.shape[0]
+    T, max_pos = _turns(table, rot, positions)
     n, m = Hq * D, Hk * D
-    _check(_lib.qlin_rope(ROPE_LAYOUTS[layout], T, Hq, Hk, D, rot, _p(table), table.shape[0], _p(positions), _p(q),
-                          _row_stride(q, n), _p(k), 0 if k is None else _row_stride(k, m), _p(q_out),
-                          _row_stride(q_out, n), _p(k_out), 0 if k_out is None else _row_stride(k_out, m),
+    _check(_lib.qlin_rope(ROPE_LAYOUTS[layout], T, Hq, Hk, D, rot, _p(table), max_pos, _p(positions), _p(q),
+                          _rows(q, T, n, "q"), _p(k), 0 if k is None else _rows(k, T, m, "k"), _p(q_out),
+                          _rows(q_out, T, n, "q_out"), _p(k_out), 0 if k_out is None else _rows(k_out, T, m, "k_out"),
                           _stream(stream)), "qlin_rope")
 
 
 def qlin_rope_kv_store_mixed(layout, Hq: int, rot: int, table, positions, q, k, v, q_out, slots, k_cache, k_scale,
                              v_cache, v_scale, stream=None):
     """q turned into q_out; k (turned) and v quantized into their slots of the caches of kv_cache_alloc()."""
-    if table.shape[1] != rot:
-        raise ValueError(f"the table turns {table.shape[1]} dimensions, not {rot}")
-    S, H, D = k_cache.shape
+    T, max_pos = _turns(table, rot, positions)
+    S, H, D = _mixed_cache(k_cache, k_scale, v_cache, v_scale)
     n, m = Hq * D, H * D
-    _check(_lib.qlin_rope_kv_store_mixed(ROPE_LAYOUTS[layout], positions.shape[0], Hq, H, D, rot, _p(table),
-                                         table.shape[0], _p(positions), _p(q), _row_stride(q, n), _p(k),
-                                         _row_stride(k, m), _p(v), _row_stride(v, m), _p(q_out),
-                                         _row_stride(q_out, n), _p(slots), S, _p(k_cache), _p(k_scale), _p(v_cache),
-                                         _p(v_scale), _stream(stream)), "qlin_rope_kv_store_mixed")
+    _dense(slots, _I64, T, "slots")
+    _check(_lib.qlin_rope_kv_store_mixed(ROPE_LAYOUTS[layout], T, Hq, H, D, rot, _p(table), max_pos, _p(positions),
+                                         _p(q), _rows(q, T, n, "q"), _p(k), _rows(k, T, m, "k"), _p(v),
+                                         _rows(v, T, m, "v"), _p(q_out), _rows(q_out, T, n, "q_out"), _p(slots), S,
+                                         _p(k_cache), _p(k_scale), _p(v_cache), _p(v_scale), _stream(stream)),
+           "qlin_rope_kv_store_mixed")
 
 
 def qlin_attn_mixed(q, q_start, kv_len, block_table, block_size: int, k_cache, k_scale, v_cache, v_scale, max_q: int,
                     max_kv: int, scale: float, causal: bool, window: int, out, ws=None, stream=None):
     """q, out BF16 [T, Hq*D] rows; q_start int32 [B+1]; kv_len int32 [B]; block_table int32 [B, max_blocks]."""
-    S, H, D = k_cache.shape
-    T, B = q.shape[0], kv_len.shape[0]
-    n = q.shape[1]
+    S, H, D = _mixed_cache(k_cache, k_scale, v_cache, v_scale)
+    T, n = q.shape
+    B, blocks = kv_len.shape[0], block_table.shape[1]
+    if n % D:
+        raise ValueError(f"rows of q hold {n} elements, not heads of {D}")
+    _dense(q_start, _I32, B + 1, "q_start")
+    _dense(kv_len, _I32, B, "kv_len")
+    _dense(block_table, _I32, B * blocks, "block_table")
     wp, wb = _ws(ws)
-    _check(_lib.qlin_attn_mixed(B, T, n // D, H, D, _p(q), _row_stride(q, n), _p(q_start), max_q, _p(kv_len), max_kv,
-                                _p(block_table), block_table.shape[1], block_size, S, _p(k_cache), _p(k_scale),
-                                _p(v_cache), _p(v_scale), scale, int(causal), window, _p(out), _row_stride(out, n),
-                                wp, wb, _stream(stream)), "qlin_attn_mixed")
+    _check(_lib.qlin_attn_mixed(B, T, n // D, H, D, _p(q), _rows(q, T, n, "q"), _p(q_start), max_q, _p(kv_len), max_kv,
+                                _p(block_table), blocks, block_size, S, _p(k_cache), _p(k_scale), _p(v_cache),
+                                _p(v_scale), scale, int(causal), window, _p(out), _rows(out, T, n, "out"), wp, wb,
+                                _stream(stream)), "qlin_attn_mixed")
 
 
 def qlin_attn_mixed_workspace_bytes(B: int, Hq: int, H: int, D: int, max_q: int, max_kv: int, window: int = 0) -> int:
