@@ -116,9 +116,10 @@ struct RmsParams {
 };
 
 // The quantizer of a row: codes of fl32(y / s), by quotient() of common.cuh two
-// elements at a time.  Under a static scale |y| is first cut to `bound`, beyond
-// which every code is the largest (127.25 s rounds to 127, 512 s saturates);
-// that also keeps the quotient's intermediates finite.
+// elements at a time.  Under a static scale y is first cut to +-`bound`, beyond
+// which every code is the largest (127.25 s rounds to 127, 512 s saturates); that
+// also keeps the quotient's intermediates finite.  A NaN stays one for E4M3; for INT8
+// it becomes -bound, which gives quantize_one's code of a NaN (-127).
 template <int OUT, bool BOUNDED>
 struct RowQuantizer {
   Scale c;
@@ -129,13 +130,20 @@ struct RowQuantizer {
     r2 = f32x2_pack(c.r, c.r);
     ns2 = f32x2_pack(-s, -s);
   }
-  __device__ __forceinline__ static float cut(float x, float b) {  // the sign of x, the smaller magnitude
-    float d;
-    asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(b));
-    return d;
+  __device__ __forceinline__ float cut(float y) const {
+    if constexpr (OUT == kNormInt8) {
+      y = fmaxf(y, -bound);  // of a NaN and a number, the number
+      return BOUNDED ? y : fminf(y, bound);
+    } else if constexpr (BOUNDED) {
+      return y;
+    } else {
+      float d;  // the sign of y, the smaller magnitude
+      asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(y), "f"(bound));
+      return d;
+    }
   }
   __device__ __forceinline__ uint64_t quotients(uint64_t y) const {
-    if constexpr (!BOUNDED) y = f32x2_pack(cut(f32x2_lo(y), bound), cut(f32x2_hi(y), bound));
+    y = f32x2_pack(cut(f32x2_lo(y)), cut(f32x2_hi(y)));
     const uint64_t q = f32x2_mul(y, r2);
     return f32x2_fma(f32x2_fma(q, ns2, y), r2, q);
   }
