@@ -20,9 +20,13 @@
 // again), E4M3 by conversion; q is scaled by a power of two per row to
 // use float16's whole range; the products of one 32-dimension key group are
 // summed in fp32 and then scaled by the group's scale in fp32.  P is multiplied
-// by the value scales (and a power of two that keeps the product below 2^15)
-// in fp32 and rounded once to float16.  P^T as the second operand needs P's
-// fragments transposed: two movmatrix per 16 positions.
+// by the value scales in fp32 and rounded once to float16.  The scales of a tile share
+// a power of two, taken from that tile, under which P of a score at the maximum lies
+// between 1 and 2^15.  Where they lie too far apart for that (a position that few rows
+// see, or that has no weight, can have any scale) or one is zero, the part is done
+// again in a general form: each position's exponent joins its score, and O has a
+// reference of its own for each row.  P^T as the second operand needs P's fragments
+// transposed: two movmatrix per 16 positions.
 //
 // What bounds it beside HBM is the instructions of the conversions, so positions
 // of whole pages take their addresses from one table entry and one multiplication
@@ -40,6 +44,8 @@ namespace qlin {
 namespace {
 
 constexpr int kAttnWarps = 4;
+constexpr int kSpan = 14;    // exponents of the value scales of a tile: this far apart they share a window
+constexpr unsigned kWindow = (kSpan + 1u) << 23, kNoWindow = 0xFF000000u;
 constexpr int kAlign = 32;   // parts begin at multiples of this: the most positions a warp handles at once
 
 struct SplitParams : AttnDev {
@@ -72,6 +78,10 @@ __device__ __forceinline__ void mma_f16_from(float (&d)[4], const uint32_t (&a)[
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+// Exponent e of a value scale, 2^e <= |s| < 2^(e+1), from its bits (0, and what is not finite: the ends of float16).
+__device__ __forceinline__ int scale_exponent(unsigned abs_bits) {
+  return min(max((int)(abs_bits >> 23) - 127, -24), 15);
 }
 // base + i * step (one instruction).
 __device__ __forceinline__ const uint8_t *step_from(const uint8_t *base, uint32_t step, uint32_t i) {
@@ -111,13 +121,13 @@ struct Geometry {
   static constexpr int kRowStep = 32 / kChunks;         // rows the warp copies at once
   static constexpr int kCodes = kTile * D;
   static constexpr int kStages = D >= 128 ? 2 : 3;  // tiles in a warp's ring
-  // one stage: key codes, value codes, key scales, value scales, {valid, largest value scale}
+  // one stage: key codes, value codes, key scales, value scales, {valid, window that its value scales fit}
   static constexpr int kScaleAt = 2 * kCodes;
   static constexpr int kVScaleAt = kScaleAt + kTile * kGroups * 4;
   static constexpr int kInfoAt = kVScaleAt + kTile * 4;
   static constexpr int kStageBytes = kInfoAt + 16;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kJoinFloats = kRows * D + 2 * kRows + 4;  // a warp's result: O, m, l, exponent
+  static constexpr int kJoinFloats = kRows * D + 3 * kRows + 4;  // a warp's result: O, m, l, window or references of O
   static constexpr int kWarpBytes = kRingBytes > kJoinFloats * 4 ? kRingBytes : kJoinFloats * 4;
   static constexpr int kSmem = kAttnWarps * kWarpBytes;
   static constexpr int kCtas = D >= 256 || NT > 1 ? 2 : 3;  // resident CTAs the registers are budgeted for
@@ -139,8 +149,10 @@ __device__ __forceinline__ int value_chunk(int row, int c) {
   return D == 64 ? c ^ (row & 2) : c ^ (row & 6);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_attn_split(const SplitParams p) {
+// The work of a CTA.  Without WIDE false, and nothing written, where the value scales of a
+// tile lie too far apart for one exponent, or one of them is zero.
+template <int D, int NT, bool WIDE>
+__device__ __forceinline__ bool split_part(const SplitParams &p) {
   using Geo = Geometry<D, NT>;
   constexpr int kGroups = Geo::kGroups, kRows = Geo::kRows, kStages = Geo::kStages;
   constexpr int kTile = Geo::kTile, kHalves = kTile / 16;  // 16 positions are the rows of an MMA
@@ -169,7 +181,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
   const Sequence sq = sequence(p, b);
   if (sq.broken && h == 0 && tile == 0 && split == 0 && threadIdx.x == 0) set_status(p.status, QLIN_ERR_INVALID_ARG);
   const int R = sq.kept * p.G, r0 = tile * kRows;
-  if (r0 >= R || R > p.few_rows) return;
+  if (r0 >= R || R > p.few_rows) return true;
 
   // token and head of row r0 + i: one division for the tile
   const int tok0 = r0 / p.G, head0 = r0 - tok0 * p.G;
@@ -267,23 +279,28 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     }
     cp_async_commit();
   };
+  // Value scales are taken relative to 2^vexp.  `window` is its bit pattern: scales from it to
+  // 2^(vexp + 15) keep P of a score at the maximum between 1 and 2^15.
+  unsigned window = kNoWindow;
   // the scales of the tile issued last, as fp32, into its stage
   const auto put_scales = [&](int n) {
     if (n >= mine) return;
     uint8_t *at = ring + (n % kStages) * Geo::kStageBytes;
     const float v = half_bits_to_f32((uint16_t)sv);
-    const unsigned top = __reduce_max_sync(~0u, min(__float_as_uint(fabsf(v)), 0x7F7FFFFFu));
+    const bool fits = !((there >> lane) & 1) || __float_as_uint(v) - window < kWindow;
+    const unsigned fit = __all_sync(~0u, fits) ? window : ~0u;
     if (kTile == 32 || lane < kTile) {
       float *k = reinterpret_cast<float *>(at + Geo::kScaleAt) + lane * kGroups;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) k[i] = half_bits_to_f32((uint16_t)(sc[i / 2] >> (16 * (i & 1))));
       reinterpret_cast<float *>(at + Geo::kVScaleAt)[lane] = v;
     }
-    if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(there, top);
+    if (lane == 0) *reinterpret_cast<uint2 *>(at + Geo::kInfoAt) = make_uint2(there, fit);
   };
 
   // warps without a tile (few positions) go to the join, which leaves them out: 149 x 8 kv
   // heads over 2 positions 15.2 us, 17.1 with all warps prepared, written and joined
+  bool apart = false;
   if (mine > 0) {
     // the first tiles are on their way while q arrives
     for (int n = 0; n < kStages - 1; ++n) {
@@ -349,7 +366,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
 #pragma unroll
       for (int i = 0; i < kDims / 2; ++i) O[nt][i][0] = O[nt][i][1] = O[nt][i][2] = O[nt][i][3] = 0.0f;
     }
-    int vexp = -1000;  // O is sum p v 2^-vexp
+    // O is sum p v 2^-vexp with p = 2^(s - m); WIDE: sum 2^s v 2^-ref, a reference for each column
+    float ref[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) ref[nt][0] = ref[nt][1] = -INFINITY;
 
     for (int n = 0; n < mine; ++n) {
       cp_async_wait<kStages - 2>();
@@ -359,6 +379,23 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
       const uint32_t at = ring_at + (n % kStages) * Geo::kStageBytes;
       uint8_t *stage = ring + (n % kStages) * Geo::kStageBytes;
       const uint2 info = *reinterpret_cast<const uint2 *>(stage + Geo::kInfoAt);
+      if (!WIDE && info.y != window) {
+        // the tile needs another window, or has scales that no window holds
+        const unsigned a =
+            (info.x >> lane) & 1 ? __float_as_uint(fabsf(reinterpret_cast<float *>(stage + Geo::kVScaleAt)[own])) : ~0u;
+        const unsigned low = __reduce_min_sync(~0u, a), top = __reduce_max_sync(~0u, a == ~0u ? 0u : a);
+        const int e_top = scale_exponent(top), e_low = min(scale_exponent(low), e_top);
+        apart |= low == 0 || e_top - e_low > kSpan;  // (a way out of the loop costs the others 0.5 %)
+        const unsigned now = (unsigned)(max(e_top - kSpan, e_low - 4) + 127) << 23;
+        const float by = window == kNoWindow ? 0.0f : __uint_as_float(0x3F800000u + window - now);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < kDims / 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) O[nt][i][c] *= by;
+        window = now;
+      }
       const int j0 = first_of(n);
       const bool full = info.x == (~0u >> (32 - kTile)) && j0 >= all_lo && j0 + kTile <= all_hi;
       float vs[kHalves][2];  // of positions g and g + 8 of each half
@@ -437,24 +474,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
         __syncwarp();
       }
 
-      // value scales relative to 2^vexp; the exponent grows when P would pass 2^15
-      int e = (int)(info.y >> 23) - 127;
-      e = min(max(e, -24), 16);
-      if (e - vexp > 13) {
-        const float down = exp2_approx((float)(vexp - (e - 7)));
+      float ev[kHalves][2];  // WIDE: exponents of the scales, which are left between 1 and 2
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int f = 0; f < kHalves; ++f)
 #pragma unroll
-          for (int i = 0; i < kDims / 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) O[nt][i][c] *= down;
-        vexp = e - 7;
-      }
-#pragma unroll
-      for (int f = 0; f < kHalves; ++f) {
-        vs[f][0] *= pow2i(-vexp);
-        vs[f][1] *= pow2i(-vexp);
-      }
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (WIDE) {
+            const unsigned a = __float_as_uint(fabsf(vs[f][i]));
+            ev[f][i] = a ? (float)scale_exponent(a) : -INFINITY;
+            vs[f][i] *= pow2i(-scale_exponent(a));
+          } else {
+            vs[f][i] *= __uint_as_float(0x7F000000u - window);  // 2^-vexp
+          }
+        }
 
       // online softmax per column
       uint32_t pf[kHalves][NT][2];
@@ -470,7 +502,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
           mx[0] = fmaxf(mx[0], __shfl_xor_sync(~0u, mx[0], o));
           mx[1] = fmaxf(mx[1], __shfl_xor_sync(~0u, mx[1], o));
         }
-        const bool grew = mx[0] > m[nt][0] || mx[1] > m[nt][1];
+        bool grew = mx[0] > m[nt][0] || mx[1] > m[nt][1];
+        float vx[2] = {-INFINITY, -INFINITY};  // WIDE: the largest score with its value's exponent
+        if constexpr (WIDE) {
+#pragma unroll
+          for (int f = 0; f < kHalves; ++f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vx[i & 1] = fmaxf(vx[i & 1], S[f][nt][i] + ev[f][i >> 1]);
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) {
+            vx[0] = fmaxf(vx[0], __shfl_xor_sync(~0u, vx[0], o));
+            vx[1] = fmaxf(vx[1], __shfl_xor_sync(~0u, vx[1], o));
+          }
+          grew = grew || vx[0] - 12.0f > ref[nt][0] || vx[1] - 12.0f > ref[nt][1];
+        }
         if (__any_sync(~0u, grew)) {
           float a[2];
 #pragma unroll
@@ -479,6 +524,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
             a[c] = exp2_approx(m[nt][c] - (now == -INFINITY ? 0.0f : now));
             m[nt][c] = now;
             l[nt][c] *= a[c];
+            if constexpr (WIDE) {  // P stays below 2^14
+              const float y = fmaxf(ref[nt][c], vx[c] - 12.0f);
+              a[c] = y == -INFINITY ? 1.0f : exp2_approx(ref[nt][c] - y);
+              ref[nt][c] = y;
+            }
           }
 #pragma unroll
           for (int i = 0; i < kDims / 2; ++i) {
@@ -495,7 +545,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
           l[nt][0] += p00 + p10;
           l[nt][1] += p01 + p11;
           float w00 = p00 * vs[f][0], w01 = p01 * vs[f][0], w10 = p10 * vs[f][1], w11 = p11 * vs[f][1];
-          if (!full) {  // an unseen position adds nothing, whatever its scale
+          if constexpr (WIDE) {
+            const float y0 = ref[nt][0] == -INFINITY ? 0.0f : ref[nt][0];
+            const float y1 = ref[nt][1] == -INFINITY ? 0.0f : ref[nt][1];
+            w00 = exp2_approx(s[0] + ev[f][0] - y0) * vs[f][0], w01 = exp2_approx(s[1] + ev[f][0] - y1) * vs[f][0];
+            w10 = exp2_approx(s[2] + ev[f][1] - y0) * vs[f][1], w11 = exp2_approx(s[3] + ev[f][1] - y1) * vs[f][1];
+          }
+          if (WIDE || !full) {  // an unseen position adds nothing, whatever its scale
             if (s[0] == -INFINITY) w00 = 0.0f;
             if (s[1] == -INFINITY) w01 = 0.0f;
             if (s[2] == -INFINITY) w10 = 0.0f;
@@ -569,11 +625,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
         if (g == 0) {
           res[kRows * D + r] = m[nt][c];
           res[kRows * D + kRows + r] = l[nt][c];
+          if constexpr (WIDE) res[kRows * D + 2 * kRows + r] = ref[nt][c];
         }
       }
-    if (lane == 0) res[kRows * D + 2 * kRows] = pow2i(vexp);
+    if (!WIDE && lane == 0) res[kRows * D + 2 * kRows] = __uint_as_float(window);  // 2^vexp
   }
-  __syncthreads();
+  if constexpr (WIDE) {
+    __syncthreads();
+  } else if (__syncthreads_or(apart)) {
+    return false;
+  }
   const int active = min(tiles, kAttnWarps);
   for (int i = threadIdx.x; i < kRows * D / 4; i += 32 * kAttnWarps) {
     const int r = i / (D / 4), d = i % (D / 4) * 4;
@@ -585,6 +646,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
     for (int k = 0; k < kAttnWarps; ++k)
       if (k < active) top = fmaxf(top, w[k * kStep + kRows * D + r]);
     const float z = top == -INFINITY ? 0.0f : top;
+    float y0 = z;  // the reference of O
+    if constexpr (WIDE) {
+      y0 = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kAttnWarps; ++k)
+        if (k < active) y0 = fmaxf(y0, w[k * kStep + kRows * D + 2 * kRows + r]);
+      y0 = y0 == -INFINITY ? 0.0f : y0;
+    }
     float L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -593,11 +662,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
       const float *x = w + k * kStep;
       const float f = exp2_approx(x[kRows * D + r] - z);
       L = fmaf(f, x[kRows * D + kRows + r], L);
-      const float fo = f * x[kRows * D + 2 * kRows];
+      const float fo = WIDE ? exp2_approx(x[kRows * D + 2 * kRows + r] - y0) : f * x[kRows * D + 2 * kRows];
       const float4 y = *reinterpret_cast<const float4 *>(x + r * D + d);
       o.x = fmaf(fo, y.x, o.x), o.y = fmaf(fo, y.y, o.y), o.z = fmaf(fo, y.z, o.z), o.w = fmaf(fo, y.w, o.w);
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    if constexpr (WIDE) {
+      // 2^(y0 - z) in two halves: it can lie below binary32's range where its product with O does not
+      const float half = exp2_approx(0.5f * (y0 - z));
+      o.x *= half, o.y *= half, o.z *= half, o.w *= half;
+      inv *= half;
+    }
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
     if (p.parts.splits == 1) {
       const int rr = r0 + r;
@@ -611,6 +686,23 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas) k_att
       if (d == 0) p.parts.lse[at] = L == 0.0f ? -INFINITY : top + log2f(L);
     }
   }
+  return true;
+}
+
+// The general form begins again: carried on from where the other leaves, its code costs that
+// one 4 % (D 128, batch of 256 ragged contexts up to 4096: 77.7 us; as here 74.2).  From D 128 on it is
+// a function of its own for the same reason (inline 79.0 us); below, the call costs more than the
+// code (D 64, 64 contexts, 8 kv heads: 57.5 us with it, 54.6 inline).
+template <int D, int NT>
+__device__ __noinline__ void split_part_wide(const SplitParams &p) {
+  split_part<D, NT, true>(p);
+}
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas)
+    k_attn_split(const __grid_constant__ SplitParams p) {
+  if (split_part<D, NT, false>(p)) return;
+  if constexpr (D >= 128) split_part_wide<D, NT>(p);
+  else split_part<D, NT, true>(p);
 }
 
 // Joins the parts of one row: out = sum_s w_s o_s / sum_s w_s with
