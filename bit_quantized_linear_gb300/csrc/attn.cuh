@@ -100,10 +100,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half(uint16_t c) {
 }
 
 // Partial results of rows whose positions several CTAs share: [unit][part][row of
-// the unit's tile] O (D fp32) and the base-2 logarithm of its sum (-inf: nothing
-// seen), unit = (b * H + h) * row_tiles + tile.
+// the unit's tile] O (D fp32, divided by its sum), and the sum with the base-2
+// reference it was taken under ({-inf, 0}: nothing seen; kept apart, as a logarithm
+// of the sum would round away beside a large reference),
+// unit = (b * H + h) * row_tiles + tile.
 struct AttnParts {
-  float *o, *lse;
+  float *o;
+  float2 *sum;  // {reference, sum}
   int row_tiles, rows, splits;
 };
 // Joins them into `out`.  many: of the sequences with more than p.few_rows rows, else of the others.

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       if (p.parts.splits > 1) {
         float4 *o = reinterpret_cast<float4 *>(p.parts.o + part_row(r) * D) + i % (D / 8) * 2;
         o[0] = o[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (i % (D / 8) == 0) p.parts.lse[part_row(r)] = -INFINITY;
+        if (i % (D / 8) == 0) p.parts.sum[part_row(r)] = make_float2(-INFINITY, 0.0f);
         continue;
       }
       uint16_t *dst = p.out + (int64_t)(sq.first + r / p.G) * p.ldo + (int64_t)(h * p.G + r % p.G) * D;
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               to[i] = make_float4(out(o[4 * i]), out(o[4 * i + 1]), out(o[4 * i + 2]), out(o[4 * i + 3]));
-            if (c == 0) p.parts.lse[part_row(r)] = l == 0.0f ? -INFINITY : m_l - kPBias + log2f(l);
+            if (c == 0) p.parts.sum[part_row(r)] = make_float2(m_l, l);
           }
           continue;
         }
@@ -801,7 +801,7 @@ AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t G, int64_t D, in
   plan.chunk = (range_tiles + plan.splits - 1) / plan.splits;
   plan.splits = (range_tiles + plan.chunk - 1) / plan.chunk;
   plan.ws_bytes = plan.image_bytes;
-  if (plan.splits > 1) plan.ws_bytes += round_up((size_t)(ctas * plan.splits * rows * (D + 1) * 4), 256);
+  if (plan.splits > 1) plan.ws_bytes += round_up((size_t)(ctas * plan.splits * rows * (D + 2) * 4), 256);
   return plan;
 }
 
@@ -816,7 +816,7 @@ cudaError_t launch_attn_prefill(const AttnArgs &a, const AttnPrefillPlan &plan, 
   p.chunk = (int)plan.chunk;
   p.parts.row_tiles = p.row_tiles, p.parts.rows = 2 * kRowTile, p.parts.splits = (int)plan.splits;
   p.parts.o = reinterpret_cast<float *>((char *)ws + plan.image_bytes);
-  p.parts.lse = p.parts.o + a.B * a.H * plan.row_tiles * plan.splits * p.parts.rows * a.D;
+  p.parts.sum = (float2 *)(p.parts.o + a.B * a.H * plan.row_tiles * plan.splits * p.parts.rows * a.D);
   if (a.D == 64) return launch_d<64>(p, plan.heads, st);
   if (a.D == 128) return launch_d<128>(p, plan.heads, st);
   return cudaErrorInvalidValue;

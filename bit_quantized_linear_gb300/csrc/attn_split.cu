@@ -46,6 +46,7 @@ namespace {
 constexpr int kAttnWarps = 4;
 constexpr int kSpan = 14;    // exponents of the value scales of a tile: this far apart they share a window
 constexpr unsigned kWindow = (kSpan + 1u) << 23, kNoWindow = 0xFF000000u;
+constexpr float kWideBias = 14.0f;  // in the general form P of the maximum lies between 2^14 and 2^15
 constexpr int kAlign = 32;   // parts begin at multiples of this: the most positions a warp handles at once
 
 struct SplitParams : AttnDev {
@@ -127,7 +128,7 @@ struct Geometry {
   static constexpr int kInfoAt = kVScaleAt + kTile * 4;
   static constexpr int kStageBytes = kInfoAt + 16;
   static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr int kJoinFloats = kRows * D + 3 * kRows + 4;  // a warp's result: O, m, l, window or references of O
+  static constexpr int kJoinFloats = kRows * D + 4 * kRows + 4;  // a warp's result: O, m, l, window or references of O
   static constexpr int kWarpBytes = kRingBytes > kJoinFloats * 4 ? kRingBytes : kJoinFloats * 4;
   static constexpr int kSmem = kAttnWarps * kWarpBytes;
   static constexpr int kCtas = D >= 256 || NT > 1 ? 2 : 3;  // resident CTAs the registers are budgeted for
@@ -366,10 +367,12 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
 #pragma unroll
       for (int i = 0; i < kDims / 2; ++i) O[nt][i][0] = O[nt][i][1] = O[nt][i][2] = O[nt][i][3] = 0.0f;
     }
-    // O is sum p v 2^-vexp with p = 2^(s - m); WIDE: sum 2^s v 2^-ref, a reference for each column
-    float ref[NT][2];
+    // O is sum p v 2^-vexp with p = 2^(s - m); WIDE: sum 2^s v 2^(bias - ref_s - ref_v) with references for
+    // each column, a score and the exponent of its value.  They are kept apart: differences of scores
+    // are exact near the maximum, and the exponents join them, however large the scores are.
+    float ref_s[NT][2], ref_v[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) ref[nt][0] = ref[nt][1] = -INFINITY;
+    for (int nt = 0; nt < NT; ++nt) ref_s[nt][0] = ref_s[nt][1] = -INFINITY, ref_v[nt][0] = ref_v[nt][1] = 0.0f;
 
     for (int n = 0; n < mine; ++n) {
       cp_async_wait<kStages - 2>();
@@ -440,8 +443,9 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          S[f][nt][0] *= cf[nt][0], S[f][nt][2] *= cf[nt][0];
-          S[f][nt][1] *= cf[nt][1], S[f][nt][3] *= cf[nt][1];
+          // rounded here: the differences from the maximum are those of the rounded scores
+          S[f][nt][0] = __fmul_rn(S[f][nt][0], cf[nt][0]), S[f][nt][2] = __fmul_rn(S[f][nt][2], cf[nt][0]);
+          S[f][nt][1] = __fmul_rn(S[f][nt][1], cf[nt][1]), S[f][nt][3] = __fmul_rn(S[f][nt][3], cf[nt][1]);
         }
       }
       if (!full) {
@@ -503,18 +507,26 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
           mx[1] = fmaxf(mx[1], __shfl_xor_sync(~0u, mx[1], o));
         }
         bool grew = mx[0] > m[nt][0] || mx[1] > m[nt][1];
-        float vx[2] = {-INFINITY, -INFINITY};  // WIDE: the largest score with its value's exponent
+        // WIDE: the largest score with its value's exponent
+        float top_s[2] = {ref_s[nt][0], ref_s[nt][1]}, top_v[2] = {ref_v[nt][0], ref_v[nt][1]};
         if constexpr (WIDE) {
+          const auto take = [&](int c, float x, float e) {
+            if ((x - top_s[c]) + (e - top_v[c]) > 0.0f) top_s[c] = x, top_v[c] = e;
+          };
 #pragma unroll
           for (int f = 0; f < kHalves; ++f)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vx[i & 1] = fmaxf(vx[i & 1], S[f][nt][i] + ev[f][i >> 1]);
+            for (int i = 0; i < 4; ++i) take(i & 1, S[f][nt][i], ev[f][i >> 1]);
 #pragma unroll
-          for (int o = 4; o < 32; o *= 2) {
-            vx[0] = fmaxf(vx[0], __shfl_xor_sync(~0u, vx[0], o));
-            vx[1] = fmaxf(vx[1], __shfl_xor_sync(~0u, vx[1], o));
-          }
-          grew = grew || vx[0] - 12.0f > ref[nt][0] || vx[1] - 12.0f > ref[nt][1];
+          for (int o = 4; o < 32; o *= 2)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float x = __shfl_xor_sync(~0u, top_s[c], o), e = __shfl_xor_sync(~0u, top_v[c], o);
+              take(c, x, e);
+            }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            grew = grew || (top_s[c] - ref_s[nt][c]) + (top_v[c] - ref_v[nt][c]) > 0.0f;
         }
         if (__any_sync(~0u, grew)) {
           float a[2];
@@ -524,10 +536,10 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
             a[c] = exp2_approx(m[nt][c] - (now == -INFINITY ? 0.0f : now));
             m[nt][c] = now;
             l[nt][c] *= a[c];
-            if constexpr (WIDE) {  // P stays below 2^14
-              const float y = fmaxf(ref[nt][c], vx[c] - 12.0f);
-              a[c] = y == -INFINITY ? 1.0f : exp2_approx(ref[nt][c] - y);
-              ref[nt][c] = y;
+            if constexpr (WIDE) {
+              const float by = (ref_s[nt][c] - top_s[c]) + (ref_v[nt][c] - top_v[c]);
+              a[c] = top_s[c] == -INFINITY ? 1.0f : exp2_approx(by);
+              ref_s[nt][c] = top_s[c], ref_v[nt][c] = top_v[c];
             }
           }
 #pragma unroll
@@ -546,10 +558,12 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
           l[nt][1] += p01 + p11;
           float w00 = p00 * vs[f][0], w01 = p01 * vs[f][0], w10 = p10 * vs[f][1], w11 = p11 * vs[f][1];
           if constexpr (WIDE) {
-            const float y0 = ref[nt][0] == -INFINITY ? 0.0f : ref[nt][0];
-            const float y1 = ref[nt][1] == -INFINITY ? 0.0f : ref[nt][1];
-            w00 = exp2_approx(s[0] + ev[f][0] - y0) * vs[f][0], w01 = exp2_approx(s[1] + ev[f][0] - y1) * vs[f][0];
-            w10 = exp2_approx(s[2] + ev[f][1] - y0) * vs[f][1], w11 = exp2_approx(s[3] + ev[f][1] - y1) * vs[f][1];
+            const float y0 = ref_s[nt][0] == -INFINITY ? 0.0f : ref_s[nt][0], e0 = kWideBias - ref_v[nt][0];
+            const float y1 = ref_s[nt][1] == -INFINITY ? 0.0f : ref_s[nt][1], e1 = kWideBias - ref_v[nt][1];
+            w00 = exp2_approx((s[0] - y0) + (ev[f][0] + e0)) * vs[f][0];
+            w01 = exp2_approx((s[1] - y1) + (ev[f][0] + e1)) * vs[f][0];
+            w10 = exp2_approx((s[2] - y0) + (ev[f][1] + e0)) * vs[f][1];
+            w11 = exp2_approx((s[3] - y1) + (ev[f][1] + e1)) * vs[f][1];
           }
           if (WIDE || !full) {  // an unseen position adds nothing, whatever its scale
             if (s[0] == -INFINITY) w00 = 0.0f;
@@ -625,7 +639,10 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
         if (g == 0) {
           res[kRows * D + r] = m[nt][c];
           res[kRows * D + kRows + r] = l[nt][c];
-          if constexpr (WIDE) res[kRows * D + 2 * kRows + r] = ref[nt][c];
+          if constexpr (WIDE) {
+            res[kRows * D + 2 * kRows + r] = ref_s[nt][c];
+            res[kRows * D + 3 * kRows + r] = ref_v[nt][c];
+          }
         }
       }
     if (!WIDE && lane == 0) res[kRows * D + 2 * kRows] = __uint_as_float(window);  // 2^vexp
@@ -646,13 +663,15 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
     for (int k = 0; k < kAttnWarps; ++k)
       if (k < active) top = fmaxf(top, w[k * kStep + kRows * D + r]);
     const float z = top == -INFINITY ? 0.0f : top;
-    float y0 = z;  // the reference of O
+    float top_s = -INFINITY, top_v = 0.0f;  // WIDE: the reference of O
     if constexpr (WIDE) {
-      y0 = -INFINITY;
 #pragma unroll
       for (int k = 0; k < kAttnWarps; ++k)
-        if (k < active) y0 = fmaxf(y0, w[k * kStep + kRows * D + 2 * kRows + r]);
-      y0 = y0 == -INFINITY ? 0.0f : y0;
+        if (k < active) {
+          const float *x = w + k * kStep + kRows * D + 2 * kRows + r;
+          if ((x[0] - top_s) + (x[kRows] - top_v) > 0.0f) top_s = x[0], top_v = x[kRows];
+        }
+      top_s = top_s == -INFINITY ? 0.0f : top_s;
     }
     float L = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -662,14 +681,15 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
       const float *x = w + k * kStep;
       const float f = exp2_approx(x[kRows * D + r] - z);
       L = fmaf(f, x[kRows * D + kRows + r], L);
-      const float fo = WIDE ? exp2_approx(x[kRows * D + 2 * kRows + r] - y0) : f * x[kRows * D + 2 * kRows];
+      const float *ref = x + kRows * D + 2 * kRows;
+      const float fo = WIDE ? exp2_approx((ref[r] - top_s) + (ref[kRows + r] - top_v)) : f * ref[0];
       const float4 y = *reinterpret_cast<const float4 *>(x + r * D + d);
       o.x = fmaf(fo, y.x, o.x), o.y = fmaf(fo, y.y, o.y), o.z = fmaf(fo, y.z, o.z), o.w = fmaf(fo, y.w, o.w);
     }
     float inv = L == 0.0f ? 0.0f : 1.0f / L;
     if constexpr (WIDE) {
-      // 2^(y0 - z) in two halves: it can lie below binary32's range where its product with O does not
-      const float half = exp2_approx(0.5f * (y0 - z));
+      // 2^(top_s + top_v - z) in two halves: it can lie below binary32's range where its product with O does not
+      const float half = exp2_approx(0.5f * ((top_s - z) + (top_v - kWideBias)));
       o.x *= half, o.y *= half, o.z *= half, o.w *= half;
       inv *= half;
     }
@@ -683,7 +703,7 @@ __device__ __forceinline__ bool split_part(const SplitParams &p) {
     } else {
       const int64_t at = cta * kRows + r;
       *reinterpret_cast<float4 *>(p.parts.o + at * D + d) = o;
-      if (d == 0) p.parts.lse[at] = L == 0.0f ? -INFINITY : top + log2f(L);
+      if (d == 0) p.parts.sum[at] = make_float2(top, L);
     }
   }
   return true;
@@ -706,7 +726,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas)
 }
 
 // Joins the parts of one row: out = sum_s w_s o_s / sum_s w_s with
-// w_s = 2^(lse_s - max lse).  Many parts: a CTA per row, its warps over the parts;
+// w_s = l_s 2^(m_s - max m).  Many parts: a CTA per row, its warps over the parts;
 // few: a warp per row.
 constexpr int kFewParts = 16;
 constexpr int kManyWarps = 16, kFewWarps = 8;  // warps of a CTA
@@ -731,26 +751,26 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps))
   const Sequence sq = sequence(p, b);
   const int rr = tile * rows + r;
   if (rr >= sq.kept * p.G || (sq.kept * p.G > p.few_rows) != many) return;
-  const float *lse = parts.lse + unit * parts.splits * rows + r;
+  const float2 *sum = parts.sum + unit * parts.splits * rows + r;
   const float *src = parts.o + (unit * parts.splits * rows + r) * D + lane * V;
   uint32_t x[kBatch][V];
-  float e[kBatch];
+  float2 e[kBatch];
   const auto load = [&](int s0) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int64_t s = s0 + i * kOver;
-      e[i] = -INFINITY;
+      e[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
       for (int v = 0; v < V; ++v) x[i][v] = 0u;
       if (s < parts.splits) {
-        e[i] = ld_input(lse + s * rows);
+        e[i] = ld_input(sum + s * rows);
         load_words<V>(src + s * rows * D, x[i]);
       }
     }
   };
   load(part);
   float top = -INFINITY;
-  for (int s = lane; s < parts.splits; s += 32) top = fmaxf(top, ld_input(lse + (int64_t)s * rows));
+  for (int s = lane; s < parts.splits; s += 32) top = fmaxf(top, ld_input(&sum[(int64_t)s * rows].x));
   top = warp_max(top);
   const float z = top == -INFINITY ? 0.0f : top;
   float o[V], W = 0.0f;
@@ -759,7 +779,7 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps))
   for (int s0 = part; s0 < parts.splits;) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = exp2_approx(e[i] - z);  // 0 beyond the last part
+      const float w = e[i].y * exp2_approx(e[i].x - z);  // 0 beyond the last part
       W += w;
 #pragma unroll
       for (int v = 0; v < V; ++v) o[v] = fmaf(w, __uint_as_float(x[i][v]), o[v]);
@@ -882,7 +902,7 @@ AttnSplitPlan attn_split_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64
   constexpr int64_t step = kAlign * kAttnWarps;
   plan.chunk = std::max(step, (range + want * step - 1) / (want * step) * step);
   plan.splits = (int)std::max<int64_t>(1, (range + plan.chunk - 1) / plan.chunk);
-  plan.ws_bytes = plan.splits > 1 ? (size_t)(units * plan.splits * plan.rows * (D + 1) * 4) : 0;
+  plan.ws_bytes = plan.splits > 1 ? (size_t)(units * plan.splits * plan.rows * (D + 2) * 4) : 0;
   plan.ws_bytes = round_up(plan.ws_bytes, 256);
   return plan;
 }
@@ -895,7 +915,7 @@ cudaError_t launch_attn_split(const AttnArgs &a, const AttnSplitPlan &plan, int 
   p.parts.row_tiles = plan.row_tiles, p.parts.rows = plan.rows, p.parts.splits = plan.splits, p.chunk = plan.chunk;
   const int64_t units = a.B * a.H * plan.row_tiles;
   p.parts.o = (float *)ws;
-  p.parts.lse = p.parts.o ? p.parts.o + units * plan.splits * plan.rows * a.D : nullptr;
+  p.parts.sum = p.parts.o ? (float2 *)(p.parts.o + units * plan.splits * plan.rows * a.D) : nullptr;
   switch (a.D) {
     case 32: return launch_d<32>(p, plan.rows, units, st);
     case 64: return launch_d<64>(p, plan.rows, units, st);
