@@ -22,8 +22,9 @@
 //
 // Scaling.  q rows are scaled by powers of two to use float16's range.  The keys
 // of 32 (D 128) or 64 (D 64) positions, a unit, are scaled by code scale * 2^-ek
-// and the values by 2^-ev, with one exponent each for the unit (where its value
-// scales lie too far apart for float16, one for each position), so float16 holds
+// and the values by 2^-ev, with one exponent each for the unit (where its key or
+// value scales lie too far apart for float16, one for each position: a position that
+// a row does not see leaves that row's others in place), so float16 holds
 // them whatever the cache's scales; 2^ek joins the score's factor and ev the
 // exponent, so that neither costs the softmax an instruction per score.  O is
 // rescaled only where a row's maximum grew by more than 2^6 since its reference;
@@ -31,7 +32,6 @@
 // reference (they would push P of the others out of float16): they count in the
 // sum of the row alone, which for that has a reference of its own.
 #include <algorithm>
-#include <type_traits>
 
 #include "attn.cuh"
 #include "common.cuh"
@@ -52,18 +52,21 @@ constexpr int kThreads = 320;
 constexpr int kMetaSlots = 4;
 constexpr float kPBias = 8.0f;  // P is 2^8 p: float16's subnormals lie below 2^-22 p
 constexpr float kGrowth = 6.0f;
-constexpr float kLead = 32.0f;  // a score without a value may pass the sum's reference by 2^this
+constexpr float kLead = 32.0f;  // a score may pass the sum's reference by 2^this where O has another
 constexpr int kValueUp = 5;     // a value's scale becomes 2^5..2^6 (times at most 448: below float16's 65504)
 constexpr int kValueSpan = 8;   // scales of a unit within 2^8 share an exponent: E4M3's 2^-9 stays normal
+constexpr int kKeySpan = 14;    // key scales within 2^14: a code of 1 stays normal
+constexpr int kNoValue = -128;  // in pos_ev, of a position whose value scale is 0
 
 // What the softmax needs of a position tile beside S, per 32 positions: the
 // exponents of keys and values, positions present, positions whose value is not
-// finite (zero in the tile, so that P = 0 leaves it alone), and
-// whether the values have an exponent for each position instead (pos_ev).
+// finite (zero in the tile, so that P = 0 leaves it alone); and for the general loop exponents of
+// each position.  `wide`: some unit's scales lie too far apart for one exponent.
 struct __align__(16) TileMeta {
   int ek[4], ev[4];
-  unsigned valid[4], poison[4], wide[4];
-  float pos_ev[kPos];
+  unsigned valid[4], poison[4];
+  signed char pos_ek[kPos], pos_ev[kPos];
+  int wide;
 };
 
 template <int D>
@@ -132,7 +135,7 @@ __device__ __forceinline__ float half_at(uint32_t w, int i) {
 // of values.  A lane holds the codes of 16 dimensions (chunk lane % C) of positions
 // 8 * (lane / C) + i.
 template <int D>
-__global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const PrefillParams p) {
+__global__ void __launch_bounds__(64 * Config<D>::kUnits, D == 128 ? 4 : 7) k_attn_unpack(const PrefillParams p) {
   using C = Config<D>;
   constexpr int kWords = C::kUnit / 32;  // 32-position words of a unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -207,16 +210,32 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
     low = a ? min(low, a) : low;
   }
   const int e = exponent(__reduce_max_sync(~0u, top));
+  const int span = e - min(exponent(__reduce_min_sync(~0u, low)), e);
+  bool nothing = false;  // a position there with a value scale of 0
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) nothing |= value && ((valid[i] >> lane) & 1) && (scale[i] & 0x7FFFu) == 0;
+  const bool wide = __any_sync(~0u, nothing) || span > (value ? kValueSpan : kKeySpan);
+  const int tile_wide = __syncthreads_or(wide);
+  if (threadIdx.x == 0) tm.wide = tile_wide;
 
   if (!value) {
-    const float down = pow2i(-e);
     if (lane < kWords) {
       tm.ek[block * kWords + lane] = e;
       tm.valid[block * kWords + lane] = lane == 0 ? valid[0] : valid[kWords - 1];
     }
     uint32_t sw[2];
+    int ep = e;  // of the position whose scales word i holds
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sw[i] = half2_of(half_at(scale[i], 0) * down, half_at(scale[i], 1) * down);
+    for (int i = 0; i < 2; ++i) {
+      if (i < kWords) {
+        uint32_t most = __vmaxu2(scale[i] & 0x7FFF7FFFu, kWords == 1 ? scale[1] & 0x7FFF7FFFu : 0u);
+        most = max(most & 0xFFFFu, most >> 16);
+        ep = wide && most ? exponent(__float_as_uint(half_at(most, 0))) : e;
+        tm.pos_ek[block * C::kUnit + i * 32 + lane] = (signed char)ep;
+      }
+      const float down = pow2i(-ep);
+      sw[i] = half2_of(half_at(scale[i], 0) * down, half_at(scale[i], 1) * down);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int t = octet * 8 + i, r = block * C::kUnit + t;
@@ -238,11 +257,6 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
     return;
   }
 
-  bool nothing = false;  // a position there with a scale of 0
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) nothing |= ((valid[i] >> lane) & 1) && (scale[i] & 0x7FFFu) == 0;
-  const bool wide =
-      __any_sync(~0u, nothing) || e - min(exponent(__reduce_min_sync(~0u, low)), e) > kValueSpan;
   // Values that are not finite: zeros in the tile, and a mark.
   unsigned poison[kWords];
 #pragma unroll
@@ -267,7 +281,6 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
   if (lane < kWords) {
     tm.ev[block * kWords + lane] = e - kValueUp;
     tm.poison[block * kWords + lane] = lane == 0 ? poison[0] : poison[kWords - 1];
-    tm.wide[block * kWords + lane] = wide;
   }
   // scales as float16, the octet's then two positions at a time
   uint32_t sw[kWords];
@@ -276,7 +289,7 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
     const float s = half_at(scale[i], 0);
     const unsigned a = __float_as_uint(fabsf(s));
     const int es = wide && a ? exponent(a) : e;
-    tm.pos_ev[block * C::kUnit + i * 32 + lane] = a ? (float)(es - kValueUp) : -INFINITY;
+    tm.pos_ev[block * C::kUnit + i * 32 + lane] = (signed char)(a ? es - kValueUp : kNoValue);
     const uint32_t w = __half_as_ushort(__float2half_rn(s * pow2i(kValueUp - es)));
     sw[i] = w | (__shfl_down_sync(~0u, w, 1) << 16);
   }
@@ -431,187 +444,199 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     const uint32_t s_at = at + C::kS + half * kPos, o_at = at + C::kO + half * D;
     int row_lo = lo, row_hi = end;
     if (r < R) sees(p, sq, r / p.G, row_lo, row_hi);
-    // O is sum p v under the reference m, l is sum p under m_l >= m; to_l = 2^(m - m_l)
-    float m = -INFINITY, m_l = -INFINITY, l = 0.0f, to_l = 0.0f;
+    // O is sum p v under the reference m + m_v (m_v: a value's exponent), l is sum p under m_l
+    float m = -INFINITY, m_v = 0.0f, m_l = -INFINITY, l = 0.0f;
     bool ok = true;
     int j = 0;
-    // The tiles from j on; without ANY, up to the first with a unit that is wide (m_l
-    // is m until then).  Such tiles are rare, and their code in the loop of the others
-    // costs each of them: 1342 us against 1169 at 8192 x 16384, 28 heads over 4 of 128.
-    const auto tiles = [&](auto any) {
-      constexpr bool ANY = decltype(any)::value;
-      for (; j < n; ++j) {
-        ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
-             mbar_wait(&sh.s_full[half], j & 1, abort_flag);
-        if (!__all_sync(~0u, ok)) break;
-        tc_fence_after();
-        const TileMeta &tm = sh.meta[j % kMetaSlots];
-        if (!ANY && (tm.wide[0] | tm.wide[1] | tm.wide[2] | tm.wide[3])) break;
-        const int j0 = beg + j * kPos;
-        const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
-                          (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
-                          (tm.poison[0] | tm.poison[1] | tm.poison[2] | tm.poison[3]) == 0;
-        // Scores this row does not see become -inf, those of a NaN value NaN (32 columns
-        // from c * 32 on).
-        const auto mask = [&](int c, uint32_t (&s)[32]) {
-          const int from = row_lo - (j0 + c * 32), to = row_hi - (j0 + c * 32);
-          unsigned seen = tm.valid[c];
-          seen &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
-          seen &= to <= 0 ? 0u : to >= 32 ? ~0u : ~(~0u << to);
+    const auto arrives = [&] {  // S of tile j, with its metadata
+      ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
+           mbar_wait(&sh.s_full[half], j & 1, abort_flag);
+      tc_fence_after();
+      return __all_sync(~0u, ok) != 0;
+    };
+    // Scores this row does not see become -inf, those of a NaN value NaN (32 columns
+    // from c * 32 on).
+    const auto mask = [&](const TileMeta &tm, int c, uint32_t (&s)[32]) {
+      const int at_c = beg + j * kPos + c * 32, from = row_lo - at_c, to = row_hi - at_c;
+      unsigned seen = tm.valid[c];
+      seen &= from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+      seen &= to <= 0 ? 0u : to >= 32 ? ~0u : ~(~0u << to);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1 ? s[i] : 0xFF800000u;
-          const unsigned bad = tm.poison[c] & seen;
-          if (bad) {
+      for (int i = 0; i < 32; ++i) s[i] = (seen >> i) & 1 ? s[i] : 0xFF800000u;
+      const unsigned bad = tm.poison[c] & seen;
+      if (bad) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = (bad >> i) & 1 ? 0x7FFFFFFFu : s[i];
-          }
-        };
-        // a score's factor (never 0, so that -inf stays -inf)
-        const auto factor = [&](int ek) { return fmaxf(row_factor * pow2i(ek), 0x1p-100f); };
-
-        // The row's largest exponent.  P of the first half of the scores goes over them, so
-        // they stay in registers; those of the second half (columns that P leaves alone)
-        // are read again: 128 registers of scores spill (1173 us against 1162).
-        uint32_t s[4][32];
-        float f[4];
-        int ev[4];
-        unsigned wide[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          f[c] = factor(tm.ek[c]);
-          ev[c] = tm.ev[c];
-          wide[c] = ANY ? tm.wide[c] : 0;
-        }
-        float now = m, nothing = -INFINITY;  // nothing: the largest score of a position without a value
-        const auto maximum = [&](int c, const uint32_t (&s)[32]) {
-          float mx = -INFINITY;
-          if (!ANY || wide[c] == 0) {
-            float t[4];  // four chains
-#pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[i]);
-#pragma unroll
-            for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[i]));
-            mx = fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float x = __uint_as_float(s[i]) * f[c], e = tm.pos_ev[c * 32 + i];
-              mx = fmaxf(mx, x + e);
-              if (e == -INFINITY) nothing = fmaxf(nothing, x);
-            }
-          }
-          now = fmaxf(now, mx);
-        };
-        const auto arrived = [&](int c) {
-          tmem_ld_wait();
-          tie(s[c]);
-          if (__builtin_expect(!full, 0)) mask(c, s[c]);
-        };
-        tmem_ld32(s_at + 2 * 32, s[2]);
-        arrived(2);
-        tmem_ld32(s_at + 3 * 32, s[3]);
-        maximum(2, s[2]);
-        arrived(3);
-        tmem_ld32(s_at, s[0]);
-        maximum(3, s[3]);
-        arrived(0);
-        tmem_ld32(s_at + 32, s[1]);
-        maximum(0, s[0]);
-        arrived(1);
-        maximum(1, s[1]);
-        if (__any_sync(~0u, now > m + kGrowth || (ANY && nothing > m_l + kLead))) {
-          // a new reference: what was summed under the old one is scaled down
-          const bool grew = now > m + kGrowth;
-          const float a = grew ? exp2_approx(m - now) : 1.0f;
-          if (grew) m = now;
-          if constexpr (ANY) {
-            const float most = fmaxf(fmaxf(m, m_l), nothing > m_l + kLead ? nothing : m_l);
-            if (most > m_l) {
-              l *= exp2_approx(m_l - most);
-              m_l = most;
-            }
-            to_l = m == -INFINITY ? 0.0f : exp2_approx(m - m_l);
-          } else {
-            l *= a;
-          }
-          if (j > 0) {
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t o[16];
-              tmem_ld16(o_at + k * 16, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st16(o_at + k * 16, o);
-            }
-          }
-        }
-        // P = 2^(s + ev - m + bias), over S
-        {
-          const float z = kPBias - (m == -INFINITY ? 0.0f : m);
-          const auto probabilities = [&](int k, const uint32_t (&s)[32], float f, int ev, unsigned wide) {
-            uint32_t o[16];
-            float sum;
-            if (!ANY || wide == 0) {
-              const float g = (float)ev + z;
-              const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
-              uint64_t sum2[2] = {0, 0};
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
-                const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
-                sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
-                o[i] = half2_of(a, e);
-              }
-              sum2[0] = f32x2_add(sum2[0], sum2[1]);
-              sum = (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * (ANY ? pow2i(-ev) * to_l : pow2i(-ev));
-            } else {
-              // an exponent for each position; l counts P without it
-              sum = 0.0f;
-              const float z_l = kPBias - (m_l == -INFINITY ? 0.0f : m_l);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float e0 = tm.pos_ev[k * 32 + 2 * i], e1 = tm.pos_ev[k * 32 + 2 * i + 1];
-                const float a = exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, e0 + z));
-                const float e = exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, e1 + z));
-                sum += exp2_approx(fmaf(__uint_as_float(s[2 * i]), f, z_l)) +
-                       exp2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, z_l));
-                o[i] = half2_of(a, e);
-              }
-            }
-            l += sum;
-            tmem_st16(s_at + k * 16, o);
-          };
-          tmem_ld32(s_at + 2 * 32, s[2]);
-          probabilities(0, s[0], f[0], ev[0], wide[0]);
-          probabilities(1, s[1], f[1], ev[1], wide[1]);
-          arrived(2);
-          tmem_ld32(s_at + 3 * 32, s[3]);
-          tmem_st_wait();  // the first half of P: its products start
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.p_half[half]);
-          probabilities(2, s[2], f[2], ev[2], wide[2]);
-          arrived(3);
-          probabilities(3, s[3], f[3], ev[3], wide[3]);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[half]);
+        for (int i = 0; i < 32; ++i) s[i] = (bad >> i) & 1 ? 0x7FFFFFFFu : s[i];
       }
     };
-    tiles(std::false_type{});
+    // a score's factor (never 0, so that -inf stays -inf)
+    const auto factor = [&](int ek) { return fmaxf(row_factor * pow2i(ek), 0x1p-100f); };
+    const auto rescale = [&](float a) {  // O under a new reference
+      if (j == 0) return;
+#pragma unroll 1
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t o[16];
+        tmem_ld16(o_at + k * 16, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+        tmem_st16(o_at + k * 16, o);
+      }
+    };
+    const auto hand_over = [&](uint64_t *bar) {  // P up to here
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+
+    // Up to the first tile that is wide: m_v is 0 and m_l is m.
+    for (; j < n; ++j) {
+      if (!arrives()) break;
+      const TileMeta &tm = sh.meta[j % kMetaSlots];
+      if (tm.wide) break;
+      const int j0 = beg + j * kPos;
+      const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
+                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
+                        (tm.poison[0] | tm.poison[1] | tm.poison[2] | tm.poison[3]) == 0;
+      // The row's largest exponent.  P of the first half of the scores goes over them, so
+      // they stay in registers; those of the second half (columns that P leaves alone)
+      // are read again: 128 registers of scores spill (1173 us against 1162).
+      uint32_t s[4][32];
+      float f[4];
+      int ev[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f[c] = factor(tm.ek[c]);
+        ev[c] = tm.ev[c];
+      }
+      float now = m;
+      const auto maximum = [&](int c, const uint32_t (&s)[32]) {
+        float t[4];  // four chains
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[i]);
+#pragma unroll
+        for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[i]));
+        now = fmaxf(now, fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]));
+      };
+      const auto arrived = [&](int c) {
+        tmem_ld_wait();
+        tie(s[c]);
+        if (__builtin_expect(!full, 0)) mask(tm, c, s[c]);
+      };
+      tmem_ld32(s_at + 2 * 32, s[2]);
+      arrived(2);
+      tmem_ld32(s_at + 3 * 32, s[3]);
+      maximum(2, s[2]);
+      arrived(3);
+      tmem_ld32(s_at, s[0]);
+      maximum(3, s[3]);
+      arrived(0);
+      tmem_ld32(s_at + 32, s[1]);
+      maximum(0, s[0]);
+      arrived(1);
+      maximum(1, s[1]);
+      if (__any_sync(~0u, now > m + kGrowth)) {
+        // a new reference: what was summed under the old one is scaled down
+        const bool grew = now > m + kGrowth;
+        const float a = grew ? exp2_approx(m - now) : 1.0f;
+        if (grew) m = now;
+        l *= a;
+        rescale(a);
+      }
+      // P = 2^(s + ev - m + bias), over S
+      const float z = kPBias - (m == -INFINITY ? 0.0f : m);
+      const auto probabilities = [&](int k, const uint32_t (&s)[32]) {
+        const float g = (float)ev[k] + z;
+        const uint64_t f2 = f32x2_pack(f[k], f[k]), g2 = f32x2_pack(g, g);
+        uint64_t sum2[2] = {0, 0};
+        uint32_t o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
+          const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
+          sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
+          o[i] = half2_of(a, e);
+        }
+        sum2[0] = f32x2_add(sum2[0], sum2[1]);
+        l += (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * pow2i(-ev[k]);
+        tmem_st16(s_at + k * 16, o);
+      };
+      tmem_ld32(s_at + 2 * 32, s[2]);
+      probabilities(0, s[0]);
+      probabilities(1, s[1]);
+      arrived(2);
+      tmem_ld32(s_at + 3 * 32, s[3]);
+      hand_over(&sh.p_half[half]);  // the first half of P: its products start
+      probabilities(2, s[2]);
+      arrived(3);
+      probabilities(3, s[3]);
+      hand_over(&sh.p_full[half]);
+    }
+    // From there on each position has its own exponents, and differences of scores, which are
+    // exact near the maximum, are taken before the exponents of the values are added.  Such
+    // tiles are rare: a loop of its own, with few registers (as a case of the one above it
+    // cost that one 1342 us against 1169 at 8192 x 16384, 28 heads over 4 of 128).
     m_l = m;
-    if (j < n && __all_sync(~0u, ok)) {
-      to_l = m == -INFINITY ? 0.0f : 1.0f;
-      tiles(std::true_type{});
+    for (; j < n && __all_sync(~0u, ok); ++j) {
+      if (!arrives()) break;
+      const TileMeta &tm = sh.meta[j % kMetaSlots];
+      uint32_t s[32];
+      const auto scores = [&](int c) {
+        tmem_ld32(s_at + c * 32, s);
+        tmem_ld_wait();
+        tie(s);
+        mask(tm, c, s);
+      };
+      // position i's score, and the exponent of its value
+      const auto single = [&](uint32_t s, int i, float &x, float &e) {
+        x = __fmul_rn(__uint_as_float(s), factor(tm.pos_ek[i]));  // rounded, wherever it is used
+        e = tm.pos_ev[i] == kNoValue ? -INFINITY : (float)tm.pos_ev[i];
+      };
+      float now = m, now_v = m_v, top = m_l;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        scores(c);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float x, e;
+          single(s[i], c * 32 + i, x, e);
+          if ((x - now) + (e - now_v) > 0.0f) now = x, now_v = e;
+          top = fmaxf(top, x);
+        }
+      }
+      const float by = (now - m) + (now_v - m_v);
+      if (top - m_l > kLead) {
+        l *= exp2_approx(m_l - top);
+        m_l = top;
+      }
+      if (__any_sync(~0u, by > kGrowth)) {
+        const float a = by > kGrowth ? exp2_approx(-by) : 1.0f;
+        if (by > kGrowth) m = now, m_v = now_v;
+        rescale(a);
+      }
+      const float m_0 = m == -INFINITY ? 0.0f : m, l_0 = m_l == -INFINITY ? 0.0f : m_l;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        scores(c);
+        uint32_t o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float x0, x1, e0, e1;
+          single(s[2 * i], c * 32 + 2 * i, x0, e0);
+          single(s[2 * i + 1], c * 32 + 2 * i + 1, x1, e1);
+          l += exp2_approx((x0 - l_0) + kPBias) + exp2_approx((x1 - l_0) + kPBias);
+          o[i] = half2_of(exp2_approx((x0 - m_0) + (e0 - m_v + kPBias)), exp2_approx((x1 - m_0) + (e1 - m_v + kPBias)));
+        }
+        tmem_st16(s_at + c * 16, o);
+        if (c & 1) hand_over(c == 1 ? &sh.p_half[half] : &sh.p_full[half]);
+      }
     }
     if (__all_sync(~0u, ok)) ok = mbar_wait(&sh.o_full[half], 0, abort_flag);
     if (__all_sync(~0u, ok)) {
       tc_fence_after();
-      // 2^(m - m_l) goes on in two halves: it can be below binary32's range where its product with O is not
-      const float half_to = m == -INFINITY ? 0.0f : exp2_approx(0.5f * (m - m_l));
+      // 2^(m + m_v - m_l) goes on in two halves: it can be below binary32's range where its product with O is not
+      const float half_to = m == -INFINITY ? 0.0f : exp2_approx(0.5f * ((m - m_l) + m_v));
       const float inv = l == 0.0f ? 0.0f : half_to / l;
       const auto out = [&](uint32_t x) { return (__uint_as_float(x) * half_to) * inv; };
       uint16_t *dst = p.out + (int64_t)(sq.first + r / p.G) * p.ldo + (int64_t)(h * p.G + r % p.G) * D;
