@@ -30,7 +30,8 @@
 // rescaled only where a row's maximum grew by more than 2^6 since its reference;
 // P stays below 2^14.  Positions whose value scale is 0 do not raise that
 // reference (they would push P of the others out of float16): they count in the
-// sum of the row alone, which for that has a reference of its own.
+// sum of the row alone, which for that has a reference of its own.  Scores too large
+// for a reference in binary32 to be exact enough go the same rare way as wide units.
 #include <algorithm>
 
 #include "attn.cuh"
@@ -53,20 +54,23 @@ constexpr int kMetaSlots = 4;
 constexpr float kPBias = 8.0f;  // P is 2^8 p: float16's subnormals lie below 2^-22 p
 constexpr float kGrowth = 6.0f;
 constexpr float kLead = 32.0f;  // a score may pass the sum's reference by 2^this where O has another
+constexpr float kHuge = 0x1p22f;  // scores up to here have a reference good to 2^-2, below 2^(P's bound)
 constexpr int kValueUp = 5;     // a value's scale becomes 2^5..2^6 (times at most 448: below float16's 65504)
 constexpr int kValueSpan = 8;   // scales of a unit within 2^8 share an exponent: E4M3's 2^-9 stays normal
 constexpr int kKeySpan = 14;    // key scales within 2^14: a code of 1 stays normal
+constexpr int kWide = 127;      // in TileMeta::most
 constexpr int kNoValue = -128;  // in pos_ev, of a position whose value scale is 0
 
 // What the softmax needs of a position tile beside S, per 32 positions: the
 // exponents of keys and values, positions present, positions whose value is not
 // finite (zero in the tile, so that P = 0 leaves it alone); and for the general loop exponents of
-// each position.  `wide`: some unit's scales lie too far apart for one exponent.
+// each position.  `most` is the largest ek, or kWide where some unit's scales lie too far apart
+// for one exponent.
 struct __align__(16) TileMeta {
   int ek[4], ev[4];
   unsigned valid[4], poison[4];
   signed char pos_ek[kPos], pos_ev[kPos];
-  int wide;
+  int most;
 };
 
 template <int D>
@@ -215,8 +219,12 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits, D == 128 ? 4 : 7) k_at
 #pragma unroll
   for (int i = 0; i < kWords; ++i) nothing |= value && ((valid[i] >> lane) & 1) && (scale[i] & 0x7FFFu) == 0;
   const bool wide = __any_sync(~0u, nothing) || span > (value ? kValueSpan : kKeySpan);
-  const int tile_wide = __syncthreads_or(wide);
-  if (threadIdx.x == 0) tm.wide = tile_wide;
+  __shared__ int s_most;
+  if (threadIdx.x == 0) s_most = -kWide;
+  __syncthreads();
+  if (lane == 0 && (wide || !value)) atomicMax(&s_most, wide ? kWide : e);
+  __syncthreads();
+  if (threadIdx.x == 0) tm.most = s_most;
 
   if (!value) {
     if (lane < kWords) {
@@ -400,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
 
   // q rows -> float16 in shared memory, by the softmax threads
   float row_factor = 0.0f;
+  bool some = false;  // something but zeros
   const int r = r0 + threadIdx.x;  // a softmax thread's row
   if (warp < kSoftmaxWarps) {
     uint4 w[D / 8];
@@ -417,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     // a negative softmax scale turns q around, so that the score's factor is positive
     const float up = p.scale_log2 < 0.0f ? -pow2i(14 - e) : pow2i(14 - e);
     row_factor = fabsf(p.scale_log2) * pow2i(max(e - 14, -126));
+    some = top > 0.0f && row_factor > 0.0f;
     const uint32_t at = smem_u32(smem) + (warp >> 2) * C::kQBytes;
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) {
@@ -448,6 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     float m = -INFINITY, m_v = 0.0f, m_l = -INFINITY, l = 0.0f;
     bool ok = true;
     int j = 0;
+    // Keys whose exponent passes this may give scores beyond kHuge, whose reference is rounded by
+    // more than P in float16 can bear: |S| is below 2^15 * 254 * D.  (Rows of zeros have factor 1.)
+    const int ek_most = __reduce_min_sync(
+        ~0u, some ? (int)fminf(floorf(log2f(kHuge / (0x1p15f * 254.0f * D)) - log2f(row_factor)), kWide - 1.0f) : kWide - 1);
     const auto arrives = [&] {  // S of tile j, with its metadata
       ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
            mbar_wait(&sh.s_full[half], j & 1, abort_flag);
@@ -490,11 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       if (lane == 0) mbar_arrive(bar);
     };
 
-    // Up to the first tile that is wide: m_v is 0 and m_l is m.
+    // Up to the first tile that passes ek_most: m_v is 0 and m_l is m.
     for (; j < n; ++j) {
       if (!arrives()) break;
       const TileMeta &tm = sh.meta[j % kMetaSlots];
-      if (tm.wide) break;
+      if (tm.most > ek_most) break;
       const int j0 = beg + j * kPos;
       const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
                         (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&

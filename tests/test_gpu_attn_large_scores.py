@@ -15,7 +15,7 @@ def capi():
     return c
 
 
-MANY = []
+MANY = [(D, 200, 400) for D in (64, 128)]
 FEW = [(D, nq, 400) for D in (32, 64, 128, 256) for nq in (1, 4)]
 
 
