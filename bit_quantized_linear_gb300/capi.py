@@ -242,26 +242,21 @@ def qlin_kv_load_mixed(slots, k_cache, k_scale, v_cache, v_scale, k_out, v_out, 
 
 
 # The C entry points see addresses: what a tensor's type, size or strides would make them misread, the functions
-# below refuse.  (An index array of another type, or a slice of a wider table, is read as other numbers.)
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+# below refuse.  (An index array of another type, or a slice of a wider table, is read as other numbers.)  Arrays that
+# are read whole are told by their bytes, a cheaper question than type and count.
+_BF16 = torch.bfloat16
 
 
-def _dense(t, dtype, size: int, what: str):
-    """t: contiguous, of `size` elements of dtype."""
-    if t.dtype is not dtype or t.numel() != size or not t.is_contiguous():
-        raise ValueError(f"{what}: {size} contiguous elements of {dtype}, not {t.dtype} {tuple(t.shape)} with strides "
-                         f"{t.stride()}")
-
-
-def _bytes(t, size: int, what: str):
-    """t: contiguous, of `size` bytes (codes and scales, whatever type they are held as)."""
-    if t.nbytes != size or not t.is_contiguous():
-        raise ValueError(f"{what}: {size} contiguous bytes, not {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+def _refuse(**arrays):
+    """What an array (tensor, bytes) should have been."""
+    said = "; ".join(f"{k}: {n} contiguous bytes, not {t.dtype} {tuple(t.shape)} with strides {t.stride()}"
+                     for k, (t, n) in arrays.items() if t.nbytes != n or not t.is_contiguous())
+    raise ValueError(said or ", ".join(f"{k}: BF16, not {t.dtype}" for k, (t, _) in arrays.items()))
 
 
 def _rows(t, rows: int, least: int, what: str) -> int:
     """Row stride (elements) of BF16 rows of `least` elements or more."""
-    if t.dtype is _BF16 and t.dim() == 2:
+    if t.dtype is _BF16:
         (m, n), (row, one) = t.shape, t.stride()
         if m == rows and n >= least and one == 1:
             return row if row >= least or m > 1 else least  # a single row's is whatever its tensor says
@@ -273,42 +268,47 @@ def _mixed_cache(k_cache, k_scale, v_cache, v_scale):
     """Slots, heads and head size of the four arrays of kv_cache_alloc()."""
     S, H, D = k_cache.shape
     n = S * H
-    _bytes(k_cache, n * D, "k_cache")
-    _bytes(k_scale, n * (D // 32) * 2, "k_scale")
-    _bytes(v_cache, n * D, "v_cache")
-    _bytes(v_scale, n * 2, "v_scale")
+    if (k_cache.nbytes != n * D or k_scale.nbytes != D // 32 * 2 * n or v_cache.nbytes != n * D
+            or v_scale.nbytes != 2 * n or not (k_cache.is_contiguous() and k_scale.is_contiguous()
+                                               and v_cache.is_contiguous() and v_scale.is_contiguous())):
+        _refuse(k_cache=(k_cache, n * D), k_scale=(k_scale, D // 32 * 2 * n), v_cache=(v_cache, n * D),
+                v_scale=(v_scale, 2 * n))
     return S, H, D
 
 
-def _norm_inputs(x, residual, weight, h_out):
-    M, K = x.shape
-    _dense(weight, _BF16, K, "weight")
-    if h_out is not None:
-        _dense(h_out, _BF16, M * K, "h_out")
-    return _rows(x, M, K, "x"), 0 if residual is None else _rows(residual, M, K, "residual")
+def _norm_arrays(M: int, K: int, weight, h_out):
+    if weight.dtype is not _BF16 or weight.nbytes != 2 * K or not weight.is_contiguous():
+        _refuse(weight=(weight, 2 * K))
+    if h_out is not None and (h_out.dtype is not _BF16 or h_out.nbytes != 2 * M * K or not h_out.is_contiguous()):
+        _refuse(h_out=(h_out, 2 * M * K))
 
 
 def qlin_rmsnorm(x, residual, weight, eps: float, h_out, y_out, stream=None):
     """x, residual (or None) BF16 [M, K] rows; h_out (with a residual) and y_out BF16 [M, K]."""
     M, K = x.shape
-    ldx, ldr = _norm_inputs(x, residual, weight, h_out)
-    _dense(y_out, _BF16, M * K, "y_out")
-    _check(_lib.qlin_rmsnorm(M, K, _p(x), ldx, _p(residual), ldr, _p(weight), eps, _p(h_out), _p(y_out),
-                             _stream(stream)), "qlin_rmsnorm")
+    _norm_arrays(M, K, weight, h_out)
+    if y_out.dtype is not _BF16 or y_out.nbytes != 2 * M * K or not y_out.is_contiguous():
+        _refuse(y_out=(y_out, 2 * M * K))
+    _check(_lib.qlin_rmsnorm(M, K, _p(x), _rows(x, M, K, "x"), _p(residual),
+                             0 if residual is None else _rows(residual, M, K, "residual"), _p(weight), eps, _p(h_out),
+                             _p(y_out), _stream(stream)), "qlin_rmsnorm")
 
 
 def qlin_rmsnorm_quant(qtype, x, residual, weight, eps: float, input_scale, h_out, qx, x_scale, stream=None):
     """As qlin_rmsnorm with 1-byte codes qx [M, K]: under input_scale [1] (x_scale None), or per-token
     scales written to x_scale [M] (input_scale None)."""
     M, K = x.shape
-    ldx, ldr = _norm_inputs(x, residual, weight, h_out)
-    _bytes(qx, M * K, "qx")
-    if input_scale is not None:
-        _dense(input_scale, _F32, 1, "input_scale")
-    if x_scale is not None:
-        _dense(x_scale, _F32, M, "x_scale")
-    _check(_lib.qlin_rmsnorm_quant(_qt(qtype), M, K, _p(x), ldx, _p(residual), ldr, _p(weight), eps, _p(input_scale),
-                                   _p(h_out), _p(qx), _p(x_scale), _stream(stream)), "qlin_rmsnorm_quant")
+    _norm_arrays(M, K, weight, h_out)
+    if qx.nbytes != M * K or not qx.is_contiguous():
+        _refuse(qx=(qx, M * K))
+    if input_scale is not None and input_scale.nbytes != 4:
+        _refuse(input_scale=(input_scale, 4))
+    if x_scale is not None and (x_scale.nbytes != 4 * M or not x_scale.is_contiguous()):
+        _refuse(x_scale=(x_scale, 4 * M))
+    _check(_lib.qlin_rmsnorm_quant(_qt(qtype), M, K, _p(x), _rows(x, M, K, "x"), _p(residual),
+                                   0 if residual is None else _rows(residual, M, K, "residual"), _p(weight), eps,
+                                   _p(input_scale), _p(h_out), _p(qx), _p(x_scale), _stream(stream)),
+           "qlin_rmsnorm_quant")
 
 
 def qlin_w8a8_linear_codes(qtype, qx, x_scale, qw, w_scale, bias, y, ws=None, stream=None):
@@ -316,14 +316,14 @@ def qlin_w8a8_linear_codes(qtype, qx, x_scale, qw, w_scale, bias, y, ws=None, st
     row's one scale is both)."""
     M, K = qx.shape
     N = qw.shape[0]
-    scales = x_scale.numel()
-    _dense(x_scale, _F32, scales if scales == 1 else M, "x_scale (one value, or one a row)")
-    _bytes(qx, M * K, "qx")
-    _bytes(qw, N * K, "qw")
-    _dense(w_scale, _F32, N, "w_scale")
-    _dense(y, _BF16, M * N, "y")
-    if bias is not None:
-        _dense(bias, _BF16, N, "bias")
+    scales = x_scale.numel()  # one value, or one a row
+    if (x_scale.nbytes != 4 * (1 if scales == 1 else M) or qx.nbytes != M * K or qw.nbytes != N * K
+            or w_scale.nbytes != 4 * N or y.dtype is not _BF16 or y.nbytes != 2 * M * N
+            or not (x_scale.is_contiguous() and qx.is_contiguous() and qw.is_contiguous() and w_scale.is_contiguous()
+                    and y.is_contiguous())):
+        _refuse(x_scale=(x_scale, 4 * M), qx=(qx, M * K), qw=(qw, N * K), w_scale=(w_scale, 4 * N), y=(y, 2 * M * N))
+    if bias is not None and (bias.dtype is not _BF16 or bias.nbytes != 2 * N or not bias.is_contiguous()):
+        _refuse(bias=(bias, 2 * N))
     wp, wb = _ws(ws)
     _check(_lib.qlin_w8a8_linear_codes(_qt(qtype), M, K, N, _p(qx), _p(x_scale), int(scales > 1), _p(qw),
                                        _p(w_scale), _p(bias), _p(y), wp, wb, _stream(stream)),
@@ -334,7 +334,8 @@ def qlin_rope_table(table, theta: float, scaling="plain", factor: float = 1.0, o
                     beta_fast: float = 32.0, beta_slow: float = 1.0, amplitude: float = 1.0, stream=None):
     """Fills table, fp32 [max_pos, rot]."""
     max_pos, rot = table.shape
-    _dense(table, _F32, max_pos * rot, "table")
+    if table.nbytes != 4 * max_pos * rot or not table.is_contiguous():
+        _refuse(table=(table, 4 * max_pos * rot))
     _check(_lib.qlin_rope_table(max_pos, rot, theta, ROPE_SCALINGS[scaling], factor, original_context, beta_fast,
                                 beta_slow, amplitude, _p(table), _stream(stream)), "qlin_rope_table")
 
@@ -344,9 +345,10 @@ def _turns(table, rot: int, positions):
     max_pos, turned = table.shape
     if turned != rot:
         raise ValueError(f"the table turns {turned} dimensions, not {rot}")
-    _dense(table, _F32, max_pos * rot, "table")
     T = positions.shape[0]
-    _dense(positions, _I64, T, "positions")
+    if (table.nbytes != 4 * max_pos * rot or positions.nbytes != 8 * T
+            or not (table.is_contiguous() and positions.is_contiguous())):
+        _refuse(table=(table, 4 * max_pos * rot), positions=(positions, 8 * T))
     return T, max_pos
 
 
@@ -366,7 +368,8 @@ def qlin_rope_kv_store_mixed(layout, Hq: int, rot: int, table, positions, q, k, 
     T, max_pos = _turns(table, rot, positions)
     S, H, D = _mixed_cache(k_cache, k_scale, v_cache, v_scale)
     n, m = Hq * D, H * D
-    _dense(slots, _I64, T, "slots")
+    if slots.nbytes != 8 * T or not slots.is_contiguous():
+        _refuse(slots=(slots, 8 * T))
     _check(_lib.qlin_rope_kv_store_mixed(ROPE_LAYOUTS[layout], T, Hq, H, D, rot, _p(table), max_pos, _p(positions),
                                          _p(q), _rows(q, T, n, "q"), _p(k), _rows(k, T, m, "k"), _p(v),
                                          _rows(v, T, m, "v"), _p(q_out), _rows(q_out, T, n, "q_out"), _p(slots), S,
@@ -382,9 +385,9 @@ def qlin_attn_mixed(q, q_start, kv_len, block_table, block_size: int, k_cache, k
     B, blocks = kv_len.shape[0], block_table.shape[1]
     if n % D:
         raise ValueError(f"rows of q hold {n} elements, not heads of {D}")
-    _dense(q_start, _I32, B + 1, "q_start")
-    _dense(kv_len, _I32, B, "kv_len")
-    _dense(block_table, _I32, B * blocks, "block_table")
+    if (q_start.nbytes != 4 * (B + 1) or kv_len.nbytes != 4 * B or block_table.nbytes != 4 * B * blocks
+            or not (q_start.is_contiguous() and kv_len.is_contiguous() and block_table.is_contiguous())):
+        _refuse(q_start=(q_start, 4 * (B + 1)), kv_len=(kv_len, 4 * B), block_table=(block_table, 4 * B * blocks))
     wp, wb = _ws(ws)
     _check(_lib.qlin_attn_mixed(B, T, n // D, H, D, _p(q), _rows(q, T, n, "q"), _p(q_start), max_q, _p(kv_len), max_kv,
                                 _p(block_table), blocks, block_size, S, _p(k_cache), _p(k_scale), _p(v_cache),
