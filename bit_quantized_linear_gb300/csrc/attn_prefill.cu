@@ -139,7 +139,7 @@ __device__ __forceinline__ float half_at(uint32_t w, int i) {
 // of values.  A lane holds the codes of 16 dimensions (chunk lane % C) of positions
 // 8 * (lane / C) + i.
 template <int D>
-__global__ void __launch_bounds__(64 * Config<D>::kUnits, D == 128 ? 4 : 7) k_attn_unpack(const PrefillParams p) {
+__global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const PrefillParams p) {
   using C = Config<D>;
   constexpr int kWords = C::kUnit / 32;  // 32-position words of a unit
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -219,12 +219,15 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits, D == 128 ? 4 : 7) k_at
 #pragma unroll
   for (int i = 0; i < kWords; ++i) nothing |= value && ((valid[i] >> lane) & 1) && (scale[i] & 0x7FFFu) == 0;
   const bool wide = __any_sync(~0u, nothing) || span > (value ? kValueSpan : kKeySpan);
-  __shared__ int s_most;
-  if (threadIdx.x == 0) s_most = -kWide;
+  __shared__ int s_most[2 * C::kUnits];
+  if (lane == 0) s_most[warp] = wide ? kWide : value ? -kWide : e;
   __syncthreads();
-  if (lane == 0 && (wide || !value)) atomicMax(&s_most, wide ? kWide : e);
-  __syncthreads();
-  if (threadIdx.x == 0) tm.most = s_most;
+  if (threadIdx.x == 0) {
+    int most = s_most[0];
+#pragma unroll
+    for (int i = 1; i < 2 * C::kUnits; ++i) most = max(most, s_most[i]);
+    tm.most = most;
+  }
 
   if (!value) {
     if (lane < kWords) {

@@ -730,8 +730,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas)
 // few: a warp per row.
 constexpr int kFewParts = 16;
 constexpr int kManyWarps = 16, kFewWarps = 8;  // warps of a CTA
-template <int D, bool MANY>
-__global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps))
+template <int D, bool MANY, int CTAS>
+__global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps), CTAS)
     k_attn_join(const AttnDev p, const AttnParts parts, bool many) {
   const int rows = parts.rows;
   constexpr int V = D / 32;                  // floats of a lane
@@ -841,9 +841,13 @@ template <int D>
 cudaError_t launch_join_d(const AttnDev &p, const AttnParts &parts, bool many, cudaStream_t st) {
   const int64_t rows = (int64_t)p.B * p.H * parts.row_tiles * parts.rows;
   if (parts.splits <= kFewParts)
-    return launch_kernel(k_attn_join<D, false>, dim3((unsigned)((rows + kFewWarps - 1) / kFewWarps)),
+    return launch_kernel(k_attn_join<D, false, 1>, dim3((unsigned)((rows + kFewWarps - 1) / kFewWarps)),
                          dim3(32 * kFewWarps), 0, st, 1, p, parts, many);
-  return launch_kernel(k_attn_join<D, true>, dim3((unsigned)rows), dim3(32 * kManyWarps), 0, st, 1, p, parts, many);
+  // Rows for one CTA a multiprocessor at most: registers for all loads of a batch at once (one context of
+  // 32768: 14.4 us, 15.2 with two CTAs' registers).  More: two CTAs (168 rows over 8192: 32.7 us, 34.1 with one).
+  constexpr int kTwo = D <= 128 ? 2 : 1;
+  return launch_kernel(rows > sm_count() ? k_attn_join<D, true, kTwo> : k_attn_join<D, true, 1>, dim3((unsigned)rows),
+                       dim3(32 * kManyWarps), 0, st, 1, p, parts, many);
 }
 template <int D>
 cudaError_t launch_d(const SplitParams &p, int rows, int64_t units, cudaStream_t st) {
