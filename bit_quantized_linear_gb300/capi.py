@@ -381,8 +381,7 @@ def qlin_attn_mixed(q, q_start, kv_len, block_table, block_size: int, k_cache, k
                     max_kv: int, scale: float, causal: bool, window: int, out, ws=None, stream=None):
     """q, out BF16 [T, Hq*D] rows; q_start int32 [B+1]; kv_len int32 [B]; block_table int32 [B, max_blocks]."""
     S, H, D = _mixed_cache(k_cache, k_scale, v_cache, v_scale)
-    T, n = q.shape
-    B, blocks = kv_len.shape[0], block_table.shape[1]
+    (T, n), (B, blocks) = q.shape, block_table.shape
     if n % D:
         raise ValueError(f"rows of q hold {n} elements, not heads of {D}")
     if (q_start.nbytes != 4 * (B + 1) or kv_len.nbytes != 4 * B or block_table.nbytes != 4 * B * blocks
@@ -568,12 +567,11 @@ def rope_table(max_pos: int, rot: int, theta: float = 10000.0, device=None, **sc
 def attn_mixed(q, q_start, kv_len, block_table, block_size: int, cache, max_q: int, max_kv: int, scale=None,
                causal: bool = True, window: int = 0, out=None, ws=None):
     """Attention of q over a mixed cache (the four arrays of kv_cache_alloc()); scale defaults to D^-1/2."""
-    D = cache[0].shape[2]
+    _, H, D = cache[0].shape
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if ws is None:
-        n = qlin_attn_mixed_workspace_bytes(kv_len.shape[0], q.shape[1] // D, cache[0].shape[1], D, max_q, max_kv,
-                                            window)
+        n = qlin_attn_mixed_workspace_bytes(kv_len.shape[0], q.shape[1] // D, H, D, max_q, max_kv, window)
         if 0 < n < 2 ** 63:  # invalid sizes are the call's to report
             ws = torch.empty(n, dtype=torch.uint8, device=q.device)
     qlin_attn_mixed(q, q_start, kv_len, block_table, block_size, *cache, max_q, max_kv,
