@@ -844,7 +844,8 @@ cudaError_t launch_join_d(const AttnDev &p, const AttnParts &parts, bool many, c
     return launch_kernel(k_attn_join<D, false, 1>, dim3((unsigned)((rows + kFewWarps - 1) / kFewWarps)),
                          dim3(32 * kFewWarps), 0, st, 1, p, parts, many);
   // Rows for one CTA a multiprocessor at most: registers for all loads of a batch at once (one context of
-  // 32768: 14.4 us, 15.2 with two CTAs' registers).  More: two CTAs (168 rows over 8192: 32.7 us, 34.1 with one).
+  // 32768: 14.4 us, 15.2 with two CTAs' registers).  More: two CTAs (168 rows over 8192: 30.6 us; 34.1 against
+  // 32.7 before the unpacking ahead of it had all its registers).
   constexpr int kTwo = D <= 128 ? 2 : 1;
   return launch_kernel(rows > sm_count() ? k_attn_join<D, true, kTwo> : k_attn_join<D, true, 1>, dim3((unsigned)rows),
                        dim3(32 * kManyWarps), 0, st, 1, p, parts, many);

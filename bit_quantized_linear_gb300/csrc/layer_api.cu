@@ -59,13 +59,14 @@ qlin_status check_attn_sizes(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_
 // sees at most, the split kernel reads all of u once for every 16 rows: 8 us and, of a
 // ragged batch, 4.3e-5 us (head size 64: 2.9e-5) for each (16 rows, unit of u).  The tcgen05
 // kernels unpack u once: 22 us and 3e-4 us a unit, whatever the rows.  The limit is where
-// the two meet; a lone sequence has no second kernel to launch, and no raggedness.
+// the two meet; a lone sequence has no second kernel to launch, and no raggedness: its limit
+// falls with 1 / u from 512 rows, and at u = 32768 the tcgen05 kernels lead from 84 rows on.
 // Beyond it they take those sequences of the batch that have more than kFewRows rows,
 // and the split kernel the others; each leaves the other's sequences.  Measured (split and
-// tcgen05, us), one sequence of 28 heads over 4 of 128: 84 rows over 8192 positions 28.2
-// and 25.5, 168 over 8192 43.3 and 30.6, 420 over 2048 32.9 and 23.6.  Batches: 4 x 84 rows
-// over 8192 33.7 and 61.0, 2 x 280 over 4096 46.8 and 33.7, 8 x 196 over 2492 50.2 and 51.4;
-// 8 heads of 128, 4 x 200 over 2048 40.7 and 33.9; of 64, 5 x 333 over 1024 32.8 and 38.5.
+// tcgen05, us), one sequence of 28 heads over 4 of 128: 84 rows over 8192 positions 28.7
+// and 26.3, 168 over 8192 42.5 and 30.6, 420 over 2048 31.8 and 23.6.  Batches: 4 x 84 rows
+// over 8192 33.3 and 60.2, 2 x 280 over 4096 45.9 and 33.4, 8 x 196 over 2492 48.6 and 48.6;
+// 8 heads of 128, 4 x 200 over 2048 40.4 and 33.9; of 64, 5 x 333 over 1024 33.1 and 38.4.
 constexpr int64_t kFewRows = 64;
 int64_t attn_most_split_rows(int64_t B, int64_t H, int64_t D, int64_t max_kv, int64_t window) {
   const int64_t range = window > 0 ? std::min(window, max_kv) : max_kv;

@@ -16,13 +16,14 @@
 //
 // One pass: a row's vectors stay in registers between the sum and the output
 // (and, for per-token scales, between the output's maximum and its codes).  A
-// row is the work of `wpr` warps.  Bound by HBM: x, residual and h_out are 2 bytes an element, the
-// output 1 or 2.  With codes the arithmetic is close behind, so it runs on pairs
-// of elements as packed binary32 operations (the same roundings, lane by lane),
-// and a CTA walks over rows: the weights are unpacked once, and the next row is on
-// its way while this one is worked on (8192 x 2048 static E4M3 with residual:
-// 25.6 us without; 20.9 us, 5.6 TB/s, with it and the residual added as BF16).  BF16 output has arithmetic to spare and gains more from whole rows in
-// flight (32640 x 3584: 146 us walking, 134 not).
+// row is the work of `wpr` warps.  Bound by HBM: x, residual and h_out are 2
+// bytes an element, the output 1 or 2.  With codes the arithmetic is close
+// behind, so it runs on pairs of elements as packed binary32 operations (the
+// same roundings, lane by lane), and a CTA walks over rows: the weights are
+// unpacked once, and the next row is on its way while this one is worked on
+// (8192 x 2048 static E4M3 with residual: 25.6 us without; 21.2 us, 5.5 TB/s,
+// with it and the residual added as BF16).  BF16 output has arithmetic to spare
+// and gains more from whole rows in flight (32640 x 3584: 146 us walking, 134 not).
 #include "common.cuh"
 #include "kernels.h"
 #include "kv_quant.cuh"

@@ -345,6 +345,7 @@ qlin_status qlin_kv_load_mixed(int64_t T, int64_t H, int64_t D, const int64_t *s
  *       qlin_quantize_act_static makes them; x_scale must be NULL;
  *     input_scale NULL: x_scale[m] = max_k |y| / QMAX (1 if that is 0), codes
  *       Q(y / x_scale[m]), as qlin_quantize_act_dynamic makes them.
+ *     A NaN y is E4M3's NaN code, and -127 in INT8; the maximum leaves it out.
  *     qlin_w8a8_linear_codes takes the codes and scales.
  *   x         [M] rows of K BF16, row stride ldx elements (>= K, a multiple of 8).
  *   residual  likewise with ldr, or NULL.
@@ -452,16 +453,20 @@ qlin_status qlin_rope_kv_store_mixed(qlin_rope_layout layout, int64_t T, int64_t
  *              < p + window); 0: no window.
  * A row that sees no position gives +0 (kv_len 0, as in the padding rows of a
  * captured batch; rows before position 0).  What is stored at positions that a
- * row does not see (NaN included) does not reach it; a row that sees a NaN value
- * code has NaN outputs.  Softmax statistics and sums are fp32; P and the scaled
- * keys and values enter the matrix products as float16 (11 significant bits,
- * under exponents of their own, so no value of the cache overflows).
+ * row does not see (codes and scales, NaN and infinities included) does not reach
+ * it; a row that sees a NaN value code has NaN outputs, not in that code's
+ * dimension alone, and one that sees a scale that is not finite has outputs that are
+ * not finite.  Softmax statistics and sums are fp32.  P, which is the weight times the value's scale, enters the matrix products
+ * as float16 (11 significant bits, under an exponent per row); with many rows so do the
+ * keys and values times their scales, under an exponent for each position where those
+ * lie far apart, so no value of the cache overflows.  There a key's groups are
+ * rounded beside its largest one: below 2^-14 of its scale they lose bits.
  * A page outside [0, num_slots / block_size), rows or positions beyond T, max_q,
  * max_kv or max_blocks * block_size break the contract: they are left out and the
  * device status word is set to QLIN_ERR_INVALID_ARG.
  *   ws: qlin_attn_mixed_workspace_bytes(B, Hq, H, D, max_q, max_kv, window)
  *   bytes: partial results where the positions are split over CTAs, and for many
- *   rows the positions as float16 (4 D + 5 bytes for each position of max_kv, kv
+ *   rows the positions as float16 (4 D + 3 bytes for each position of max_kv, kv
  *   head and sequence; beyond about 2 GB the kv heads go in groups, of one at least).
  *   max_q and max_kv bound the launch: tight ones cost less memory and time.
  * Requirements: B >= 0, D 32, 64, 128 or 256, Hq a multiple of H, Hq / H <= 128,
