@@ -726,7 +726,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, Geometry<D, NT>::kCtas)
 }
 
 // Joins the parts of one row: out = sum_s w_s o_s / sum_s w_s with
-// w_s = l_s 2^(m_s - max m).  Many parts: a CTA per row, its warps over the parts;
+// w_s = l_s 2^(m_s - max m), the exponent of l_s joined to the other, which alone can be
+// below binary32's range where w_s is not.  Many parts: a CTA per row, its warps over the parts;
 // few: a warp per row.
 constexpr int kFewParts = 16;
 constexpr int kManyWarps = 16, kFewWarps = 8;  // warps of a CTA
@@ -779,7 +780,9 @@ __global__ void __launch_bounds__(32 * (MANY ? kManyWarps : kFewWarps), CTAS)
   for (int s0 = part; s0 < parts.splits;) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = e[i].y * exp2_approx(e[i].x - z);  // 0 beyond the last part
+      const int k = (int)(__float_as_uint(e[i].y) >> 23);  // 0 beyond the last part, and w with it
+      const float mantissa = e[i].y * __uint_as_float((unsigned)(254 - k) << 23);
+      const float w = mantissa * exp2_approx((e[i].x - z) + (float)(k - 127));
       W += w;
 #pragma unroll
       for (int v = 0; v < V; ++v) o[v] = fmaf(w, __uint_as_float(x[i][v]), o[v]);
