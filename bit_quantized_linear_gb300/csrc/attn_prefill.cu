@@ -54,23 +54,26 @@ constexpr int kMetaSlots = 4;
 constexpr float kPBias = 8.0f;  // P is 2^8 p: float16's subnormals lie below 2^-22 p
 constexpr float kGrowth = 6.0f;
 constexpr float kLead = 32.0f;  // a score may pass the sum's reference by 2^this where O has another
-constexpr float kHuge = 0x1p22f;  // scores up to here have a reference good to 2^-2, below 2^(P's bound)
-constexpr int kValueUp = 5;     // a value's scale becomes 2^5..2^6 (times at most 448: below float16's 65504)
-constexpr int kValueSpan = 8;   // scales of a unit within 2^8 share an exponent: E4M3's 2^-9 stays normal
+constexpr float kHuge = 0x1p24f;  // scores up to here have a reference good to 1/2: P stays below 2^14.5
+constexpr int kValueUp = 6;     // a value's scale becomes 2^6..2^7 (times at most 448: below float16's 65504)
+constexpr int kValueSpan = 11;  // scales of a unit within 2^11 share an exponent: E4M3's 2^-9 stays normal
 constexpr int kKeySpan = 14;    // key scales within 2^14: a code of 1 stays normal
-constexpr int kWide = 127;      // in TileMeta::most
-constexpr int kNoValue = -128;  // in pos_ev, of a position whose value scale is 0
+constexpr int kWide = 1024;     // added to TileMeta::code
 
 // What the softmax needs of a position tile beside S, per 32 positions: the
 // exponents of keys and values, positions present, positions whose value is not
-// finite (zero in the tile, so that P = 0 leaves it alone); and for the general loop exponents of
-// each position.  `most` is the largest ek, or kWide where some unit's scales lie too far apart
-// for one exponent.
+// finite (zero in the tile, so that P = 0 leaves it alone), and (bits of `wide`) whether the
+// scales of keys or values lie too far apart for one exponent.  `code` is the largest ek, and
+// kWide more where something is wide.
 struct __align__(16) TileMeta {
   int ek[4], ev[4];
   unsigned valid[4], poison[4];
-  signed char pos_ek[kPos], pos_ev[kPos];
-  int most;
+  int code;
+  unsigned wide;
+};
+// Of a position of a wide word: 2^ek of its key, and ev of its value (-inf: scale 0).
+struct __align__(8) PositionMeta {
+  float up_k, ev;
 };
 
 template <int D>
@@ -96,6 +99,7 @@ struct Shared {
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2];  // of row tiles A and B
   uint32_t tmem;
   int abort;
+  const PositionMeta *positions;  // of the CTA's first tile (here, since the common loop has no register for it)
   TileMeta meta[kMetaSlots];
 };
 
@@ -129,6 +133,7 @@ struct PrefillParams : AttnDev {
   int chunk;
   uint8_t *images;           // [B, heads, tiles] key and value tile
   TileMeta *meta;            // [B, heads, tiles]
+  PositionMeta *positions;   // [B, heads, tiles, kPos]
 };
 
 __device__ __forceinline__ float half_at(uint32_t w, int i) {
@@ -161,6 +166,7 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
   const int64_t at_tile = ((int64_t)b * p.heads + hh) * p.tiles + tile;
   uint8_t *image = p.images + at_tile * C::kImage + (value ? C::kTileBytes : 0);
   TileMeta &tm = p.meta[at_tile];
+  PositionMeta *pm = p.positions + at_tile * kPos;
 
   // rows (slot, head) of the lane's positions, and which are there
   const int32_t *table = p.block_table + (int64_t)b * p.max_blocks;
@@ -219,14 +225,22 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
 #pragma unroll
   for (int i = 0; i < kWords; ++i) nothing |= value && ((valid[i] >> lane) & 1) && (scale[i] & 0x7FFFu) == 0;
   const bool wide = __any_sync(~0u, nothing) || span > (value ? kValueSpan : kKeySpan);
-  __shared__ int s_most[2 * C::kUnits];
-  if (lane == 0) s_most[warp] = wide ? kWide : value ? -kWide : e;
+  __shared__ int s_code[2 * C::kUnits];
+  if (lane == 0) s_code[warp] = (wide ? kWide : 0) + (value ? -kWide / 4 : e);
   __syncthreads();
+  // the positions' own figures are written where either their keys or their values are wide
+  const bool write_own = max(s_code[block], s_code[block + C::kUnits]) >= kWide / 2;
   if (threadIdx.x == 0) {
-    int most = s_most[0];
+    int most = -kWide;
+    unsigned words = 0;
 #pragma unroll
-    for (int i = 1; i < 2 * C::kUnits; ++i) most = max(most, s_most[i]);
-    tm.most = most;
+    for (int i = 0; i < C::kUnits; ++i) {
+      const bool own = max(s_code[i], s_code[i + C::kUnits]) >= kWide / 2;
+      most = max(most, s_code[i] - (s_code[i] >= kWide / 2 ? kWide : 0));
+      if (own) words |= (kWords == 1 ? 1u : 3u) << (i * kWords);
+    }
+    tm.code = most + (words ? kWide : 0);
+    tm.wide = words;
   }
 
   if (!value) {
@@ -242,7 +256,7 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
         uint32_t most = __vmaxu2(scale[i] & 0x7FFF7FFFu, kWords == 1 ? scale[1] & 0x7FFF7FFFu : 0u);
         most = max(most & 0xFFFFu, most >> 16);
         ep = wide && most ? exponent(__float_as_uint(half_at(most, 0))) : e;
-        tm.pos_ek[block * C::kUnit + i * 32 + lane] = (signed char)ep;
+        if (write_own) pm[block * C::kUnit + i * 32 + lane].up_k = pow2i(ep);
       }
       const float down = pow2i(-ep);
       sw[i] = half2_of(half_at(scale[i], 0) * down, half_at(scale[i], 1) * down);
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(64 * Config<D>::kUnits) k_attn_unpack(const Pr
     const float s = half_at(scale[i], 0);
     const unsigned a = __float_as_uint(fabsf(s));
     const int es = wide && a ? exponent(a) : e;
-    tm.pos_ev[block * C::kUnit + i * 32 + lane] = (signed char)(a ? es - kValueUp : kNoValue);
+    if (write_own) pm[block * C::kUnit + i * 32 + lane].ev = a ? (float)(es - kValueUp) : -INFINITY;
     const uint32_t w = __half_as_ushort(__float2half_rn(s * pow2i(kValueUp - es)));
     sw[i] = w | (__shfl_down_sync(~0u, w, 1) << 16);
   }
@@ -405,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     }
     for (int i = 0; i < kMetaSlots; ++i) mbar_init(&sh.meta_full[i], 1);
     sh.abort = 0;
+    sh.positions = p.positions + (((int64_t)b * p.heads + (h - p.head0)) * p.tiles + tile0) * kPos;
     fence_barrier_init();
   }
   if (warp == kIssuer) tmem_alloc(&sh.tmem, C::kColumns);
@@ -464,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
     // Keys whose exponent passes this may give scores beyond kHuge, whose reference is rounded by
     // more than P in float16 can bear: |S| is below 2^15 * 254 * D.  (Rows of zeros have factor 1.)
     const int ek_most = __reduce_min_sync(
-        ~0u, some ? (int)fminf(floorf(log2f(kHuge / (0x1p15f * 254.0f * D)) - log2f(row_factor)), kWide - 1.0f) : kWide - 1);
+        ~0u, some ? (int)fminf(floorf(log2f(kHuge / (0x1p15f * 254.0f * D)) - log2f(row_factor)), 100.0f) : 100);
     const auto arrives = [&] {  // S of tile j, with its metadata
       ok = mbar_wait(&sh.meta_full[j % kMetaSlots], (j / kMetaSlots) & 1, abort_flag) &&
            mbar_wait(&sh.s_full[half], j & 1, abort_flag);
@@ -507,148 +522,196 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_prefill(const PrefillParam
       if (lane == 0) mbar_arrive(bar);
     };
 
-    // Up to the first tile that passes ek_most: m_v is 0 and m_l is m.
-    for (; j < n; ++j) {
-      if (!arrives()) break;
-      const TileMeta &tm = sh.meta[j % kMetaSlots];
-      if (tm.most > ek_most) break;
-      const int j0 = beg + j * kPos;
-      const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
-                        (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
-                        (tm.poison[0] | tm.poison[1] | tm.poison[2] | tm.poison[3]) == 0;
-      // The row's largest exponent.  P of the first half of the scores goes over them, so
-      // they stay in registers; those of the second half (columns that P leaves alone)
-      // are read again: 128 registers of scores spill (1173 us against 1162).
-      uint32_t s[4][32];
-      float f[4];
-      int ev[4];
+    // Tiles with one exponent for each 32 positions, and scores within kHuge: m_v is 0 and m_l is m.
+    const auto common = [&] {
+      for (; j < n; ++j) {
+        if (!arrives()) break;
+        const TileMeta &tm = sh.meta[j % kMetaSlots];
+        if (tm.code > ek_most) break;
+        const int j0 = beg + j * kPos;
+        const bool full = j0 >= all_lo && j0 + kPos <= all_hi && j0 >= lo &&
+                          (tm.valid[0] & tm.valid[1] & tm.valid[2] & tm.valid[3]) == ~0u &&
+                          (tm.poison[0] | tm.poison[1] | tm.poison[2] | tm.poison[3]) == 0;
+        // The row's largest exponent.  P of the first half of the scores goes over them, so
+        // they stay in registers; those of the second half (columns that P leaves alone)
+        // are read again: 128 registers of scores spill (1173 us against 1162).
+        uint32_t s[4][32];
+        float f[4];
+        int ev[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        f[c] = factor(tm.ek[c]);
-        ev[c] = tm.ev[c];
-      }
-      float now = m;
-      const auto maximum = [&](int c, const uint32_t (&s)[32]) {
-        float t[4];  // four chains
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[i]);
-#pragma unroll
-        for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[i]));
-        now = fmaxf(now, fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]));
-      };
-      const auto arrived = [&](int c) {
-        tmem_ld_wait();
-        tie(s[c]);
-        if (__builtin_expect(!full, 0)) mask(tm, c, s[c]);
-      };
-      tmem_ld32(s_at + 2 * 32, s[2]);
-      arrived(2);
-      tmem_ld32(s_at + 3 * 32, s[3]);
-      maximum(2, s[2]);
-      arrived(3);
-      tmem_ld32(s_at, s[0]);
-      maximum(3, s[3]);
-      arrived(0);
-      tmem_ld32(s_at + 32, s[1]);
-      maximum(0, s[0]);
-      arrived(1);
-      maximum(1, s[1]);
-      if (__any_sync(~0u, now > m + kGrowth)) {
-        // a new reference: what was summed under the old one is scaled down
-        const bool grew = now > m + kGrowth;
-        const float a = grew ? exp2_approx(m - now) : 1.0f;
-        if (grew) m = now;
-        l *= a;
-        rescale(a);
-      }
-      // P = 2^(s + ev - m + bias), over S
-      const float z = kPBias - (m == -INFINITY ? 0.0f : m);
-      const auto probabilities = [&](int k, const uint32_t (&s)[32]) {
-        const float g = (float)ev[k] + z;
-        const uint64_t f2 = f32x2_pack(f[k], f[k]), g2 = f32x2_pack(g, g);
-        uint64_t sum2[2] = {0, 0};
-        uint32_t o[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
-          const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
-          sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
-          o[i] = half2_of(a, e);
+        for (int c = 0; c < 4; ++c) {
+          f[c] = factor(tm.ek[c]);
+          ev[c] = tm.ev[c];
         }
-        sum2[0] = f32x2_add(sum2[0], sum2[1]);
-        l += (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * pow2i(-ev[k]);
-        tmem_st16(s_at + k * 16, o);
-      };
-      tmem_ld32(s_at + 2 * 32, s[2]);
-      probabilities(0, s[0]);
-      probabilities(1, s[1]);
-      arrived(2);
-      tmem_ld32(s_at + 3 * 32, s[3]);
-      hand_over(&sh.p_half[half]);  // the first half of P: its products start
-      probabilities(2, s[2]);
-      arrived(3);
-      probabilities(3, s[3]);
-      hand_over(&sh.p_full[half]);
-    }
-    // From there on each position has its own exponents, and differences of scores, which are
-    // exact near the maximum, are taken before the exponents of the values are added.  Such
-    // tiles are rare: a loop of its own, with few registers (as a case of the one above it
-    // cost that one 1342 us against 1169 at 8192 x 16384, 28 heads over 4 of 128).
-    m_l = m;
-    for (; j < n && __all_sync(~0u, ok); ++j) {
-      if (!arrives()) break;
-      const TileMeta &tm = sh.meta[j % kMetaSlots];
-      uint32_t s[32];
-      const auto scores = [&](int c) {
-        tmem_ld32(s_at + c * 32, s);
-        tmem_ld_wait();
-        tie(s);
-        mask(tm, c, s);
-      };
-      // position i's score, and the exponent of its value
-      const auto single = [&](uint32_t s, int i, float &x, float &e) {
-        x = __fmul_rn(__uint_as_float(s), factor(tm.pos_ek[i]));  // rounded, wherever it is used
-        e = tm.pos_ev[i] == kNoValue ? -INFINITY : (float)tm.pos_ev[i];
-      };
-      float now = m, now_v = m_v, top = m_l;
+        float now = m;
+        const auto maximum = [&](int c, const uint32_t (&s)[32]) {
+          float t[4];  // four chains
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = __uint_as_float(s[i]);
+#pragma unroll
+          for (int i = 4; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[i]));
+          now = fmaxf(now, fmaf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), f[c], (float)ev[c]));
+        };
+        const auto arrived = [&](int c) {
+          tmem_ld_wait();
+          tie(s[c]);
+          if (__builtin_expect(!full, 0)) mask(tm, c, s[c]);
+        };
+        tmem_ld32(s_at + 2 * 32, s[2]);
+        arrived(2);
+        tmem_ld32(s_at + 3 * 32, s[3]);
+        maximum(2, s[2]);
+        arrived(3);
+        tmem_ld32(s_at, s[0]);
+        maximum(3, s[3]);
+        arrived(0);
+        tmem_ld32(s_at + 32, s[1]);
+        maximum(0, s[0]);
+        arrived(1);
+        maximum(1, s[1]);
+        if (__any_sync(~0u, now > m + kGrowth)) {
+          // a new reference: what was summed under the old one is scaled down
+          const bool grew = now > m + kGrowth;
+          const float a = grew ? exp2_approx(m - now) : 1.0f;
+          if (grew) m = now;
+          l *= a;
+          rescale(a);
+        }
+        // P = 2^(s + ev - m + bias), over S
+        const float z = kPBias - (m == -INFINITY ? 0.0f : m);
+        const auto probabilities = [&](int k, const uint32_t (&s)[32]) {
+          const float g = (float)ev[k] + z;
+          const uint64_t f2 = f32x2_pack(f[k], f[k]), g2 = f32x2_pack(g, g);
+          uint64_t sum2[2] = {0, 0};
+          uint32_t o[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
+            const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
+            sum2[i & 1] = f32x2_add(sum2[i & 1], f32x2_pack(a, e));
+            o[i] = half2_of(a, e);
+          }
+          sum2[0] = f32x2_add(sum2[0], sum2[1]);
+          l += (f32x2_lo(sum2[0]) + f32x2_hi(sum2[0])) * pow2i(-ev[k]);
+          tmem_st16(s_at + k * 16, o);
+        };
+        tmem_ld32(s_at + 2 * 32, s[2]);
+        probabilities(0, s[0]);
+        probabilities(1, s[1]);
+        arrived(2);
+        tmem_ld32(s_at + 3 * 32, s[3]);
+        hand_over(&sh.p_half[half]);  // the first half of P: its products start
+        probabilities(2, s[2]);
+        arrived(3);
+        probabilities(3, s[3]);
+        hand_over(&sh.p_full[half]);
+      }
+      m_l = m;
+    };
+    // The other loops are rare: 32 scores at a time, and few registers (as cases of the one above
+    // they cost that one 1342 us against 1169 at 8192 x 16384, 28 heads over 4 of 128).
+    uint32_t s[32];
+    const auto scores = [&](const TileMeta &tm, int c) {
+      tmem_ld32(s_at + c * 32, s);
+      tmem_ld_wait();
+      tie(s);
+      mask(tm, c, s);
+    };
+    // The figures of position c * 32 + lane; others read them by shuffles (as loads, 32 at once spill).
+    const auto own_of = [&](const TileMeta &tm, int c) {
+      if ((tm.wide >> c) & 1) return sh.positions[j * kPos + c * 32 + lane];
+      return PositionMeta{pow2i(tm.ek[c]), (float)tm.ev[c]};
+    };
+    // Other tiles.  A word of 32 positions that is wide, or whose scores may be huge, is taken position
+    // by position: differences of scores, which are exact near the maximum, before the exponents of the
+    // values are added.  l has a reference of its own, since scores without a value do not raise m.
+    // True: the next tile is common(), O is under m alone and l under m again.
+    const auto general = [&] {
+      for (; j < n; ++j) {
+        if (!arrives()) break;
+        const TileMeta &tm = sh.meta[j % kMetaSlots];
+        if (tm.code <= ek_most && __all_sync(~0u, (m_l == m || m_l - m < 60.0f) && (m_v == 0.0f || fabsf(m) < 0x1p20f))) {
+          m += m_v, m_v = 0.0f;
+          if (m_l > -INFINITY) l *= exp2_approx(m_l - m);
+          return true;
+        }
+        const unsigned single = tm.code - (tm.code >= kWide / 2 ? kWide : 0) > ek_most ? ~0u : tm.wide;
+        float now[2] = {m, m}, now_v[2] = {m_v, m_v}, top = m_l;  // two chains
+        const auto larger = [&](int k, float x, float e) {
+          if ((x - now[k]) + (e - now_v[k]) > 0.0f) now[k] = x, now_v[k] = e;
+        };
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        scores(c);
+        for (int c = 0; c < 4; ++c) {
+          scores(tm, c);
+          const PositionMeta own = own_of(tm, c);
+          if ((single >> c) & 1) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float x, e;
-          single(s[i], c * 32 + i, x, e);
-          if ((x - now) + (e - now_v) > 0.0f) now = x, now_v = e;
-          top = fmaxf(top, x);
+            for (int i = 0; i < 32; ++i) {
+              const float f = fmaxf(row_factor * __shfl_sync(~0u, own.up_k, i), 0x1p-100f);
+              const float x = __fmul_rn(__uint_as_float(s[i]), f);  // rounded, wherever it is used
+              larger(i % 2, x, __shfl_sync(~0u, own.ev, i));
+              top = fmaxf(top, x);
+            }
+          } else {
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) t[i % 4] = fmaxf(t[i % 4], __uint_as_float(s[i]));
+            const float x = __fmul_rn(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), factor(tm.ek[c]));
+            larger(0, x, (float)tm.ev[c]);
+            top = fmaxf(top, x);
+          }
         }
-      }
-      const float by = (now - m) + (now_v - m_v);
-      if (top - m_l > kLead) {
-        l *= exp2_approx(m_l - top);
-        m_l = top;
-      }
-      if (__any_sync(~0u, by > kGrowth)) {
-        const float a = by > kGrowth ? exp2_approx(-by) : 1.0f;
-        if (by > kGrowth) m = now, m_v = now_v;
-        rescale(a);
-      }
-      const float m_0 = m == -INFINITY ? 0.0f : m, l_0 = m_l == -INFINITY ? 0.0f : m_l;
+        larger(0, now[1], now_v[1]);
+        const float by = (now[0] - m) + (now_v[0] - m_v);
+        if (top - m_l > kLead) {
+          l *= exp2_approx(m_l - top);
+          m_l = top;
+        }
+        if (__any_sync(~0u, by > kGrowth)) {
+          const float a = by > kGrowth ? exp2_approx(-by) : 1.0f;
+          if (by > kGrowth) m = now[0], m_v = now_v[0];
+          rescale(a);
+        }
+        const float m_0 = m == -INFINITY ? 0.0f : m, l_0 = m_l == -INFINITY ? 0.0f : m_l;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        scores(c);
-        uint32_t o[16];
+        for (int c = 0; c < 4; ++c) {
+          scores(tm, c);
+          const PositionMeta own = own_of(tm, c);
+          uint32_t o[16];
+          float sum = 0.0f;
+          if ((single >> c) & 1) {
+            const auto one = [&](int i) {
+              const float f = fmaxf(row_factor * __shfl_sync(~0u, own.up_k, i), 0x1p-100f);
+              const float x = __fmul_rn(__uint_as_float(s[i]), f), e = __shfl_sync(~0u, own.ev, i);
+              sum += exp2_approx((x - l_0) + kPBias);
+              return exp2_approx((x - m_0) + (e - m_v + kPBias));
+            };
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x0, x1, e0, e1;
-          single(s[2 * i], c * 32 + 2 * i, x0, e0);
-          single(s[2 * i + 1], c * 32 + 2 * i + 1, x1, e1);
-          l += exp2_approx((x0 - l_0) + kPBias) + exp2_approx((x1 - l_0) + kPBias);
-          o[i] = half2_of(exp2_approx((x0 - m_0) + (e0 - m_v + kPBias)), exp2_approx((x1 - m_0) + (e1 - m_v + kPBias)));
+            for (int i = 0; i < 16; ++i) {
+              const float a = one(2 * i), e = one(2 * i + 1);
+              o[i] = half2_of(a, e);
+            }
+          } else {
+            const float f = factor(tm.ek[c]), g = (float)tm.ev[c] - m_v + kPBias - m_0;
+            const uint64_t f2 = f32x2_pack(f, f), g2 = f32x2_pack(g, g);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x = f32x2_fma((uint64_t)s[2 * i] | ((uint64_t)s[2 * i + 1] << 32), f2, g2);
+              const float a = exp2_approx(f32x2_lo(x)), e = exp2_approx(f32x2_hi(x));
+              sum += a + e;
+              o[i] = half2_of(a, e);
+            }
+            sum *= pow2i(-tm.ev[c]) * exp2_approx((m_0 - l_0) + m_v);
+          }
+          l += sum;
+          tmem_st16(s_at + c * 16, o);
+          if (c & 1) hand_over(c == 1 ? &sh.p_half[half] : &sh.p_full[half]);
         }
-        tmem_st16(s_at + c * 16, o);
-        if (c & 1) hand_over(c == 1 ? &sh.p_half[half] : &sh.p_full[half]);
       }
-    }
+      return false;
+    };
+    do common();
+    while (j < n && __all_sync(~0u, ok) && general());
     if (__all_sync(~0u, ok)) ok = mbar_wait(&sh.o_full[half], 0, abort_flag);
     if (__all_sync(~0u, ok)) {
       tc_fence_after();
@@ -801,8 +864,9 @@ cudaError_t launch_d(PrefillParams p, int64_t group, cudaStream_t st) {
   }
   for (p.head0 = 0; p.head0 < p.H; p.head0 += p.heads) {
     p.heads = (int)std::min<int64_t>(group, p.H - p.head0);  // the increment sees it, too
-    p.meta = reinterpret_cast<TileMeta *>(p.images + (int64_t)p.B * p.heads * p.tiles * C::kImage);
     const int64_t pairs = (int64_t)p.B * p.heads;
+    p.meta = reinterpret_cast<TileMeta *>(p.images + pairs * p.tiles * C::kImage);
+    p.positions = reinterpret_cast<PositionMeta *>(p.meta + pairs * p.tiles);
     e = launch_kernel(k_attn_unpack<D>, dim3((unsigned)(pairs * p.tiles)), dim3(64 * C::kUnits), 0, st, 1, p);
     if (e != cudaSuccess) return e;
     e = launch_kernel(k_attn_prefill<D>, dim3((unsigned)(pairs * p.row_tiles * p.parts.splits)), dim3(kThreads),
@@ -825,7 +889,7 @@ AttnPrefillPlan attn_prefill_plan(int64_t B, int64_t H, int64_t G, int64_t D, in
                                   int64_t window, int sms) {
   AttnPrefillPlan plan{};
   const int64_t tiles = std::max<int64_t>(1, (max_kv + kPos - 1) / kPos);
-  const int64_t head = B * tiles * (4 * kPos * D + (int64_t)sizeof(TileMeta));
+  const int64_t head = B * tiles * (4 * kPos * D + (int64_t)(sizeof(TileMeta) + kPos * sizeof(PositionMeta)));
   plan.heads = std::max<int64_t>(1, std::min(H, ((int64_t)2 << 30) / head));
   plan.image_bytes = round_up((size_t)(head * plan.heads), 256);
   constexpr int64_t rows = 2 * kRowTile;

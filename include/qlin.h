@@ -466,7 +466,7 @@ qlin_status qlin_rope_kv_store_mixed(qlin_rope_layout layout, int64_t T, int64_t
  * device status word is set to QLIN_ERR_INVALID_ARG.
  *   ws: qlin_attn_mixed_workspace_bytes(B, Hq, H, D, max_q, max_kv, window)
  *   bytes: partial results where the positions are split over CTAs, and for many
- *   rows the positions as float16 (4 D + 3 bytes for each position of max_kv, kv
+ *   rows the positions as float16 (4 D + 9 bytes for each position of max_kv, kv
  *   head and sequence; beyond about 2 GB the kv heads go in groups, of one at least).
  *   max_q and max_kv bound the launch: tight ones cost less memory and time.
  * Requirements: B >= 0, D 32, 64, 128 or 256, Hq a multiple of H, Hq / H <= 128,
