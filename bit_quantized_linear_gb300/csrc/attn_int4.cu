@@ -902,8 +902,8 @@ AttnInt4Plan attn_int4_plan(int64_t B, int64_t Hq, int64_t H, int64_t D, int64_t
   AttnInt4Plan plan{};
   plan.rows = rows <= 8 || D >= 256 ? 8 : 16;
   const int64_t tile = D >= 256 ? 16 : 32, tiles = (rows + plan.rows - 1) / plan.rows, units = B * H * tiles;
-  int64_t range = max_kv;
-  if (window > 0) range = std::min(range, 2 * window + plan.rows / (Hq / H) + 1) + kAlign - 1;
+  int64_t range = max_kv;  // (a window may be as wide as its type: beyond max_kv it is none, doubled or not)
+  if (window > 0) range = std::min(range, 2 * std::min(window, max_kv) + plan.rows / (Hq / H) + 1) + kAlign - 1;
   const int64_t resident = (int64_t)sms * attn_int4_ctas(D, plan.rows);
   plan.step_shift = tile == 16 ? 6 : 7;
   const auto steps_of = [&](int shift) { return std::max<int64_t>(1, (range + ((int64_t)1 << shift) - 1) >> shift); };
