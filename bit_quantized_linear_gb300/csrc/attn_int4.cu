@@ -19,8 +19,8 @@
 //     summed in fp32 and then scaled by the group's scale in fp32.
 //   * Values: the same bits beside 0x6400 are 1024 + 8 + c, and minus 1032 the code; times the scale it is
 //     rounded to float16 once.
-//   * P is 2^8 times the weight under a row's reference, in float16; the reference is taken anew only where a score
-//     passes it by more than 7.
+//   * P is the weight under a row's reference, 2^8 for the largest score where it is taken, in float16; it is taken anew
+//     only where a score is above it by more than 15.
 // A position with a scale that the store does not write gives NaN to the rows that see it
 // and nothing to the others: its scores are NaN where seen and its values 0.
 #include <algorithm>
@@ -36,7 +36,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kBias = 8.0f, kGrowth = 7.0f;  // P stays below 2^15
+// A row's reference lies kBias below its largest score when it is taken, and no score passes it by more than kTop: P
+// stays below 2^15.5.  Beyond kExact, where binary32 has no room for the bias (from 2^27 on it rounds by up to itself, and P
+// left float16), the reference is the largest score.
+constexpr float kBias = 8.0f, kTop = kBias + 7.0f, kExact = 0x1p22f;
 constexpr int kAlign = 32;  // a unit's first position is rounded down to a multiple of this
 
 // A unit whose steps are split, as the range where it begins notes it: in the list of ranges, or (few units) in
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, Geometry4<D, NT>::kCtas) k_attn_int4
       all_lo = __reduce_max_sync(~0u, all_lo);
       all_hi = __reduce_min_sync(~0u, all_hi);
 
-      // a score near the largest one, the sum of P
+      // what P's exponents are counted from, the sum of P
       float ref[NT][2], l[NT][2], O[NT][kMmas][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -588,14 +591,14 @@ __global__ void __launch_bounds__(kThreads, Geometry4<D, NT>::kCtas) k_attn_int4
             mx[0] = fmaxf(mx[0], fmaxf(S[kHalves - 1][nt][0], S[kHalves - 1][nt][2]));
             mx[1] = fmaxf(mx[1], fmaxf(S[kHalves - 1][nt][1], S[kHalves - 1][nt][3]));
           }
-          if (__any_sync(~0u, mx[0] > ref[nt][0] + kGrowth || mx[1] > ref[nt][1] + kGrowth)) {
-            // new references: the largest scores
+          if (__any_sync(~0u, mx[0] - ref[nt][0] > kTop || mx[1] - ref[nt][1] > kTop)) {
+            // new references, by the largest scores
             float a[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
               for (int o = 4; o < 32; o *= 2) mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], o));
-              const float now = fmaxf(ref[nt][c], mx[c]);
+              const float now = fmaxf(ref[nt][c], fabsf(mx[c]) < kExact ? mx[c] - kBias : mx[c]);
               a[c] = exp2_approx(ref[nt][c] - (now == -INFINITY ? 0.0f : now));
               ref[nt][c] = now;
               l[nt][c] *= a[c];
@@ -606,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, Geometry4<D, NT>::kCtas) k_attn_int4
               O[nt][i][1] *= a[1], O[nt][i][3] *= a[1];
             }
           }
-          const float z0 = ref[nt][0] == -INFINITY ? 0.0f : ref[nt][0] - kBias;
-          const float z1 = ref[nt][1] == -INFINITY ? 0.0f : ref[nt][1] - kBias;
+          const float z0 = ref[nt][0] == -INFINITY ? 0.0f : ref[nt][0];
+          const float z1 = ref[nt][1] == -INFINITY ? 0.0f : ref[nt][1];
 #pragma unroll
           for (int f = 0; f < kHalves; ++f) {
             const float(&x)[4] = S[f][nt];
@@ -676,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, Geometry4<D, NT>::kCtas) k_attn_int4
           for (int i = 0; i < kMmas; ++i)
             *reinterpret_cast<float2 *>(res + r * D + g * kDims + 2 * i) = make_float2(O[nt][i][c], O[nt][i][2 + c]);
           if (g == 0) {
-            res[kRows * D + r] = ref[nt][c] - kBias;
+            res[kRows * D + r] = ref[nt][c];
             res[kRows * D + kRows + r] = l[nt][c];
           }
         }
