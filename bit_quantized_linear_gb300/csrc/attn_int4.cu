@@ -24,6 +24,7 @@
 // A position with a scale that the store does not write gives NaN to the rows that see it
 // and nothing to the others: its scores are NaN where seen and its values 0.
 #include <algorithm>
+#include <cfloat>
 
 #include "attn.cuh"
 #include "common.cuh"
@@ -403,7 +404,10 @@ __global__ void __launch_bounds__(kThreads, Geometry4<D, NT>::kCtas) k_attn_int4
         most = __vmaxu2(most, __shfl_xor_sync(~0u, most, 2));
         const float top = __uint_as_float(max(most & 0xFFFFu, most >> 16) << 16);
         const int e = q_exponent(top);
-        const float up = pow2i(14 - e), factor = (p.scale_log2 * pow2i(max(e - 14, -126))) * 0x1p24f;
+        // A factor beyond binary32 (|q| from about 2^121 on) becomes its largest number: scores that are not equal lie far
+        // apart under either, and those of 0 stay 0.
+        const float up = pow2i(14 - e);
+        const float factor = fminf(fmaxf((p.scale_log2 * pow2i(max(e - 14, -126))) * 0x1p24f, -FLT_MAX), FLT_MAX);
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
           const uint32_t u[4] = {qw[nt][k].x, qw[nt][k].y, qw[nt][k].z, qw[nt][k].w};

@@ -110,6 +110,13 @@ def test_steps(capi, D, nq, kv, B, H, step, base, order):
     assert ((_run(capi, a, scale=_scale_of(0)) - want).abs() <= tol).all()
 
 
+def _near(out, want, a):
+    """Means of values: the output's rounding, those of P and of values to float16 (2^-11 of the largest), binary32 sums."""
+    sizes = torch.cat([_values(a, b).abs().amax(0).repeat_interleave(a.G, dim=0).reshape(1, -1).expand(n, -1)
+                       for b, n in enumerate(a.nq)])
+    assert ((out - want).abs() <= 2.0 ** -8 * want.abs() + sizes * (2 * 2.0 ** -11 + 2.0 ** -18)).all()
+
+
 @pytest.mark.parametrize("D,nq,kv,B,H", FEW + MANY)
 @pytest.mark.parametrize("lift", [2.0 ** 20, 2.0 ** 22, 2.0 ** 24, 2.0 ** 30, 2.0 ** 50])
 def test_the_largest_score_takes_all(capi, D, nq, kv, B, H, lift):
@@ -121,8 +128,27 @@ def test_the_largest_score_takes_all(capi, D, nq, kv, B, H, lift):
     a.q += torch.randint(0, 2, a.q.shape, generator=torch.Generator().manual_seed(D)) * 0.5
     limit, _ = a.reference(scale=4096.0)  # all weight on the best
     a.q *= lift
-    out = _run(capi, a, scale=1.0)
-    sizes = torch.cat([_values(a, b).abs().amax(0).repeat_interleave(a.G, dim=0).reshape(1, -1).expand(n, -1)
-                       for b, n in enumerate(a.nq)])
-    tol = 2.0 ** -8 * limit.abs() + sizes * (2 * 2.0 ** -11 + 2.0 ** -18)
-    assert ((out - limit).abs() <= tol).all()
+    _near(_run(capi, a, scale=1.0), limit, a)
+
+
+@pytest.mark.parametrize("D,nq,kv,B,H", FEW + MANY)
+@pytest.mark.parametrize("e", [118, 121, 124, 126])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_largest_queries(capi, D, nq, kv, B, H, e, sign):
+    """Rows of q up to the end of BF16's range beside ordinary ones, under key scales that leave their scores binary32
+    numbers: the best positions take all, the first ones with keys of zeros, whose scores are 0, among them."""
+    a = _case(capi, D, nq, kv, B, H, seed=2)
+    a.ks[a.ks.isfinite()] = 2.0 ** -24
+    a.kcode[:] = torch.where(a.kcode >= 0, 3, -3).to(torch.int8)
+    for b in range(B):
+        page, off = a.place(b, torch.arange(kv // 8))
+        a.kcode[page, :, off] = 0
+    q = torch.where(a.q >= 0, 1.0, -1.0).view(-1, H * 4, D)
+    q[:, 1] = 0  # all scores 0
+    small = q.clone()
+    small[:, 2::4] *= 2.0 ** -60  # of nearly no score
+    a.q = small.view(a.q.shape).bfloat16()
+    big = (q * 2.0 ** torch.tensor([e, e, -60, e - 3.0])[torch.arange(H * 4) % 4][:, None]).view(a.q.shape).bfloat16()
+    want, _ = a.reference(scale=sign * 2.0 ** 40)  # all weight on the best, or none
+    a.q = big
+    _near(_run(capi, a, scale=sign * D ** -0.5), want, a)
