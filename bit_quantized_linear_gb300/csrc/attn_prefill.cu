@@ -33,8 +33,8 @@
 // a row does not see leaves that row's others in place), so float16 holds
 // them whatever the cache's scales; 2^ek joins the score's factor and ev the
 // exponent, so that neither costs the softmax an instruction per score.  O is
-// rescaled only where a row's maximum grew by more than 2^6 (of the 4-bit cache 2^10) since its reference;
-// P stays below 2^14.  Positions whose value scale is 0 do not raise that
+// rescaled only where a row's maximum grew by more than 2^6 (of the 4-bit cache 2^7.75) since its reference;
+// P stays below 2^14 (2^15.9).  Positions whose value scale is 0 do not raise that
 // reference (they would push P of the others out of float16): they count in the
 // sum of the row alone, which for that has a reference of its own.  Scores too large
 // for a reference in binary32 to be exact enough go the same rare way as wide units.
@@ -55,13 +55,16 @@ using namespace tc;
 constexpr int kPos = 128;       // positions of a tile
 constexpr int kRowTile = 128;   // rows of an MMA
 constexpr int kMetaSlots = 4;
-// P is 2^kPBias p and may grow by 2^kGrowth before its reference is taken anew: below 2^14, and with float16's subnormals
-// below 2^-22 p (the mixed cache), or 2^-18 p.  The latter needs a new reference, for which the tensor core waits, less
-// often: 8192 x 16384, 28 heads over 4 of 128: 1178 us with 8 and 6, 1121 with 4 and 10, 1112 with 2 and 12.
-constexpr float kPBiasOf(bool int4) { return int4 ? 4.0f : 8.0f; }
-constexpr float kGrowthOf(bool int4) { return int4 ? 10.0f : 6.0f; }
+// P is 2^kPBias p and may grow by 2^kGrowth before its reference is taken anew, for which the tensor core waits: below 2^14
+// (the mixed cache) or 2^15.9.  Its subnormals lie below 2^-22 p, so that what small weights add up to, beside a heavy
+// position without a value, is as exact as with few rows.  8192 x 16384, 28 heads over 4 of 128: growth 6 1165 us, 7 1153,
+// 7.75 1141; a bias of 4 with 10 took 1110, with weights below 2^-18 of the largest losing bits.
+constexpr float kPBias = 8.0f;
+constexpr float kGrowthOf(bool int4) { return int4 ? 7.75f : 6.0f; }
 constexpr float kLead = 32.0f;  // a score may pass the sum's reference by 2^this where O has another
-constexpr float kHuge = 0x1p24f;  // scores up to here have a reference good to 1/2: P stays below 2^14.5
+// Scores up to here have a reference good to 1/2, so P stays below 2^14.5; or (growth 7.75) their maximum, reference and
+// difference are each good to 2^-5, and P stays below 2^15.9.
+constexpr float kHugeOf(bool int4) { return int4 ? 0x1p20f : 0x1p24f; }
 constexpr int kValueUp = 6;     // a value's scale becomes 2^6..2^7 (times at most 448: below float16's 65504)
 constexpr int kValueSpan = 11;  // scales of a unit within 2^11 share an exponent: E4M3's 2^-9 stays normal
 constexpr int kKeySpan = 14;    // key scales within 2^14: a code of 1 stays normal
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(kUnpack4Threads) k_attn_unpack4(const PrefillP
 
 template <int D, bool INT4>
 __global__ void __launch_bounds__(Config<D>::kThreads, 1) k_attn_prefill(const PrefillParams p) {
-  constexpr float kPBias = kPBiasOf(INT4), kGrowth = kGrowthOf(INT4);
+  constexpr float kGrowth = kGrowthOf(INT4), kHuge = kHugeOf(INT4);
   using C = Config<D>;
   constexpr bool kOne = C::kRowTiles == 1;
   constexpr int kSoftmaxWarps = C::kSoftmaxWarps, kCopier = C::kCopier, kIssuer = C::kIssuer, kThreads = C::kThreads;
