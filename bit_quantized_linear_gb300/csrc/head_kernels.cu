@@ -204,16 +204,18 @@ __device__ __forceinline__ float head_rms(const HeadParams &p, const uint32_t *x
   return rms_reciprocal(S, p.inv_d, p.eps);
 }
 
-// Reciprocal root mean square of a query head, within 2^-21: one packed operation for each pair, against
-// eight above.
+// Reciprocal root mean square of a query head, within 2^-20.4 (the sum's and the quotient's roundings, fourteen of 2^-24 at
+// most, halved by the root, and two ulp of rsqrtf): one packed operation for each pair, against eight above.  `wild`: the
+// sum of squares is not a number of binary32.
 template <int width>
-__device__ __forceinline__ float head_rms_fast(const HeadParams &p, const uint32_t (&x)[8]) {
+__device__ __forceinline__ float head_rms_fast(const HeadParams &p, const uint32_t (&x)[8], bool &wild) {
   uint64_t S2[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 8; ++j) S2[j % 2] = f32x2_fma(f32x2_of(x[j]), f32x2_of(x[j]), S2[j % 2]);
   float S = (f32x2_lo(S2[0]) + f32x2_hi(S2[0])) + (f32x2_lo(S2[1]) + f32x2_hi(S2[1]));
 #pragma unroll
   for (int o = width / 2; o > 0; o >>= 1) S += __shfl_xor_sync(~0u, S, o);
+  wild = !(S < INFINITY);
   return rsqrtf(fmaf(S, p.inv_d.hi, p.eps));
 }
 
@@ -234,6 +236,41 @@ __device__ __forceinline__ void wait_stages() {
 __device__ __forceinline__ void get_chunks(const uint8_t *from, uint32_t (&x)[8]) {
   const uint4 a = *reinterpret_cast<const uint4 *>(from), b = *reinterpret_cast<const uint4 *>(from + 512);
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// The heads of a warp, token t's for this lane, by the binary32 steps as they are written, from a stage of the ring into dst
+// where `store` is set.  For queries that the fused operations do not hold: rare, so apart, with loads of its own.
+template <int width, bool HALF>
+__device__ __noinline__ void exact_heads(const HeadParams &p, const uint8_t *stage, const uint16_t *w, int64_t t, uint16_t *dst,
+                                         bool store, unsigned *status) {
+  const int lane = threadIdx.x & 31;
+  const Pieces own = pieces_of<HALF>(p, lane % width, p.per);
+  uint32_t x[8], o[8];
+  get_chunks(stage, x);
+  const float r = head_rms<8, width>(p, x, lane);
+  if (!store) return;
+  Rows rows;
+  token_rows(p, t, rows, status);
+  float c[8], s[8], y[16];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j] = 1.0f, s[j] = 0.0f;
+  load_angles<HALF>(p, rows, own, c, s);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float v = j & 1 ? hi_f(x[j / 2]) : lo_f(x[j / 2]);
+    y[j] = __fmul_rn(__fmul_rn(v, r), __uint_as_float((uint32_t)ld_input(w + own.d0 + (j < 8 ? j : own.piece + j - 8)) << 16));
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = HALF ? j : 2 * j, k = HALF ? 8 + j : 2 * j + 1;
+    if (!own.turns[HALF ? 0 : j / 4]) continue;
+    const float a = y[i], b = y[k];
+    y[i] = turn_a(a, b, c[j], s[j]), y[k] = turn_b(a, b, c[j], s[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4 *>(dst + own.piece) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 constexpr int kDepth = 4, kRingBytes = kDepth * 1024;  // the stages of norm_rotate, a head of each lane in one
@@ -330,7 +367,8 @@ __device__ __forceinline__ void norm_rotate(const HeadParams &p, const HeadParam
     get_chunks(ring + k % kDepth * 1024, x);
     copy(k + kDepth - 1);
     float r = 0.0f;
-    if (FAST) r = head_rms_fast<width>(p, x);
+    bool wild = false;
+    if (FAST) r = head_rms_fast<width>(p, x, wild);
     else if (w) r = head_rms<8, width>(p, x, lane);
     const uint64_t r2 = f32x2_pack(r, r);
     uint64_t y[8];
@@ -368,10 +406,13 @@ __device__ __forceinline__ void norm_rotate(const HeadParams &p, const HeadParam
     uint32_t o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = bf16x2_of(y[j]);
-    if (stored && batch * at_once + first < units.heads) {
+    const bool here = stored && batch * at_once + first < units.heads;
+    if (here) {
       *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<uint4 *>(dst + piece) = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    if (FAST && __builtin_expect(__any_sync(~0u, wild && here), 0))
+      exact_heads<width, HALF>(p, ring + k % kDepth * 1024, w, t, dst, wild && here, status);
     if (++batch == units.batches) {
       batch = 0;
       t += units.tokens;
