@@ -40,6 +40,7 @@ struct HeadParams {
   int Hq, Hk, D, rot, half_layout, axes;
   uint32_t axis[16];         // two bits for each pair
   float eps, one;            // 1, where the compiler does not see it (sum_of)
+  float least;               // sums of squares below lose bits beside eps (head_rms_fast)
   TwoFloat inv_d;
   double eps64, inv_d64;
   int per, width;            // a head is `per` of `width` (a power of two) lanes
@@ -206,7 +207,7 @@ __device__ __forceinline__ float head_rms(const HeadParams &p, const uint32_t *x
 
 // Reciprocal root mean square of a query head, within 2^-20.4 (the sum's and the quotient's roundings, fourteen of 2^-24 at
 // most, halved by the root, and two ulp of rsqrtf): one packed operation for each pair, against eight above.  `wild`: the
-// sum of squares is not a number of binary32.
+// sum of squares is beyond what binary32 holds so well, or below where eps does not hide it.
 template <int width>
 __device__ __forceinline__ float head_rms_fast(const HeadParams &p, const uint32_t (&x)[8], bool &wild) {
   uint64_t S2[2] = {0, 0};
@@ -215,7 +216,7 @@ __device__ __forceinline__ float head_rms_fast(const HeadParams &p, const uint32
   float S = (f32x2_lo(S2[0]) + f32x2_hi(S2[0])) + (f32x2_lo(S2[1]) + f32x2_hi(S2[1]));
 #pragma unroll
   for (int o = width / 2; o > 0; o >>= 1) S += __shfl_xor_sync(~0u, S, o);
-  wild = !(S < INFINITY);
+  wild = !(S >= p.least && S < 0x1p126f);
   return rsqrtf(fmaf(S, p.inv_d.hi, p.eps));
 }
 
@@ -685,6 +686,7 @@ HeadParams head_params(const HeadArgs &a, int key_heads, int sms) {
   for (int i = 0; a.pair_axis && i < p.rot / 2; ++i) p.axis[i / 16] |= (uint32_t)a.pair_axis[i] << (2 * (i % 16));
   p.one = 1.0f;
   p.eps = a.eps, p.eps64 = (double)a.eps, p.inv_d64 = 1.0 / (double)a.D;
+  p.least = a.eps >= 0x1p-80f ? 0.0f : 0x1p-80f;
   p.inv_d.hi = (float)p.inv_d64;
   p.inv_d.lo = (float)(p.inv_d64 - (double)p.inv_d.hi);
   p.per = p.D / 16;

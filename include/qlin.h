@@ -446,8 +446,8 @@ qlin_status qlin_rope_kv_store_mixed(qlin_rope_layout layout, int64_t T, int64_t
  * sums of y, cosine and sine), and all are rounded to BF16 once.  For k, and for q without a
  * weight, these are the binary32 operations as written, and r, as in qlin_rmsnorm, is
  * reproducible; q with a weight is within 2^-19 (of the two products that a turned element
- * is the sum of) before its rounding.  (Heads of q whose squares leave binary32's range, about
- * |x| beyond 2^60, are not finite or 0.)
+ * is the sum of) before its rounding.  Heads whose squares leave binary32's range, and infinities and
+ * NaN, give what these operations give.
  *   q_weight, k_weight  [D] BF16 or NULL.  With both NULL and one axis the outputs
  *              are those of qlin_rope.
  *   axes       1 to 4: positions is int64 [axes, T], a token's position on each axis (time,

@@ -81,3 +81,26 @@ def test_one_infinity(capi, layout, D, rot, what):
         for d in range(D):  # token d: element d of one head
             x[d, d % 3, d] = what
         _check(capi, x, D, rot, layout, 1e-6, store)
+
+
+@pytest.mark.parametrize("layout", ["half", "pairs"])
+@pytest.mark.parametrize("D,rot", SHAPES)
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-24, 1e-30, 1.5e-38, 1e-44])
+def test_all_magnitudes(capi, layout, D, rot, eps):
+    """Heads from BF16's smallest numbers to its largest, alone and one large element among small ones; zeros, NaN."""
+    e = np.concatenate([np.arange(-133, 127, 5), [-76, -75, -74, -63, -62, -60, -42, -41, -40, 58, 60, 61, 62, 63, 64, 126]])
+    T = 2 * len(e) + 3
+    x = np.empty((T, 5, D), dtype=np.float32)
+    x[:] = np.clip(_rand((T, 5, D), D), -1.9, 1.9)
+    with np.errstate(all="ignore"):
+        for i, k in enumerate(e):
+            x[i] = (x[i].astype(np.float64) * 2.0 ** float(k)).astype(np.float32)
+            if i % 2:
+                x[i, ::2] = x[i, ::2] * np.float32(2.0 ** -7)  # heads of other sizes beside them
+            x[len(e) + i, 1, i % D] = np.float32(2.0 ** float(k))
+            x[len(e) + i, 4] = np.float32(2.0 ** max(-140.0, float(k) - 9)) * np.sign(x[len(e) + i, 4])
+    x[-3, 2] = 0
+    x[-2] = 0
+    x[-1, 3, D // 2] = np.nan
+    for store in (False, True) if D in (32, 64, 128, 256) else (False,):
+        _check(capi, x, D, rot, layout, eps, store)
