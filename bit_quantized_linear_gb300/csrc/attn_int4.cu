@@ -810,11 +810,9 @@ __device__ __forceinline__ void join_parts(const JoinRow &row, int part, int ste
 // Units that few ranges share: a warp for each row of the unit that begins in a range and ends in another.
 constexpr int kJoinWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_attn_int4_join(const __grid_constant__ Int4Params p, int rows) {
+__device__ __forceinline__ void join_of_range(const Int4Params &p, int rows) {
   constexpr int V = D / 32;  // floats of a lane
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
-  pdl_trigger();
   JoinRow row{join_entry(p.list + blockIdx.x), rows, 0, p.sum, p.o};
   if (row.e.ranges == 0) return;
   for (row.r = warp; row.r < rows && row.e.r0 + row.r < row.e.R; row.r += kJoinWarps) {
@@ -839,13 +837,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_int4_join(const __grid
 // Few units, in many parts each: a CTA for each row, its warps over the parts.
 constexpr int kManyWarps = 16;
 template <int D>
-__global__ void __launch_bounds__(32 * kManyWarps) k_attn_int4_join_many(const __grid_constant__ Int4Params p, int rows) {
+__device__ __forceinline__ void join_of_unit(const Int4Params &p, int rows) {
   constexpr int V = D / 32;
   __shared__ float s_o[kManyWarps][D];
   __shared__ float s_w[kManyWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
-  pdl_trigger();
   const JoinRow row{join_entry(p.list + blockIdx.x / rows), rows, (int)blockIdx.x % rows, p.sum, p.o};
   if (row.e.ranges == 0 || row.e.r0 + row.r >= row.e.R) return;
   float o[V], W = 0.0f;
@@ -871,6 +867,15 @@ __global__ void __launch_bounds__(32 * kManyWarps) k_attn_int4_join_many(const _
   }
 }
 
+template <int D, bool BY_UNIT>
+__global__ void __launch_bounds__(32 * (BY_UNIT ? kManyWarps : kJoinWarps))
+    k_attn_int4_join(const __grid_constant__ Int4Params p, int rows) {
+  pdl_wait();
+  pdl_trigger();
+  if constexpr (BY_UNIT) join_of_unit<D>(p, rows);
+  else join_of_range<D>(p, rows);
+}
+
 template <int D, int NT, bool EVEN>
 cudaError_t launch_nt(const Int4Params &p, const AttnInt4Plan &plan, cudaStream_t st) {
   using Geo = Geometry4<D, NT>;
@@ -886,9 +891,9 @@ cudaError_t launch_nt(const Int4Params &p, const AttnInt4Plan &plan, cudaStream_
   e = launch_kernel(k_attn_int4<D, NT, EVEN>, dim3((unsigned)plan.ctas), dim3(kThreads), Geo::kSmem, st, 1, p);
   if (e != cudaSuccess || !plan.joins) return e;
   if (plan.by_unit)
-    return launch_kernel(k_attn_int4_join_many<D>, dim3((unsigned)(plan.units * plan.rows)), dim3(32 * kManyWarps), 0, st,
+    return launch_kernel(k_attn_int4_join<D, true>, dim3((unsigned)(plan.units * plan.rows)), dim3(32 * kManyWarps), 0, st,
                          1, p, plan.rows);
-  return launch_kernel(k_attn_int4_join<D>, dim3((unsigned)plan.ctas), dim3(32 * kJoinWarps), 0, st, 1, p, plan.rows);
+  return launch_kernel(k_attn_int4_join<D, false>, dim3((unsigned)plan.ctas), dim3(32 * kJoinWarps), 0, st, 1, p, plan.rows);
 }
 template <int D>
 cudaError_t launch_d(const Int4Params &p, const AttnInt4Plan &plan, cudaStream_t st) {
