@@ -714,29 +714,6 @@ def kv_store_int4(k, v, slots, cache):
     qlin_qk_norm_rope_kv_store_int4("half", 0, 0, None, slots, None, k, v, None, None, 0.0, None, slots, *cache)
 
 
-class _Scratch:
-    """Workspace of one call: a block of torch's allocator for the current stream, as a tensor's memory is (also while
-    the stream is captured), without the tensor (27.4 -> 23.4 us a call of attn_int4)."""
-    __slots__ = ("n", "at")
-
-    def __init__(self, n: int):
-        self.n = n
-        self.at = torch._C._cuda_cudaCachingAllocator_raw_alloc(n, _stream(None))
-
-    def data_ptr(self):
-        return self.at
-
-    def numel(self):
-        return self.n
-
-    def element_size(self):
-        return 1
-
-    def __del__(self):  # later work of the stream may have the memory, as with a tensor
-        if hasattr(self, "at"):
-            torch._C._cuda_cudaCachingAllocator_raw_delete(self.at)
-
-
 def attn_int4(q, q_start, kv_len, block_table, cache, max_q: int, max_kv: int, scale=None, causal: bool = True,
               window: int = 0, out=None, ws=None):
     """Attention of q over a 4-bit cache (the four arrays of kv_int4_alloc()); scale defaults to D^-1/2."""
@@ -747,7 +724,7 @@ def attn_int4(q, q_start, kv_len, block_table, cache, max_q: int, max_kv: int, s
     if ws is None:
         n = qlin_attn_int4_workspace_bytes(kv_len.shape[0], q.shape[1] // D, H, D, max_q, max_kv, window)
         if 0 < n < 2 ** 63:  # invalid sizes are the call's to report
-            ws = _Scratch(n)
+            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
     qlin_attn_int4(q, q_start, kv_len, block_table, *cache, max_q, max_kv, D ** -0.5 if scale is None else scale,
                    causal, window, out, ws)
     return out
