@@ -33,7 +33,7 @@
 // a row does not see leaves that row's others in place), so float16 holds
 // them whatever the cache's scales; 2^ek joins the score's factor and ev the
 // exponent, so that neither costs the softmax an instruction per score.  O is
-// rescaled only where a row's maximum grew by more than 2^6 (of the 4-bit cache 2^7.75) since its reference;
+// rescaled only where a row's maximum grew by more than 2^6 (of the 4-bit cache 2^7.5) since its reference;
 // P stays below 2^14 (2^15.9).  Positions whose value scale is 0 do not raise that
 // reference (they would push P of the others out of float16): they count in the
 // sum of the row alone, which for that has a reference of its own.  Scores too large
@@ -58,13 +58,14 @@ constexpr int kMetaSlots = 4;
 // P is 2^kPBias p and may grow by 2^kGrowth before its reference is taken anew, for which the tensor core waits: below 2^14
 // (the mixed cache) or 2^15.9.  Its subnormals lie below 2^-22 p, so that what small weights add up to, beside a heavy
 // position without a value, is as exact as with few rows.  8192 x 16384, 28 heads over 4 of 128: growth 6 1165 us, 7 1153,
-// 7.75 1141; a bias of 4 with 10 took 1110, with weights below 2^-18 of the largest losing bits.
+// 7.5 1147, 7.75 1141 (with scores up to 2^20 only); a bias of 4 with 10 took 1110, and weights below 2^-18 of the largest
+// lost bits.
 constexpr float kPBias = 8.0f;
-constexpr float kGrowthOf(bool int4) { return int4 ? 7.75f : 6.0f; }
+constexpr float kGrowthOf(bool int4) { return int4 ? 7.5f : 6.0f; }
 constexpr float kLead = 32.0f;  // a score may pass the sum's reference by 2^this where O has another
-// Scores up to here have a reference good to 1/2, so P stays below 2^14.5; or (growth 7.75) their maximum, reference and
-// difference are each good to 2^-5, and P stays below 2^15.9.
-constexpr float kHugeOf(bool int4) { return int4 ? 0x1p20f : 0x1p24f; }
+// Scores up to here have a reference good to 1/2, so P stays below 2^14.5; or (the 4-bit cache) their maximum, its limit and
+// the reference with the bias are each good to 1/8, and P stays below 2^15.9.
+constexpr float kHugeOf(bool int4) { return int4 ? 0x1p22f : 0x1p24f; }
 constexpr int kValueUp = 6;     // a value's scale becomes 2^6..2^7 (times at most 448: below float16's 65504)
 constexpr int kValueSpan = 11;  // scales of a unit within 2^11 share an exponent: E4M3's 2^-9 stays normal
 constexpr int kKeySpan = 14;    // key scales within 2^14: a code of 1 stays normal
