@@ -23,8 +23,8 @@
 // tile, beside q, the shared memory.  So a CTA takes 128 rows, with warps 0-3 for their softmax, warp 4 for copies
 // and warp 5 for the products; position tiles have two places for S in turn, so that the products with P of tile
 // j - 1 and S of tile j + 1 run while the softmax has tile j, and halves of a key or value tile are copied as soon as
-// their last products are done.  28 heads over 4 of 256: 2048 new of 8192 positions 308 us, 1.37 PFLOP/s (by the
-// kernels for few rows 3.2 ms), 8192 of 16384 1.60 PFLOP/s.
+// their last products are done.  28 heads over 4 of 256: 2048 new of 8192 positions 307 us, 1.37 PFLOP/s (by the
+// kernels for few rows 3.2 ms), 8192 of 16384 1.51 to 1.57 PFLOP/s.
 //
 // Scaling.  q rows are scaled by powers of two to use float16's range.  The keys
 // of 32 (D 128) or 64 (D 64) positions, a unit, are scaled by code scale * 2^-ek

@@ -8,10 +8,10 @@
 // (the errors of the additions are kept, as in norm_kernels.cu), so their codes
 // are reproducible bit for bit.  Queries with a weight, which nothing quantizes, take the sum, the weights and the
 // turn as fused operations (within 2^-19 of a pair's magnitude before the rounding to BF16), for a quarter of the
-// instructions.  Positions may have up to four axes (time, height,
+// instructions; heads that these do not hold take the single operations.  Positions may have up to four axes (time, height,
 // width): a pair's angle then comes from the table's row of its own axis.
 //
-// Bound by HBM: heads in and out, codes out (29.6 us for 8192 tokens of 28 + 4 heads of 128 into the cache, 4.8 TB/s; 25.7
+// Bound by HBM: heads in and out, codes out (29.8 us for 8192 tokens of 28 + 4 heads of 128 into the cache, 4.8 TB/s; 25.8
 // us for the norms alone, 5.4 TB/s).  A head is D/16 lanes of 16 dimensions, whose rows come by
 // asynchronous copies some heads ahead.  Queries and keys run different code beside each other, and its size shows: one
 // kernel for both layouts took 32.3 and 27.6 us where two took 31.3 and 27.0, loops unrolled by two 36.5 and 32.0.
@@ -89,8 +89,8 @@ __device__ __forceinline__ uint64_t difference_of(const HeadParams &p, uint64_t 
 
 // A lane's 16 dimensions of a head: two pieces of 8, d0 and d0 + piece on.  HALF: the first and second elements of eight
 // pairs, or pieces past rot half of what is there apart; otherwise four pairs each, `per` pieces apart, so that lanes side by side have a row's
-// pieces side by side (16 dimensions one after the other, half of each sector at a time, took 36.5 us against 27.5 for 8192
-// tokens of 28 + 4 heads of 128, with the store 40.8 against 29.0).  Pairs pair[i] ... pair[i] + 3 turn where turns[i].
+// pieces side by side (16 dimensions one after the other, half of each sector at a time, took 36.5 us against 27.9 for 8192
+// tokens of 28 + 4 heads of 128, with the store 40.8 against 29.1).  Pairs pair[i] ... pair[i] + 3 turn where turns[i].
 struct Pieces {
   int d0, piece, pair[2];
   bool turns[2];

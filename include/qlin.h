@@ -552,7 +552,8 @@ const char *qlin_attn_mixed_kernel_name(int64_t B, int64_t Hq, int64_t H, int64_
  * Attention over the 4-bit KV cache that qlin_qk_norm_rope_kv_store_int4 writes: as
  * qlin_attn_mixed, with keys and values the codes times their scales, and num_blocks pages.
  * Softmax statistics and sums are fp32; P enters the matrix products as float16 (a weight is off by
- * 2^-11 of itself, or by 2^-33 of the row's largest where that is more), values times
+ * 2^-11 of itself, or by 2^-33 of the row's largest where that is more; by 2^-25 of it among scores beyond 2^22, which
+ * are themselves rounded by a quarter), values times
  * their scales do (rounded once), and with many rows so do the keys.
  * What is stored at positions that a row does not see does not reach it.  A row that
  * sees a position with a scale that the store does not write (above 9344, negative, infinite, NaN;
